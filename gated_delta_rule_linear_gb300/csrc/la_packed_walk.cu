@@ -1,0 +1,142 @@
+// Packed retention, token by token on the CUDA cores in float32: the float32
+// path of la_packed_fwd and la_packed_bwd.
+//
+// One CTA of 128 threads owns 32 value columns of one (sequence, head) and
+// walks its tokens, the state slice da x 32 in registers: thread (w, l) holds
+// the rows w*da/4 .. of column l. Tokens come 16 at a time through shared
+// memory; every warp's partial of out_t over its rows goes to shared memory and
+// is added up once per block of tokens. The walk is bound by its own serial
+// chain, about da/2 FMAs a token and warp, not by memory.
+#include <cuda_bf16.h>
+
+#include "la_layer_internal.h"
+
+namespace la {
+namespace {
+
+constexpr int kTok = 16, kCols = 32;
+
+template <typename T> __device__ __forceinline__ float rd(const void *p, size_t i) {
+  return static_cast<float>(static_cast<const T *>(p)[i]);
+}
+
+template <typename T, int DA>
+__global__ void __launch_bounds__(128) packed_walk_kernel(const PackedPass p) {
+  __shared__ __align__(16) float sx[kTok][DA], sy[kTok][DA];
+  __shared__ float sz[kTok][kCols], part[kTok][4][kCols];
+  constexpr int R = DA / 4;
+  const int s = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * kCols;
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31, c0 = w * R, col = v0 + l;
+  int a, b;
+  packed_range(p.cu, s, p.total, &a, &b);
+  const int slot = packed_slot(p.slots, s, p.n_slots);
+  const size_t sbase = ((size_t)max(slot, 0) * p.H + h) * p.sized;
+  float S[R];
+#pragma unroll
+  for (int c = 0; c < R; ++c) {
+    const size_t at = p.in_t ? (size_t)col * DA + c0 + c : (size_t)(c0 + c) * p.db + col;
+    S[c] = (p.S_in && slot >= 0) ? p.S_in[sbase + at] : 0.f;
+  }
+  const Decay decay(p.g ? __ldg(p.g + h) : 0.f, 1);
+  const size_t xh = (size_t)(h / p.rx) * DA, yh = (size_t)(h / p.ry) * DA, zh = (size_t)(h / p.rz) * p.db;
+
+  for (int done = 0; done < b - a; done += kTok) {
+    const int m = min(kTok, b - a - done);
+    auto token = [&](int i) { return (size_t)(p.reverse ? b - 1 - done - i : a + done + i); };
+    __syncthreads();
+    for (int i = threadIdx.x; i < m * DA; i += 128) {
+      const size_t t = token(i / DA);
+      sx[i / DA][i % DA] = rd<T>(p.x, t * p.ldx + xh + i % DA);
+      sy[i / DA][i % DA] = rd<T>(p.y, t * p.ldy + yh + i % DA);
+    }
+    for (int i = threadIdx.x; i < m * kCols; i += 128)
+      sz[i / kCols][i % kCols] = rd<T>(p.z, token(i / kCols) * p.ldz + zh + v0 + i % kCols);
+    __syncthreads();
+    for (int i = 0; i < m; ++i) {
+      const float z = sz[i][l];
+      float o = 0.f;
+#pragma unroll
+      for (int c = 0; c < R; ++c) {
+        const float y = sy[i][c0 + c], x = sx[i][c0 + c];
+        S[c] = fmaf(y, z, p.reverse ? S[c] : decay(S[c]));
+        o = fmaf(x, S[c], o);
+        if (p.reverse) S[c] = decay(S[c]);
+      }
+      part[i][w][l] = o;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < m * kCols; i += 128) {
+      const int t = i / kCols, c = i % kCols;
+      const float o = (part[t][0][c] + part[t][1][c]) + (part[t][2][c] + part[t][3][c]);
+      const size_t at = token(t) * p.ldo + (size_t)h * p.db + v0 + c;
+      if (p.out_f32)
+        static_cast<float *>(p.out)[at] = o;
+      else
+        static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(o);
+    }
+  }
+  if (p.S_out && slot >= 0)
+#pragma unroll
+    for (int c = 0; c < R; ++c) p.S_out[sbase + (size_t)(c0 + c) * p.db + col] = S[c];
+}
+
+// Gradients of shared heads: the float32 parts of the heads that use one.
+template <typename T>
+__global__ void __launch_bounds__(256) head_sum_kernel(const float *__restrict__ src, T *__restrict__ dst,
+                                                       long long quads, int share, int d) {
+  const int dq = d / 4;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < quads; i += gridDim.x * 256LL) {
+    const long long row = i / dq;  // (token, shared head)
+    const int c = static_cast<int>(i % dq);
+    const float4 *s = reinterpret_cast<const float4 *>(src + row * share * d) + c;
+    float4 t = __ldcs(s);
+    for (int j = 1; j < share; ++j) {
+      const float4 u = __ldcs(s + (size_t)j * dq);
+      t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+    }
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float4 *>(dst)[i] = t;
+    } else {
+      __nv_bfloat162 u[2] = {__floats2bfloat162_rn(t.x, t.y), __floats2bfloat162_rn(t.z, t.w)};
+      reinterpret_cast<uint2 *>(dst)[i] = *reinterpret_cast<uint2 *>(u);
+    }
+  }
+}
+
+}  // namespace
+
+int launch_packed_walk(const PackedPass &p, cudaStream_t stream) {
+  const dim3 grid(p.n_seq, p.H, p.db / kCols);
+  if (p.f32) {
+    if (p.da == 64) packed_walk_kernel<float, 64><<<grid, 128, 0, stream>>>(p);
+    else packed_walk_kernel<float, 128><<<grid, 128, 0, stream>>>(p);
+  } else {
+    if (p.da == 64) packed_walk_kernel<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(p);
+    else packed_walk_kernel<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(p);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("packed retention: launch failed: %s", cudaGetErrorString(e));
+    return LA_ERR_CUDA;
+  }
+  return LA_OK;
+}
+
+int launch_head_sum(const float *src, void *dst, int f32, int N, int Hk, int share, int d, cudaStream_t stream) {
+  const long long quads = (long long)N * Hk * (d / 4);
+  if (quads == 0) return LA_OK;
+  const long long want = (quads + 255) / 256;
+  const int grid = static_cast<int>(want < 16384 ? want : 16384);
+  if (f32)
+    head_sum_kernel<<<grid, 256, 0, stream>>>(src, static_cast<float *>(dst), quads, share, d);
+  else
+    head_sum_kernel<<<grid, 256, 0, stream>>>(src, static_cast<__nv_bfloat16 *>(dst), quads, share, d);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("la_packed_bwd: head sum launch failed: %s", cudaGetErrorString(e));
+    return LA_ERR_CUDA;
+  }
+  return LA_OK;
+}
+
+}  // namespace la
