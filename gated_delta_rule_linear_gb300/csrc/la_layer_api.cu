@@ -49,7 +49,10 @@ int check_packing(const char *fn, const int *cu, const int *slots, int n_seq, in
   return LA_OK;
 }
 
-int run_pass(const PackedPass &p, cudaStream_t stream) { return launch_packed_walk(p, stream); }
+// float32 and calls without a token go to the walk, bfloat16 to the tensor cores.
+int run_pass(const PackedPass &p, cudaStream_t stream) {
+  return p.f32 || p.total == 0 ? launch_packed_walk(p, stream) : launch_packed_tc(p, stream);
+}
 
 }  // namespace
 

@@ -80,6 +80,7 @@ struct Decay {
 };
 
 int launch_packed_walk(const PackedPass &p, cudaStream_t stream);
+int launch_packed_tc(const PackedPass &p, cudaStream_t stream);
 // dst[n][hk][d] = sum over the `share` heads of src float32 [n][hk * share][d]
 int launch_head_sum(const float *src, void *dst, int f32, int N, int Hk, int share, int d, cudaStream_t stream);
 

@@ -1,0 +1,667 @@
+// Packed retention on tcgen05 + TMEM + TMA, bf16 inputs, float32 state: the
+// passes of la_packed_fwd and la_packed_bwd (PackedPass).
+//
+// Chunks of 128 tokens, rows i, j of a chunk of n rows ("Talk Linear Attention"
+// sections 3.2 and 5.2), with the state S (da x 64 value columns) that enters
+// the chunk:
+//
+//   P   = (X Y^T) . gamma^(i-j), j <= i     out = gamma^(i+1) (X S) + P Z
+//   S  <- gamma^n S + dS,                   dS  = Y^T Z',  Z' = gamma^(n-1-j) Z
+//
+// and for reversed passes gamma^(j-i) over j >= i, gamma^(n-1-i) for the row and
+// gamma^(j+1) for Z, chunks from the last to the first. The decay of a head is
+// one number, so every power comes from a table of gamma^0 .. gamma^128.
+//
+// Work. A unit is one segment (up to seg tokens) of one sequence; one CTA takes
+// a unit, a head and 64 value columns. Sequences longer than the segment first
+// go through the same kernel with STATE set, which only forms each segment's
+// own contribution to the state, and a scan over the segments. Unit u of
+// sequence s are the numbers from floor(cu[s]/seg) + s on: enough for its
+// segments, increasing in s, and known without a table.
+//
+// The state stays in registers: every chunk's dS is formed in a TMEM tile of
+// its own and added by float32 FMAs, gamma^n - 1 carrying the decay. Adding in
+// TMEM instead would cut every product's sum at the accumulator's last bit, and
+// thousands of tokens of that show in a float32 state. For the same reason Z'
+// goes to the tensor cores as a bf16 high and low part (2^-16), side by side as
+// one operand of twice the width: one part alone would leave the state with
+// bf16's error. P and the state's copy for X S are rounded to bf16 once; their
+// errors are of the order of the output's own rounding.
+//
+// Out-of-sequence rows: a tile may reach into the next sequence or behind the
+// last token. The foreign rows of Y and Z are cleared in shared memory before
+// they are multiplied, so that whatever they hold (NaN included) stays out;
+// foreign rows of X reach only output rows that are not written.
+//
+// Roles, 768 threads. Every group works on its own part of a chunk and hands it
+// on through mbarriers, up to two chunks apart; a group of its own for each
+// step, because the steps are bound by their instructions' latency:
+//   warp 0        TMA loads of X, Y, Z, two stages
+//   warp 1        MMAs: scores, dS          warp 3  MMAs: X S, P Z
+//   warp 2        TMEM
+//   warps 4-7     state: S <- gamma^n S + dS, its bf16 copy
+//   warps 8-11    output: gamma^(i+1) X S + P Z, to memory by TMA
+//   warps 12-15   Z' high and low
+//   warps 16-23   P, in TMEM over its scores
+// Every wait is bounded; on expiry the CTA raises the status word, all roles
+// leave, copies and MMAs in flight are drained and TMEM is released.
+#include <algorithm>
+#include <climits>
+
+#include "la_layer_internal.h"
+#include "la_tc_common.cuh"
+
+namespace la {
+namespace {
+
+using namespace sm100;
+using namespace tc;
+
+constexpr int kThreads = 768, kN = 128;  // tokens of a chunk
+constexpr uint32_t kSpin = 1u << 22;     // polls before a wait gives up (tens of milliseconds at least)
+// Registers a thread of each group, at most what the block was launched with: 80 * 6.
+constexpr int kRegsIssue = 56, kRegsState = 104;
+
+struct Segments {
+  int tokens;       // of a segment; 0: every sequence is one unit
+  int units;        // sequences, or the numbers units may have
+  const float *in;  // [unit][H][dk][dv] entering states, or null: S_in by slot
+  float *out;       // STATE: the segments' own contributions
+};
+
+// First unit number of sequence s.
+__device__ __forceinline__ int first_unit(const PackedPass &p, int seg, int s) {
+  return min(max(__ldg(p.cu + s), 0), p.total) / seg + s;
+}
+
+// The tokens [t0, t1) of unit u, and its sequence's [a, b). False: no such unit.
+__device__ __forceinline__ bool find_unit(const PackedPass &p, const Segments &sg, int u, int *s, int *a, int *b,
+                                          int *t0, int *t1) {
+  if (sg.tokens == 0) {
+    *s = u;
+    packed_range(p.cu, u, p.total, a, b);
+    *t0 = *a;
+    *t1 = *b;
+    return true;
+  }
+  int count = 0;
+  for (int base = 0; base < p.n_seq; base += blockDim.x) {
+    const int i = base + threadIdx.x;
+    count += __syncthreads_count(i < p.n_seq && first_unit(p, sg.tokens, i) <= u);
+  }
+  if (count == 0) return false;
+  *s = count - 1;
+  packed_range(p.cu, *s, p.total, a, b);
+  const long long from = (long long)(u - first_unit(p, sg.tokens, *s)) * sg.tokens;
+  if (from < 0 || (from > 0 && from >= *b - *a)) return false;
+  *t0 = *a + static_cast<int>(from);
+  *t1 = min(*b, *t0 + sg.tokens);
+  return true;
+}
+
+// Shared memory, in 16 KB tiles (128 rows of 64 bf16, 128-byte swizzle).
+constexpr uint32_t kTile = 16384;
+constexpr uint32_t kSmX = 0, kSmY = kSmX + 4 * kTile, kSmZ = kSmY + 4 * kTile, kSmW = kSmZ + 2 * kTile,
+                   kSmS = kSmW + 2 * kTile, kSmO = kSmS + kTile, kSmMisc = kSmO + kTile,
+                   kSmBytes = kSmMisc + 2048 + 1024;
+// TMEM columns: two buffers of scores, over which go P (columns 0..63) and P Z (64..127),
+// two of X S, and dS of Z' high and low.
+constexpr uint32_t kColSc = 0, kColPZ = 64, kColXS = 256, kColD = 384;
+
+// 32 lanes x 32 bits, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int R> __device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R> __device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+template <int DA, bool STATE>
+__global__ void __launch_bounds__(kThreads, 1)
+packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ CUtensorMap tm_x,
+                 const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_z,
+                 const __grid_constant__ CUtensorMap tm_o) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wq = warp & 3;
+  const int vtiles = p.db / 64;
+  const int vt = blockIdx.x % vtiles, h = blockIdx.x / vtiles % p.H, u = blockIdx.x / vtiles / p.H;
+  int s, a, b, t0, t1;
+  if (!find_unit(p, sg, u, &s, &a, &b, &t0, &t1)) return;
+  const bool leaves = p.reverse ? t0 == a : t1 == b;  // the state behind this unit is the sequence's last
+  if (STATE && leaves) return;
+  const bool by_slot = !STATE && (sg.in == nullptr || (leaves && p.S_out));
+  const int slot = by_slot ? packed_slot(p.slots, s, p.n_slots) : -1;
+  const float *src = nullptr;
+  if (!STATE)
+    src = sg.in ? sg.in + ((size_t)u * p.H + h) * p.sized
+                : (p.S_in && slot >= 0 ? p.S_in + ((size_t)slot * p.H + h) * p.sized : nullptr);
+  float *dst = nullptr;
+  if (STATE) dst = sg.out + ((size_t)u * p.H + h) * p.sized;
+  else if (p.S_out && leaves && slot >= 0) dst = p.S_out + ((size_t)slot * p.H + h) * p.sized;
+  const bool src_t = p.in_t && !sg.in;  // the segments' states lie as this pass wants them
+  const int v0 = vt * 64, db = p.db;
+  const float g = p.g ? __ldg(p.g + h) : 0.f;
+  const int chunks = (t1 - t0 + kN - 1) / kN;
+  if (chunks == 0) {  // an empty sequence: its state passes through
+    if (dst && dst != src)
+      for (int i = tid; i < DA * 64; i += kThreads) {
+        const int c = i / 64, v = v0 + i % 64;
+        dst[(size_t)c * db + v] = src ? src[src_t ? (size_t)v * DA + c : (size_t)c * db + v] : 0.f;
+      }
+    return;
+  }
+
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kSmMisc);
+  uint64_t *x_full = bars, *x_free = bars + 2, *y_full = bars + 4, *y_free = bars + 6, *z_full = bars + 8,
+           *z_free = bars + 10, *sc_full = bars + 12, *p_ready = bars + 16,
+           *w_ready = bars + 18, *d_full = bars + 20, *d_free = bars + 21, *s_ready = bars + 22, *xs_full = bars + 23,
+           *o_full = bars + 24, *o_free = bars + 26, *drain = bars + 28;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 30);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  float *pw = reinterpret_cast<float *>(sm + kSmMisc + 256);  // gamma^0 .. gamma^128
+  float *pij = pw + 132;  // [127 + i - j]: the factor of a score, zero where j is not seen from i
+
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&x_full[i], 1);
+      mbar_init(&x_free[i], 2);  // scores, X S
+      mbar_init(&y_full[i], 1);
+      mbar_init(&y_free[i], 1);
+      mbar_init(&z_full[i], 1);
+      mbar_init(&z_free[i], STATE ? 1 : 2);  // dS (behind Z'), P Z
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+      mbar_init(&p_ready[i], 8);
+      mbar_init(&w_ready[i], 4);
+      mbar_init(&drain[i], 1);
+    }
+    mbar_init(d_full, 1);
+    mbar_init(d_free, 4);
+    mbar_init(s_ready, 4);
+    mbar_init(xs_full, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (DA == 64) {  // channels 64..127 of Y: zero rows of dS
+    for (int i = tid; i < 2 * 1024; i += kThreads)
+      reinterpret_cast<uint4 *>(sm + kSmY + (2 * (i >> 10) + 1) * kTile)[i & 1023] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+  }
+  for (int i = tid; i <= kN; i += kThreads) pw[i] = decay_power(g, i);
+  for (int i = tid; i < 2 * kN - 1; i += kThreads) {
+    const int e = p.reverse ? 127 - i : i - 127;
+    pij[i] = e >= 0 ? decay_power(g, e) : 0.f;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  const uint32_t tl = tbase + (static_cast<uint32_t>(wq * 32) << 16);
+  auto chunk_at = [&](int j) { return p.reverse ? chunks - 1 - j : j; };
+  // The loop is as short as it can be (the status word is raised at the end): the code that all
+  // roles run for a chunk has to stay in the SM's instruction cache together. With the waits,
+  // products and conversions unrolled in place it did not, and a chunk took three times as long.
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kSpin; ++i) {
+      if (mbar_try_wait(bar, parity & 1)) return true;
+      if (*abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
+  };
+  // A group of four warps waits: one lane polls, the others sleep on the group's barrier.
+  // With a polling lane in each of 24 warps the polls took more issue slots than the work.
+  const int group = warp >> 2;
+  auto wait_group = [&](uint64_t *bar, uint32_t parity) {
+    bool ok = true;
+    if (wq == (group & 3) && lane == 0) ok = wait(bar, parity);
+    return group_all(ok, group);
+  };
+
+  if (warp < 4) {
+    regs_down<kRegsIssue>();
+    if (warp == 0 && lane == 0) {
+      // ----------------------------------------------------------- TMA loads
+      prefetch_tmap(&tm_y);
+      prefetch_tmap(&tm_z);
+      if (!STATE) prefetch_tmap(&tm_x);
+      const int xh = h / p.rx, yh = h / p.ry, zh = h / p.rz;
+      int j = 0;
+      for (; j < chunks; ++j) {
+        const int t = t0 + chunk_at(j) * kN, st = j & 1;
+        const uint32_t again = (j >> 1) ^ 1;
+        if (!wait(&y_free[st], again)) break;
+        mbar_arrive_expect_tx(&y_full[st], DA / 64 * kTile);
+#pragma unroll
+        for (int k = 0; k < DA / 64; ++k)
+          tma_load_3d(sm + kSmY + (2 * st + k) * kTile, &tm_y, &y_full[st], 64 * k, yh, t);
+        if (!STATE) {
+          if (!wait(&x_free[st], again)) break;
+          mbar_arrive_expect_tx(&x_full[st], DA / 64 * kTile);
+#pragma unroll
+          for (int k = 0; k < DA / 64; ++k)
+            tma_load_3d(sm + kSmX + (2 * st + k) * kTile, &tm_x, &x_full[st], 64 * k, xh, t);
+        }
+        if (!wait(&z_free[st], again)) break;
+        mbar_arrive_expect_tx(&z_full[st], kTile);
+        tma_load_3d(sm + kSmZ + st * kTile, &tm_z, &z_full[st], v0, zh, t);
+        // the chunk after the next into L2; its loads wait for this chunk's products. X and Y
+        // are read by both CTAs of a head of 128 value columns: one of them asks for each
+        if (j + 2 < chunks) {
+          const int t2 = t0 + chunk_at(j + 2) * kN;
+          tma_prefetch_3d(&tm_z, v0, zh, t2);
+#pragma unroll
+          for (int k = 0; k < DA / 64; ++k) {
+            if (vtiles == 1 || vt == 0) tma_prefetch_3d(&tm_y, 64 * k, yh, t2);
+            if (!STATE && (vtiles == 1 || vt == 1)) tma_prefetch_3d(&tm_x, 64 * k, xh, t2);
+          }
+        }
+      }
+      // given up: copies still in flight must land before the CTA's memory is released
+      // (a barrier that was never armed in its last phase just runs out its wait)
+      if (j < chunks)
+        for (int n = j; n >= 0 && n >= j - 1; --n) {
+          (void)mbar_wait_bounded(&y_full[n & 1], (n >> 1) & 1, 1u << 16);
+          if (!STATE) (void)mbar_wait_bounded(&x_full[n & 1], (n >> 1) & 1, 1u << 16);
+          (void)mbar_wait_bounded(&z_full[n & 1], (n >> 1) & 1, 1u << 16);
+        }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------- MMAs: scores and dS
+      constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false), id_d = idesc_bf16_f32(128, 128, true, true);
+      const uint64_t dx = desc_sw128(smem_u32(sm + kSmX), 16, 1024), dy = desc_sw128(smem_u32(sm + kSmY), 16, 1024);
+      const uint64_t dyt = desc_sw128(smem_u32(sm + kSmY), kTile, 1024);
+      const uint64_t dw = desc_sw128(smem_u32(sm + kSmW), kTile, 1024);
+      for (int j = 0; j < chunks; ++j) {
+        const int st = j & 1;
+        const uint32_t stage = 2 * st * kTile;
+        const bool tail = t1 - t0 < (chunk_at(j) + 1) * kN;  // foreign rows of Y are cleared behind Z'
+        if (!wait(&y_full[st], j >> 1) || (tail && !wait(&w_ready[st], j >> 1))) break;
+        if (!STATE) {
+          if (!wait(&x_full[st], j >> 1) || !wait(&o_free[st], (j >> 1) ^ 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < DA / 16; ++k) {
+            const uint32_t off = stage + (k >> 2) * kTile + (k & 3) * 32;
+            mma_bf16(tbase + kColSc + 128 * st, desc_add(dx, off), desc_add(dy, off), id_sc, k > 0);
+          }
+          mma_commit(&sc_full[st]);
+          mma_commit(&x_free[st]);
+        }
+        if (!wait(&w_ready[st], j >> 1) || !wait(d_free, j ^ 1)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kN / 16; ++k)
+          mma_bf16(tbase + kColD, desc_add(dyt, stage + k * 2048), desc_add(dw, k * 2048), id_d, k > 0);
+        mma_commit(d_full);
+        mma_commit(&y_free[st]);
+        mma_commit(&z_free[st]);
+      }
+      mma_commit(&drain[0]);
+      (void)mbar_wait_bounded(&drain[0], 0, kSpin);
+    } else if (!STATE && warp == 3 && lane == 0) {
+      // ------------------------------------------------------ MMAs: X S, P Z
+      constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);
+      const uint64_t dx = desc_sw128(smem_u32(sm + kSmX), 16, 1024);
+      const uint64_t ds = desc_sw128(smem_u32(sm + kSmS), kTile, 1024);
+      const uint64_t dz = desc_sw128(smem_u32(sm + kSmZ), kTile, 1024);
+      for (int j = 0; j < chunks; ++j) {
+        const int st = j & 1;
+        if (!wait(&x_full[st], j >> 1) || !wait(s_ready, j) ||
+            !wait(&o_free[st], (j >> 1) ^ 1))
+          break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < DA / 16; ++k)
+          mma_bf16(tbase + kColXS + 64 * st, desc_add(dx, 2 * st * kTile + (k >> 2) * kTile + (k & 3) * 32),
+                   desc_add(ds, k * 2048), id_o, k > 0);
+        mma_commit(xs_full);
+        mma_commit(&x_free[st]);
+        // (behind Z' the foreign rows of Z are clear)
+        if (!wait(&z_full[st], j >> 1) || !wait(&w_ready[st], j >> 1) || !wait(&p_ready[st], j >> 1)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kN / 16; ++k)  // blocks of 32 tokens of P in the order 0, 3, 1, 2
+          mma_bf16_ts(tbase + kColSc + 128 * st + kColPZ,
+                    tbase + kColSc + 128 * st + (0x1320u >> (k & 6) * 2 & 0xf) * 16 + (k & 1) * 8,
+                    desc_add(dz, st * kTile + k * 2048), id_o, k > 0);
+        mma_commit(&o_full[st]);
+        mma_commit(&z_free[st]);
+      }
+      mma_commit(&drain[1]);
+      (void)mbar_wait_bounded(&drain[1], 0, kSpin);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------- the state
+    regs_up<kRegsState>();
+    const int c = wq * 32 + lane;  // key channel: row of S
+    float S[64];
+    if (src && c < DA) {
+      if (src_t) {
+#pragma unroll
+        for (int n = 0; n < 64; ++n) S[n] = src[(size_t)(v0 + n) * DA + c];
+      } else {
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const float4 t = reinterpret_cast<const float4 *>(src + (size_t)c * db + v0)[n];
+          S[4 * n] = t.x; S[4 * n + 1] = t.y; S[4 * n + 2] = t.z; S[4 * n + 3] = t.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < 64; ++n) S[n] = 0.f;
+    }
+    const Decay whole(g, kN), part(g, (t1 - t0) - (chunks - 1) * kN);
+    for (int j = 0; j < chunks; ++j) {
+      if (!STATE) {  // row c of the bf16 copy, once X S of the chunk before is done with it
+        if (j > 0 && !wait_group(xs_full, j - 1)) break;
+        if (c < DA) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4 *>(sm + kSmS + sw128_off(c, 8 * q)) = pack8(S + 8 * q);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_ready);
+      }
+      if (!wait_group(d_full, j)) break;
+      tc_fence_after();
+      const Decay decay = chunk_at(j) == chunks - 1 ? part : whole;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float d[8], lo[8];
+        tmem_ld8(tl + kColD + 8 * q, d);
+        tmem_ld8(tl + kColD + 64 + 8 * q, lo);
+        tmem_wait_ld();
+#pragma unroll
+        for (int n = 0; n < 8; ++n) S[8 * q + n] = decay(S[8 * q + n]) + (d[n] + lo[n]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(d_free);
+    }
+    if (dst && c < DA) {
+#pragma unroll
+      for (int n = 0; n < 16; ++n)
+        reinterpret_cast<float4 *>(dst + (size_t)c * db + v0)[n] =
+            make_float4(S[4 * n], S[4 * n + 1], S[4 * n + 2], S[4 * n + 3]);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ the output
+    const int i = wq * 32 + lane;
+    uint8_t *ot = sm + kSmO;
+    for (int j = 0; !STATE && j < chunks; ++j) {
+      const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN), t = t0 + cc * kN + i;
+      const float r = pw[p.reverse ? max(rows - 1 - i, 0) : i + 1];
+      const bool staged = !p.out_f32 && wq * 32 + 32 <= rows;  // all of the warp's rows: through TMA
+      const size_t at = (size_t)t * p.ldo + (size_t)h * db + v0;
+      if (j > 0 && lane == 0) bulk_wait_read<0>();  // the staging rows have been read
+      if (!wait_group(&o_full[st], j >> 1)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float xs[16], pz[16];
+        tmem_ld16(tl + kColXS + 64 * st + 16 * q, xs);
+        tmem_ld16(tl + kColSc + 128 * st + kColPZ + 16 * q, pz);
+        tmem_wait_ld();
+#pragma unroll
+        for (int n = 0; n < 16; ++n) xs[n] = fmaf(r, xs[n], pz[n]);
+        if (staged) {
+          *reinterpret_cast<uint4 *>(ot + sw128_off(i, 16 * q)) = pack8(xs);
+          *reinterpret_cast<uint4 *>(ot + sw128_off(i, 16 * q + 8)) = pack8(xs + 8);
+        } else if (i < rows) {
+          if (p.out_f32) {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) + 4 * q;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) o[n] = make_float4(xs[4 * n], xs[4 * n + 1], xs[4 * n + 2], xs[4 * n + 3]);
+          } else {
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at) + 2 * q;
+            o[0] = pack8(xs);
+            o[1] = pack8(xs + 8);
+          }
+        }
+      }
+      tc_fence_before();
+      if (staged) fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&o_free[st]);
+        if (staged) {
+          tma_store_3d(&tm_o, ot + wq * 32 * 128, v0, h, t);
+          bulk_commit();
+        }
+      }
+    }
+    if (!STATE && lane == 0) bulk_wait<0>();
+  } else if (warp < 16) {
+    // -------------------------------------------------------- Z' high and low
+    const int i = wq * 32 + lane;
+    for (int j = 0; j < chunks; ++j) {
+      const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN);
+      const bool mine = i < rows;
+      if (!wait_group(&z_full[st], j >> 1) || (j > 0 && !wait_group(d_full, j - 1))) break;
+      uint8_t *zt = sm + kSmZ + st * kTile, *wt = sm + kSmW;
+      if (rows < kN) {  // foreign rows of Y and Z
+        if (!wait_group(&y_full[st], j >> 1)) break;
+        if (!mine)
+#pragma unroll 1
+          for (int q = 0; q < 8 * (1 + DA / 64); ++q)
+            *reinterpret_cast<uint4 *>((q < 8 ? zt : sm + kSmY + 2 * st * kTile + ((q >> 3) - 1) * kTile) +
+                                       sw128_off(i, 8 * (q & 7))) = make_uint4(0, 0, 0, 0);
+      }
+      const float w = mine ? pw[p.reverse ? i + 1 : rows - 1 - i] : 0.f;
+#pragma unroll 1
+      for (int q = 0; q < 8; q += 2) {
+        uint4 row[2];  // loads before the first store: they could not pass it
+#pragma unroll
+        for (int e = 0; e < 2; ++e) row[e] = *reinterpret_cast<const uint4 *>(zt + sw128_off(i, 8 * (q + e)));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float f[8], f2[8];
+          unpack8(row[e], f);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) f[n] *= w;
+          const uint4 hi = pack8(f);
+          unpack8(hi, f2);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) f[n] -= f2[n];
+          *reinterpret_cast<uint4 *>(wt + sw128_off(i, 8 * (q + e))) = hi;
+          *reinterpret_cast<uint4 *>(wt + kTile + sw128_off(i, 8 * (q + e))) = pack8(f);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_ready[st]);
+    }
+  } else {
+    // ------------------------------------------------------------------- P
+    const int half = (warp - 16) >> 2, i = wq * 32 + lane;
+    for (int j = 0; !STATE && j < chunks; ++j) {
+      const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN);
+      if (!wait_group(&sc_full[st], j >> 1)) break;
+      tc_fence_after();
+      // blocks of 32 columns against the warp's 32 rows
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        const int kb = half ? 1 + k : 3 * k, j0 = 32 * kb;  // half 0: the first and the last block
+        const uint32_t sc = tl + kColSc + 128 * st + j0, pt = tl + kColSc + 128 * st + 32 * half + 16 * k;
+        float f[32];
+        if (p.reverse ? kb < wq : kb > wq) {  // nothing of the block is seen
+#pragma unroll
+          for (int n = 0; n < 16; ++n) f[n] = 0.f;
+        } else {
+          tmem_ld32(sc, f);
+          tmem_wait_ld();
+          const float *e = pij + 127 + i - j0;
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            f[n] = __uint_as_float(pack_bf16(f[2 * n] * e[-2 * n], f[2 * n + 1] * e[-2 * n - 1]));
+        }
+        tmem_st16(pt, f);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_ready[st]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tbase, 512);
+  if (tid == 0 && *abort_flag) atomicOr(p.status, kStatusTimeout);
+}
+
+// The entering state of every segment from the segments' own contributions, in
+// place: a running sum per element, the loads of a few segments ahead in flight.
+__global__ void __launch_bounds__(256) segment_scan_kernel(const PackedPass p, int seg, int units, float *ws) {
+  const int s = blockIdx.x, h = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4;
+  int a, b;
+  packed_range(p.cu, s, p.total, &a, &b);
+  const int slot = packed_slot(p.slots, s, p.n_slots);
+  if (e >= p.sized) return;
+  const int n = max(1, (b - a + seg - 1) / seg), u0 = first_unit(p, seg, s);
+  if (u0 + n > units) return;  // only where cu_seqlens is not what it should be
+  const float g = p.g ? __ldg(p.g + h) : 0.f;
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.S_in && slot >= 0) {
+    const float *in = p.S_in + ((size_t)slot * p.H + h) * p.sized;
+    const int c = e / p.db, v = e % p.db;
+    if (p.in_t) S = make_float4(in[(size_t)v * p.da + c], in[(size_t)(v + 1) * p.da + c], in[(size_t)(v + 2) * p.da + c],
+                                in[(size_t)(v + 3) * p.da + c]);
+    else S = *reinterpret_cast<const float4 *>(in + e);
+  }
+  auto at = [&](int k) {
+    return reinterpret_cast<float4 *>(ws + ((size_t)(u0 + (p.reverse ? n - 1 - k : k)) * p.H + h) * p.sized + e);
+  };
+  const Decay whole(g, seg), part(g, b - a - (n - 1) * seg);
+  constexpr int kAhead = 4;
+  for (int k0 = 0; k0 < n; k0 += kAhead) {
+    float4 U[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (k0 + i < n - 1) U[i] = *at(k0 + i);  // nothing reads behind the last segment
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = k0 + i;
+      if (k >= n) break;
+      *at(k) = S;
+      if (k == n - 1) break;
+      const bool tail = (p.reverse ? n - 1 - k : k) == n - 1;
+      S.x = (tail ? part(S.x) : whole(S.x)) + U[i].x;
+      S.y = (tail ? part(S.y) : whole(S.y)) + U[i].y;
+      S.z = (tail ? part(S.z) : whole(S.z)) + U[i].z;
+      S.w = (tail ? part(S.w) : whole(S.w)) + U[i].w;
+    }
+  }
+}
+
+// [tokens][heads][d] with a token stride, boxes of 64 channels x 1 head x rows.
+bool make_token_map(CUtensorMap *m, const void *base, int d, int heads, int tokens, long long ld, int rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, es[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+  CUtensorMap x, y, z, o;
+};
+
+template <int DA, bool STATE>
+cudaError_t launch_as(const PackedPass &p, const Segments &sg, const Maps &m, cudaStream_t stream) {
+  auto kernel = packed_tc_kernel<DA, STATE>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmBytes);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(sg.units) * p.H * (p.db / 64);
+  kernel<<<grid, kThreads, kSmBytes, stream>>>(p, sg, m.x, m.y, m.z, m.o);
+  return cudaGetLastError();
+}
+
+template <bool STATE>
+cudaError_t launch(const PackedPass &p, const Segments &sg, const Maps &m, cudaStream_t stream) {
+  return p.da == 64 ? launch_as<64, STATE>(p, sg, m, stream) : launch_as<128, STATE>(p, sg, m, stream);
+}
+
+int fail(const char *what, cudaError_t e) {
+  set_error("packed retention: %s: %s", what, cudaGetErrorString(e));
+  return LA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_packed_tc(const PackedPass &p, cudaStream_t stream) {
+  if (!encode_fn()) {
+    set_error("packed retention: cuTensorMapEncodeTiled is unavailable");
+    return LA_ERR_CUDA;
+  }
+  Maps m;
+  if (!make_token_map(&m.x, p.x, p.da, p.H / p.rx, p.total, p.ldx, kN) ||
+      !make_token_map(&m.y, p.y, p.da, p.H / p.ry, p.total, p.ldy, kN) ||
+      !make_token_map(&m.z, p.z, p.db, p.H / p.rz, p.total, p.ldz, kN)) {
+    set_error("packed retention: tensor map encoding failed");
+    return LA_ERR_CUDA;
+  }
+  m.o = m.x;
+  if (!p.out_f32 && !make_token_map(&m.o, p.out, p.db, p.H, p.total, p.ldo, 32)) {
+    set_error("packed retention: tensor map encoding failed");
+    return LA_ERR_CUDA;
+  }
+  // Sequences are split into segments where whole ones would leave the GPU to
+  // a few long walks: the second reading of Y and Z, and the states' way through
+  // memory, cost about 0.4 of a pass.
+  const long long sms = std::max(1, sm_count());
+  const int longest = p.max_len > 0 ? std::min(p.max_len, p.total) : p.total;
+  const long long share = ((long long)p.total * p.H * (p.db / 64) + sms - 1) / sms;  // tokens of a CTA
+  Segments sg = {0, p.n_seq, nullptr, nullptr};
+  if (longest > 2 * kN && longest > share + share / 2) {
+    long long seg = (share + kN - 1) / kN * kN;
+    seg = std::max<long long>(seg, 2 * kN);
+    if (seg < longest) sg = {static_cast<int>(seg), static_cast<int>(p.total / seg) + p.n_seq, nullptr, nullptr};
+  }
+  const long long ctas = (long long)sg.units * p.H * (p.db / 64);
+  if (ctas > INT_MAX) {
+    set_error("packed retention: n_seq * H too large");
+    return LA_ERR_INVALID_ARG;
+  }
+  float *ws = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (sg.tokens) {
+    cudaMemPool_t pool = library_pool();
+    if (!pool) return fail("could not create the workspace pool", cudaGetLastError());
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), (size_t)sg.units * p.H * p.sized * 4, pool, stream);
+    if (e != cudaSuccess) return fail("workspace allocation failed", e);
+    sg.out = ws;
+    e = launch<true>(p, sg, m, stream);
+    if (e == cudaSuccess) {
+      segment_scan_kernel<<<dim3(p.n_seq, p.H, (p.sized / 4 + 255) / 256), 256, 0, stream>>>(p, sg.tokens, sg.units, ws);
+      e = cudaGetLastError();
+    }
+    sg.in = ws;
+  }
+  if (e == cudaSuccess) e = launch<false>(p, sg, m, stream);
+  if (ws) {
+    const cudaError_t f = cudaFreeAsync(ws, stream);
+    if (e == cudaSuccess) e = f;
+  }
+  return e == cudaSuccess ? LA_OK : fail("launch failed", e);
+}
+
+}  // namespace la
