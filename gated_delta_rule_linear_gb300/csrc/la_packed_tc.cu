@@ -33,16 +33,15 @@
 // they are multiplied, so that whatever they hold (NaN included) stays out;
 // foreign rows of X reach only output rows that are not written.
 //
-// Roles, 768 threads. Every group works on its own part of a chunk and hands it
+// Roles, 896 threads. Every group works on its own part of a chunk and hands it
 // on through mbarriers, up to two chunks apart; a group of its own for each
 // step, because the steps are bound by their instructions' latency:
 //   warp 0        TMA loads of X, Y, Z, two stages
-//   warp 1        MMAs: scores, dS          warp 3  MMAs: X S, P Z
-//   warp 2        TMEM
+//   warps 1-3     MMAs: dS and X S; scores (and TMEM); P Z
 //   warps 4-7     state: S <- gamma^n S + dS, its bf16 copy
 //   warps 8-11    output: gamma^(i+1) X S + P Z, to memory by TMA
-//   warps 12-15   Z' high and low
-//   warps 16-23   P, in TMEM over its scores
+//   warps 12-19   Z' high and low
+//   warps 20-27   P, in TMEM over its scores
 // Every wait is bounded; on expiry the CTA raises the status word, all roles
 // leave, copies and MMAs in flight are drained and TMEM is released.
 #include <algorithm>
@@ -57,10 +56,12 @@ namespace {
 using namespace sm100;
 using namespace tc;
 
-constexpr int kThreads = 768, kN = 128;  // tokens of a chunk
+constexpr int kThreads = 896, kN = 128;  // tokens of a chunk
 constexpr uint32_t kSpin = 1u << 22;     // polls before a wait gives up (tens of milliseconds at least)
-// Registers a thread of each group, at most what the block was launched with: 80 * 6.
-constexpr int kRegsIssue = 56, kRegsState = 104;
+// Registers a thread of each group of four warps, together at most what the block was
+// launched with, 7 * 72: issue, state, output, twice Z', twice P.
+constexpr int kRegsIssue = 56, kRegsState = 104, kRegsOut = 88, kRegsP = 72, kRegsZ = 56;
+static_assert(kRegsIssue + kRegsState + kRegsOut + 2 * kRegsP + 2 * kRegsZ <= 7 * 72, "register split");
 
 struct Segments {
   int tokens;       // of a segment; 0: every sequence is one unit
@@ -119,6 +120,36 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v) {
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Descriptors as desc_sw128's, from the operand's address: the strides are constants, so
+// the upper word is one too and only the lower word has to be moved to the issue unit.
+__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"((saddr >> 4) | (lbo >> 4) << 16), "n"(1024 >> 4 | 1 << 14 | 2 << 29));
+  return d;
+}
+
+// Two float32 operations in one instruction: half the issue slots, half the code.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2(float *r, const float *a, uint64_t b, const float *c) {  // r = a b + c
+  uint64_t t;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(pair(a[0], a[1])), "l"(b), "l"(pair(c[0], c[1])));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(t));
+}
+__device__ __forceinline__ void add2(float *r, const float *a, const float *b) {
+  uint64_t t;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(pair(a[0], a[1])), "l"(pair(b[0], b[1])));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(t));
+}
+__device__ __forceinline__ void mul2(float *r, const float *a, uint64_t b) {
+  uint64_t t;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(pair(a[0], a[1])), "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(t));
+}
+
 template <int R> __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
@@ -126,7 +157,7 @@ template <int R> __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-template <int DA, bool STATE>
+template <int DA, bool STATE, bool OF32>
 __global__ void __launch_bounds__(kThreads, 1)
 packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ CUtensorMap tm_x,
                  const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_z,
@@ -163,11 +194,10 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
   }
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kSmMisc);
-  uint64_t *x_full = bars, *x_free = bars + 2, *y_full = bars + 4, *y_free = bars + 6, *z_full = bars + 8,
-           *z_free = bars + 10, *sc_full = bars + 12, *p_ready = bars + 16,
-           *w_ready = bars + 18, *d_full = bars + 20, *d_free = bars + 21, *s_ready = bars + 22, *xs_full = bars + 23,
-           *o_full = bars + 24, *o_free = bars + 26, *drain = bars + 28;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 30);
+  uint64_t *xy_full = bars, *xy_free = bars + 2, *z_full = bars + 4, *z_free = bars + 6, *sc_full = bars + 8,
+           *p_ready = bars + 10, *w_ready = bars + 12, *o_full = bars + 14, *o_free = bars + 16, *d_full = bars + 18,
+           *d_free = bars + 19, *s_ready = bars + 20, *xs_full = bars + 21, *drain = bars + 22;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 26);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   float *pw = reinterpret_cast<float *>(sm + kSmMisc + 256);  // gamma^0 .. gamma^128
   float *pij = pw + 132;  // [127 + i - j]: the factor of a score, zero where j is not seen from i
@@ -178,23 +208,21 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&x_full[i], 1);
-      mbar_init(&x_free[i], 2);  // scores, X S
-      mbar_init(&y_full[i], 1);
-      mbar_init(&y_free[i], 1);
+      mbar_init(&xy_full[i], 1);
+      mbar_init(&xy_free[i], STATE ? 1 : 2);  // dS and X S, scores
       mbar_init(&z_full[i], 1);
-      mbar_init(&z_free[i], STATE ? 1 : 2);  // dS (behind Z'), P Z
+      mbar_init(&z_free[i], STATE ? 1 : 2);   // dS (behind it Z'), P Z
       mbar_init(&sc_full[i], 1);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&o_free[i], 4);
       mbar_init(&p_ready[i], 8);
-      mbar_init(&w_ready[i], 4);
-      mbar_init(&drain[i], 1);
+      mbar_init(&w_ready[i], 8);
+      mbar_init(&o_full[i], 2);  // X S, P Z
+      mbar_init(&o_free[i], 4);
     }
     mbar_init(d_full, 1);
     mbar_init(d_free, 4);
     mbar_init(s_ready, 4);
     mbar_init(xs_full, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -231,7 +259,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
   const int group = warp >> 2;
   auto wait_group = [&](uint64_t *bar, uint32_t parity) {
     bool ok = true;
-    if (wq == (group & 3) && lane == 0) ok = wait(bar, parity);
+    if (wq == (group & 2) && lane == 0) ok = wait(bar, parity);  // not on the schedulers of the issuing warps 1 and 3
     return group_all(ok, group);
   };
 
@@ -247,21 +275,17 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       for (; j < chunks; ++j) {
         const int t = t0 + chunk_at(j) * kN, st = j & 1;
         const uint32_t again = (j >> 1) ^ 1;
-        if (!wait(&y_free[st], again)) break;
-        mbar_arrive_expect_tx(&y_full[st], DA / 64 * kTile);
-#pragma unroll
-        for (int k = 0; k < DA / 64; ++k)
-          tma_load_3d(sm + kSmY + (2 * st + k) * kTile, &tm_y, &y_full[st], 64 * k, yh, t);
-        if (!STATE) {
-          if (!wait(&x_free[st], again)) break;
-          mbar_arrive_expect_tx(&x_full[st], DA / 64 * kTile);
-#pragma unroll
-          for (int k = 0; k < DA / 64; ++k)
-            tma_load_3d(sm + kSmX + (2 * st + k) * kTile, &tm_x, &x_full[st], 64 * k, xh, t);
-        }
+        // Z first: it is the first to be free (behind P Z) and the first to be used (Z')
         if (!wait(&z_free[st], again)) break;
         mbar_arrive_expect_tx(&z_full[st], kTile);
         tma_load_3d(sm + kSmZ + st * kTile, &tm_z, &z_full[st], v0, zh, t);
+        if (!wait(&xy_free[st], again)) break;
+        mbar_arrive_expect_tx(&xy_full[st], DA / 64 * kTile * (STATE ? 1 : 2));
+#pragma unroll
+        for (int k = 0; k < DA / 64; ++k) {
+          tma_load_3d(sm + kSmY + (2 * st + k) * kTile, &tm_y, &xy_full[st], 64 * k, yh, t);
+          if (!STATE) tma_load_3d(sm + kSmX + (2 * st + k) * kTile, &tm_x, &xy_full[st], 64 * k, xh, t);
+        }
         // the chunk after the next into L2; its loads wait for this chunk's products. X and Y
         // are read by both CTAs of a head of 128 value columns: one of them asks for each
         if (j + 2 < chunks) {
@@ -278,69 +302,74 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       // (a barrier that was never armed in its last phase just runs out its wait)
       if (j < chunks)
         for (int n = j; n >= 0 && n >= j - 1; --n) {
-          (void)mbar_wait_bounded(&y_full[n & 1], (n >> 1) & 1, 1u << 16);
-          if (!STATE) (void)mbar_wait_bounded(&x_full[n & 1], (n >> 1) & 1, 1u << 16);
+          (void)mbar_wait_bounded(&xy_full[n & 1], (n >> 1) & 1, 1u << 16);
           (void)mbar_wait_bounded(&z_full[n & 1], (n >> 1) & 1, 1u << 16);
         }
-    } else if (warp == 1 && lane == 0) {
-      // ------------------------------------------------- MMAs: scores and dS
-      constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false), id_d = idesc_bf16_f32(128, 128, true, true);
-      const uint64_t dx = desc_sw128(smem_u32(sm + kSmX), 16, 1024), dy = desc_sw128(smem_u32(sm + kSmY), 16, 1024);
-      const uint64_t dyt = desc_sw128(smem_u32(sm + kSmY), kTile, 1024);
-      const uint64_t dw = desc_sw128(smem_u32(sm + kSmW), kTile, 1024);
+    } else if (!STATE && warp == 2 && lane == 0) {
+      // -------------------------------------------------------- MMAs: scores
+      constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
+      const uint32_t dx = smem_u32(sm + kSmX), dy = smem_u32(sm + kSmY);
       for (int j = 0; j < chunks; ++j) {
         const int st = j & 1;
         const uint32_t stage = 2 * st * kTile;
         const bool tail = t1 - t0 < (chunk_at(j) + 1) * kN;  // foreign rows of Y are cleared behind Z'
-        if (!wait(&y_full[st], j >> 1) || (tail && !wait(&w_ready[st], j >> 1))) break;
-        if (!STATE) {
-          if (!wait(&x_full[st], j >> 1) || !wait(&o_free[st], (j >> 1) ^ 1)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < DA / 16; ++k) {
-            const uint32_t off = stage + (k >> 2) * kTile + (k & 3) * 32;
-            mma_bf16(tbase + kColSc + 128 * st, desc_add(dx, off), desc_add(dy, off), id_sc, k > 0);
-          }
-          mma_commit(&sc_full[st]);
-          mma_commit(&x_free[st]);
-        }
-        if (!wait(&w_ready[st], j >> 1) || !wait(d_free, j ^ 1)) break;
+        if (!wait(&xy_full[st], j >> 1) || (tail && !wait(&w_ready[st], j >> 1)) || !wait(&o_free[st], (j >> 1) ^ 1))
+          break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 4
+        for (int k = 0; k < DA / 16; ++k) {
+          const uint32_t off = stage + (k >> 2) * kTile + (k & 3) * 32;
+          mma_bf16(tbase + kColSc + 128 * st, desc(dx + off, 16), desc(dy + off, 16), id_sc, k > 0);
+        }
+        mma_commit(&sc_full[st]);
+        mma_commit(&xy_free[st]);
+      }
+      mma_commit(&drain[2]);
+      (void)mbar_wait_bounded(&drain[2], 0, kSpin);
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------- MMAs: dS, X S
+      constexpr uint32_t id_d = idesc_bf16_f32(128, 128, true, true), id_o = idesc_bf16_f32(128, 64, false, true);
+      const uint32_t dx = smem_u32(sm + kSmX);
+      const uint32_t ds = smem_u32(sm + kSmS);
+      const uint32_t dyt = smem_u32(sm + kSmY);
+      const uint32_t dw = smem_u32(sm + kSmW);
+      for (int j = 0; j < chunks; ++j) {
+        const int st = j & 1;
+        if (!wait(&xy_full[st], j >> 1) || !wait(d_free, j ^ 1) || !wait(&w_ready[st], j >> 1)) break;
+        tc_fence_after();
+#pragma unroll 4
         for (int k = 0; k < kN / 16; ++k)
-          mma_bf16(tbase + kColD, desc_add(dyt, stage + k * 2048), desc_add(dw, k * 2048), id_d, k > 0);
+          mma_bf16(tbase + kColD, desc(dyt + 2 * st * kTile + k * 2048, kTile), desc(dw + k * 2048, kTile), id_d, k > 0);
         mma_commit(d_full);
-        mma_commit(&y_free[st]);
         mma_commit(&z_free[st]);
+        if (!STATE) {  // in the time that the next Z' takes
+          if (!wait(&o_free[st], (j >> 1) ^ 1) || !wait(s_ready, j)) break;
+          tc_fence_after();
+#pragma unroll 4
+          for (int k = 0; k < DA / 16; ++k)
+            mma_bf16(tbase + kColXS + 64 * st, desc(dx + 2 * st * kTile + (k >> 2) * kTile + (k & 3) * 32, 16),
+                     desc(ds + k * 2048, kTile), id_o, k > 0);
+          mma_commit(xs_full);
+          mma_commit(&o_full[st]);
+        }
+        mma_commit(&xy_free[st]);
       }
       mma_commit(&drain[0]);
       (void)mbar_wait_bounded(&drain[0], 0, kSpin);
     } else if (!STATE && warp == 3 && lane == 0) {
-      // ------------------------------------------------------ MMAs: X S, P Z
+      // ----------------------------------------------------------- MMAs: P Z
       constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);
-      const uint64_t dx = desc_sw128(smem_u32(sm + kSmX), 16, 1024);
-      const uint64_t ds = desc_sw128(smem_u32(sm + kSmS), kTile, 1024);
-      const uint64_t dz = desc_sw128(smem_u32(sm + kSmZ), kTile, 1024);
+      const uint32_t dz = smem_u32(sm + kSmZ);
       for (int j = 0; j < chunks; ++j) {
         const int st = j & 1;
-        if (!wait(&x_full[st], j >> 1) || !wait(s_ready, j) ||
-            !wait(&o_free[st], (j >> 1) ^ 1))
-          break;
+        // (behind Z', Z is there and its foreign rows are clear)
+        if (!wait(&w_ready[st], j >> 1) || !wait(&p_ready[st], j >> 1)) break;
         tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < DA / 16; ++k)
-          mma_bf16(tbase + kColXS + 64 * st, desc_add(dx, 2 * st * kTile + (k >> 2) * kTile + (k & 3) * 32),
-                   desc_add(ds, k * 2048), id_o, k > 0);
-        mma_commit(xs_full);
-        mma_commit(&x_free[st]);
-        // (behind Z' the foreign rows of Z are clear)
-        if (!wait(&z_full[st], j >> 1) || !wait(&w_ready[st], j >> 1) || !wait(&p_ready[st], j >> 1)) break;
-        tc_fence_after();
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < kN / 16; ++k)  // blocks of 32 tokens of P in the order 0, 3, 1, 2
           mma_bf16_ts(tbase + kColSc + 128 * st + kColPZ,
-                    tbase + kColSc + 128 * st + (0x1320u >> (k & 6) * 2 & 0xf) * 16 + (k & 1) * 8,
-                    desc_add(dz, st * kTile + k * 2048), id_o, k > 0);
+                      tbase + kColSc + 128 * st + (0x1320u >> (k & 6) * 2 & 0xf) * 16 + (k & 1) * 8,
+                      desc(dz + st * kTile + k * 2048, kTile), id_o, k > 0);
         mma_commit(&o_full[st]);
         mma_commit(&z_free[st]);
       }
@@ -382,6 +411,8 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       if (!wait_group(d_full, j)) break;
       tc_fence_after();
       const Decay decay = chunk_at(j) == chunks - 1 ? part : whole;
+      // S m (+ S): see Decay
+      const uint64_t small = pair(decay.m, decay.m), one = decay.near ? pair(1.f, 1.f) : 0;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         float d[8], lo[8];
@@ -389,7 +420,11 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
         tmem_ld8(tl + kColD + 64 + 8 * q, lo);
         tmem_wait_ld();
 #pragma unroll
-        for (int n = 0; n < 8; ++n) S[8 * q + n] = decay(S[8 * q + n]) + (d[n] + lo[n]);
+        for (int n = 0; n < 8; n += 2) {
+          add2(d + n, d + n, lo + n);
+          fma2(d + n, S + 8 * q + n, small, d + n);
+          fma2(S + 8 * q + n, S + 8 * q + n, one, d + n);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -403,86 +438,96 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ the output
+    regs_up<kRegsOut>();
     const int i = wq * 32 + lane;
     uint8_t *ot = sm + kSmO;
     for (int j = 0; !STATE && j < chunks; ++j) {
       const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN), t = t0 + cc * kN + i;
       const float r = pw[p.reverse ? max(rows - 1 - i, 0) : i + 1];
-      const bool staged = !p.out_f32 && wq * 32 + 32 <= rows;  // all of the warp's rows: through TMA
+      const uint64_t rr = pair(r, r);
+      const bool staged = !OF32 && wq * 32 + 32 <= rows;  // all of the warp's rows: through TMA
       const size_t at = (size_t)t * p.ldo + (size_t)h * db + v0;
       if (j > 0 && lane == 0) bulk_wait_read<0>();  // the staging rows have been read
       if (!wait_group(&o_full[st], j >> 1)) break;
       tc_fence_after();
-#pragma unroll 1
+      uint4 o[8];
+#pragma unroll
       for (int q = 0; q < 4; ++q) {
         float xs[16], pz[16];
         tmem_ld16(tl + kColXS + 64 * st + 16 * q, xs);
         tmem_ld16(tl + kColSc + 128 * st + kColPZ + 16 * q, pz);
         tmem_wait_ld();
 #pragma unroll
-        for (int n = 0; n < 16; ++n) xs[n] = fmaf(r, xs[n], pz[n]);
-        if (staged) {
-          *reinterpret_cast<uint4 *>(ot + sw128_off(i, 16 * q)) = pack8(xs);
-          *reinterpret_cast<uint4 *>(ot + sw128_off(i, 16 * q + 8)) = pack8(xs + 8);
-        } else if (i < rows) {
-          if (p.out_f32) {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) + 4 * q;
+        for (int n = 0; n < 16; n += 2) fma2(xs + n, xs + n, rr, pz + n);
+        if constexpr (OF32) {
+          if (i < rows)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) o[n] = make_float4(xs[4 * n], xs[4 * n + 1], xs[4 * n + 2], xs[4 * n + 3]);
-          } else {
-            uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at) + 2 * q;
-            o[0] = pack8(xs);
-            o[1] = pack8(xs + 8);
-          }
+            for (int n = 0; n < 16; n += 4)
+              reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[4 * q + n / 4] =
+                  make_float4(xs[n], xs[n + 1], xs[n + 2], xs[n + 3]);
+        } else {
+          o[2 * q] = pack8(xs);
+          o[2 * q + 1] = pack8(xs + 8);
         }
       }
       tc_fence_before();
-      if (staged) fence_proxy_async();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&o_free[st]);
-        if (staged) {
+      if (lane == 0) mbar_arrive(&o_free[st]);
+      if constexpr (!OF32) {
+        // the staging tile, or straight to memory
+        uint8_t *to = staged ? ot : reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + at);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (i < rows) *reinterpret_cast<uint4 *>(to + (staged ? sw128_off(i, 8 * q) : 16u * q)) = o[q];
+        if (staged) fence_proxy_async();
+        __syncwarp();
+        if (staged && lane == 0) {
           tma_store_3d(&tm_o, ot + wq * 32 * 128, v0, h, t);
           bulk_commit();
         }
       }
     }
     if (!STATE && lane == 0) bulk_wait<0>();
-  } else if (warp < 16) {
+  } else if (warp < 20) {
     // -------------------------------------------------------- Z' high and low
-    const int i = wq * 32 + lane;
+    regs_down<kRegsZ>();
+    const int half = (warp - 12) >> 2, i = wq * 32 + lane;  // columns 32*half .. of row i
     for (int j = 0; j < chunks; ++j) {
       const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN);
       const bool mine = i < rows;
-      if (!wait_group(&z_full[st], j >> 1) || (j > 0 && !wait_group(d_full, j - 1))) break;
+      if (!wait_group(&z_full[st], j >> 1)) break;
       uint8_t *zt = sm + kSmZ + st * kTile, *wt = sm + kSmW;
       if (rows < kN) {  // foreign rows of Y and Z
-        if (!wait_group(&y_full[st], j >> 1)) break;
+        if (!wait_group(&xy_full[st], j >> 1)) break;
         if (!mine)
 #pragma unroll 1
-          for (int q = 0; q < 8 * (1 + DA / 64); ++q)
+          for (int q = 4 * half; q < 8 * (1 + DA / 64); q += (q & 3) == 3 ? 5 : 1)
             *reinterpret_cast<uint4 *>((q < 8 ? zt : sm + kSmY + 2 * st * kTile + ((q >> 3) - 1) * kTile) +
                                        sw128_off(i, 8 * (q & 7))) = make_uint4(0, 0, 0, 0);
       }
       const float w = mine ? pw[p.reverse ? i + 1 : rows - 1 - i] : 0.f;
-#pragma unroll 1
-      for (int q = 0; q < 8; q += 2) {
-        uint4 row[2];  // loads before the first store: they could not pass it
+      const uint64_t ww = pair(w, w), minus = pair(-1.f, -1.f);
+      uint4 hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) row[e] = *reinterpret_cast<const uint4 *>(zt + sw128_off(i, 8 * (q + e)));
+      for (int e = 0; e < 4; ++e) hi[e] = *reinterpret_cast<const uint4 *>(zt + sw128_off(i, 8 * (4 * half + e)));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float f[8], f2[8];
-          unpack8(row[e], f);
+      for (int e = 0; e < 4; ++e) {
+        float f[8], f2[8];
+        unpack8(hi[e], f);
 #pragma unroll
-          for (int n = 0; n < 8; ++n) f[n] *= w;
-          const uint4 hi = pack8(f);
-          unpack8(hi, f2);
+        for (int n = 0; n < 8; n += 2) mul2(f + n, f + n, ww);
+        hi[e] = pack8(f);
+        unpack8(hi[e], f2);
 #pragma unroll
-          for (int n = 0; n < 8; ++n) f[n] -= f2[n];
-          *reinterpret_cast<uint4 *>(wt + sw128_off(i, 8 * (q + e))) = hi;
-          *reinterpret_cast<uint4 *>(wt + kTile + sw128_off(i, 8 * (q + e))) = pack8(f);
-        }
+        for (int n = 0; n < 8; n += 2) fma2(f + n, f2 + n, minus, f + n);
+        lo[e] = pack8(f);
+      }
+      // the buffer itself is free once the dS before has been formed
+      if (j > 0 && !wait_group(d_full, j - 1)) break;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<uint4 *>(wt + sw128_off(i, 8 * (4 * half + e))) = hi[e];
+        *reinterpret_cast<uint4 *>(wt + kTile + sw128_off(i, 8 * (4 * half + e))) = lo[e];
       }
       fence_proxy_async();
       __syncwarp();
@@ -490,7 +535,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
     }
   } else {
     // ------------------------------------------------------------------- P
-    const int half = (warp - 16) >> 2, i = wq * 32 + lane;
+    const int half = (warp - 20) >> 2, i = wq * 32 + lane;
     for (int j = 0; !STATE && j < chunks; ++j) {
       const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN);
       if (!wait_group(&sc_full[st], j >> 1)) break;
@@ -509,8 +554,10 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
           tmem_wait_ld();
           const float *e = pij + 127 + i - j0;
 #pragma unroll
-          for (int n = 0; n < 16; ++n)
-            f[n] = __uint_as_float(pack_bf16(f[2 * n] * e[-2 * n], f[2 * n + 1] * e[-2 * n - 1]));
+          for (int n = 0; n < 16; ++n) {
+            mul2(f + 2 * n, f + 2 * n, pair(e[-2 * n], e[-2 * n - 1]));
+            f[n] = __uint_as_float(pack_bf16(f[2 * n], f[2 * n + 1]));
+          }
         }
         tmem_st16(pt, f);
       }
@@ -585,9 +632,9 @@ struct Maps {
   CUtensorMap x, y, z, o;
 };
 
-template <int DA, bool STATE>
+template <int DA, bool STATE, bool OF32>
 cudaError_t launch_as(const PackedPass &p, const Segments &sg, const Maps &m, cudaStream_t stream) {
-  auto kernel = packed_tc_kernel<DA, STATE>;
+  auto kernel = packed_tc_kernel<DA, STATE, OF32>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmBytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(sg.units) * p.H * (p.db / 64);
@@ -597,7 +644,10 @@ cudaError_t launch_as(const PackedPass &p, const Segments &sg, const Maps &m, cu
 
 template <bool STATE>
 cudaError_t launch(const PackedPass &p, const Segments &sg, const Maps &m, cudaStream_t stream) {
-  return p.da == 64 ? launch_as<64, STATE>(p, sg, m, stream) : launch_as<128, STATE>(p, sg, m, stream);
+  if constexpr (!STATE)
+    if (p.out_f32)
+      return p.da == 64 ? launch_as<64, false, true>(p, sg, m, stream) : launch_as<128, false, true>(p, sg, m, stream);
+  return p.da == 64 ? launch_as<64, STATE, false>(p, sg, m, stream) : launch_as<128, STATE, false>(p, sg, m, stream);
 }
 
 int fail(const char *what, cudaError_t e) {
