@@ -7,6 +7,22 @@
 
 namespace la {
 
+// n / d and n % d of 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(m, n) + n) >> s (the sum
+// stays below 2^32 for n below 2^31).
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ void split(uint32_t n, uint32_t &q, uint32_t &r) const {
+    q = (__umulhi(m, n) + n) >> s;
+    r = n - q * d;
+  }
+};
+
 // One pass of packed retention. All four products of the forward and backward
 // are the same sum with other tensors in its three places:
 //

@@ -47,6 +47,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "la_f32x2.cuh"
 #include "la_layer_internal.h"
 #include "la_tc_common.cuh"
 
@@ -55,6 +56,10 @@ namespace {
 
 using namespace sm100;
 using namespace tc;
+using f32x2::add2;
+using f32x2::fma2;
+using f32x2::mul2;
+using f32x2::pair;
 
 constexpr int kThreads = 896, kN = 128;  // tokens of a chunk
 constexpr uint32_t kSpin = 1u << 22;     // polls before a wait gives up (tens of milliseconds at least)
@@ -126,28 +131,6 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"((saddr >> 4) | (lbo >> 4) << 16), "n"(1024 >> 4 | 1 << 14 | 2 << 29));
   return d;
-}
-
-// Two float32 operations in one instruction: half the issue slots, half the code.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void fma2(float *r, const float *a, uint64_t b, const float *c) {  // r = a b + c
-  uint64_t t;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(pair(a[0], a[1])), "l"(b), "l"(pair(c[0], c[1])));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(t));
-}
-__device__ __forceinline__ void add2(float *r, const float *a, const float *b) {
-  uint64_t t;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(pair(a[0], a[1])), "l"(pair(b[0], b[1])));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(t));
-}
-__device__ __forceinline__ void mul2(float *r, const float *a, uint64_t b) {
-  uint64_t t;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(pair(a[0], a[1])), "l"(b));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r[0]), "=f"(r[1]) : "l"(t));
 }
 
 template <int R> __device__ __forceinline__ void regs_up() {

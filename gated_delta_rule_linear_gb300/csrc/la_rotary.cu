@@ -21,10 +21,16 @@ namespace {
 constexpr int kThreads = 256;
 
 // Offset of row (n, h) of a tensor with `heads` heads: token-major (T = 0) or head-major.
-__device__ __forceinline__ size_t row_at(int n, int h, int heads, int d, int T, long long ld) {
+__device__ __forceinline__ size_t row_at(int n, int h, int heads, int d, int T, const FastDiv &by_T, long long ld) {
   if (T == 0) return (size_t)n * ld + (size_t)h * d;
-  return (((size_t)(n / T) * heads + h) * T + n % T) * d;
+  uint32_t b, t;
+  by_T.split(n, b, t);
+  return (((size_t)b * heads + h) * T + t) * d;
 }
+
+struct RotaryDiv {
+  FastDiv items, heads, T_in, T_out, P;
+};
 
 template <typename T, int V> struct Vec {
   static __device__ __forceinline__ void load(const T *p, float *f) {
@@ -64,12 +70,13 @@ template <typename T, int V> struct Vec {
 // halves, V channels of the first half with their V partners. Channels behind
 // the pairs are copied, V at a time.
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p, int tokens) {
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p, const RotaryDiv by, int tokens) {
   extern __shared__ float2 turn[];  // [tokens][P] cos, sin
   const int P = p.s0 + p.s1 + p.s2, n0 = blockIdx.x * tokens, m = min(tokens, p.N - n0);
   for (int i = threadIdx.x; i < m * P; i += kThreads) {
-    const int n = i / P, c = i % P;
-    const int axis = c < p.s0 ? 0 : c < p.s0 + p.s1 ? 1 : 2;
+    uint32_t n, c;
+    by.P.split(i, n, c);
+    const int axis = (int)c < p.s0 ? 0 : (int)c < p.s0 + p.s1 ? 1 : 2;
     const double f = __ldg(p.freq + c) * 0.15915494309189535;  // 1 / (2 pi)
     const unsigned long long F = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0);
     const long long pos = __ldg(p.pos + (size_t)(n0 + n) * p.n_axes + axis);
@@ -83,13 +90,17 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p, 
   const int pairs = IL ? 2 * P / W : P / W;           // rotating items of a row
   const int rest = (p.d - 2 * P) / V, items = pairs + rest;
   const int heads = p.H + (p.k ? p.Hk : 0);
+#pragma unroll 4
   for (int i = threadIdx.x; i < m * heads * items; i += kThreads) {
-    const int n = i / (heads * items), hh = i / items % heads, it = i % items;
+    uint32_t q, n, head, item;
+    by.items.split(i, q, item);
+    by.heads.split(q, n, head);
+    const int hh = head, it = item;
     const bool is_k = hh >= p.H;
     const int h = is_k ? hh - p.H : hh, nh = is_k ? p.Hk : p.H;
     const T *src = static_cast<const T *>(is_k ? p.k : p.q) +
-                   row_at(n0 + n, h, nh, p.d, p.T_in, is_k ? p.ldk : p.ldq);
-    T *dst = static_cast<T *>(is_k ? p.k_out : p.q_out) + row_at(n0 + n, h, nh, p.d, p.T_out, (long long)nh * p.d);
+                   row_at(n0 + n, h, nh, p.d, p.T_in, by.T_in, is_k ? p.ldk : p.ldq);
+    T *dst = static_cast<T *>(is_k ? p.k_out : p.q_out) + row_at(n0 + n, h, nh, p.d, p.T_out, by.T_out, (long long)nh * p.d);
     const float scale = is_k ? p.scale_k : p.scale_q;
     const float2 *cs = turn + n * P;
     float a[W], b[W];
@@ -145,13 +156,20 @@ cudaError_t launch(const RotaryParams &p, cudaStream_t stream) {
   const int P = p.s0 + p.s1 + p.s2;
   const bool wide = p.d % V == 0 && (p.interleaved ? 2 * P : P) % V == 0 && aligned16(p.q) && aligned16(p.q_out) &&
                     aligned16(p.k) && aligned16(p.k_out) && (p.T_in > 0 || (p.ldq % V == 0 && p.ldk % V == 0));
-  const int tokens = 1;
+  // tokens of a CTA: enough rows that its loads overlap, not so many that the grid leaves SMs idle
+  const int W = wide ? V : p.interleaved ? 2 : 1;
+  const int items = (p.interleaved ? 2 * P / W : P / W) + (p.d - 2 * P) / (wide ? V : 1), heads = p.H + (p.k ? p.Hk : 0);
+  const long long sms = sm_count() > 0 ? sm_count() : 1;
+  int tokens = 1;
+  while (tokens < 8 && (long long)tokens * items * heads < 8 * kThreads && p.N / (2 * tokens) >= 8 * sms) tokens *= 2;
+  const RotaryDiv by = {FastDiv(items), FastDiv(heads), FastDiv(p.T_in > 0 ? p.T_in : 1),
+                        FastDiv(p.T_out > 0 ? p.T_out : 1), FastDiv(P)};
   const int grid = (p.N + tokens - 1) / tokens;
   const size_t smem = (size_t)tokens * P * sizeof(float2);
-  if (wide && p.interleaved) rotary_kernel<T, V, true><<<grid, kThreads, smem, stream>>>(p, tokens);
-  else if (wide) rotary_kernel<T, V, false><<<grid, kThreads, smem, stream>>>(p, tokens);
-  else if (p.interleaved) rotary_kernel<T, 1, true><<<grid, kThreads, smem, stream>>>(p, tokens);
-  else rotary_kernel<T, 1, false><<<grid, kThreads, smem, stream>>>(p, tokens);
+  if (wide && p.interleaved) rotary_kernel<T, V, true><<<grid, kThreads, smem, stream>>>(p, by, tokens);
+  else if (wide) rotary_kernel<T, V, false><<<grid, kThreads, smem, stream>>>(p, by, tokens);
+  else if (p.interleaved) rotary_kernel<T, 1, true><<<grid, kThreads, smem, stream>>>(p, by, tokens);
+  else rotary_kernel<T, 1, false><<<grid, kThreads, smem, stream>>>(p, by, tokens);
   return cudaGetLastError();
 }
 
