@@ -83,19 +83,42 @@ def la_epilogue_bwd(x, w, gate, act, res, scale, w_next, d_out, d_next, dx, dgat
 
 # ---- torch-tensor wrappers -----------------------------------------------------
 
-class _On:
-    """The tensors' device and the stream of a call: current inside, left as it was behind it."""
+def _refuse(t, name, dtype, shape, idx):
+    if not t.is_cuda or t.get_device() != idx:
+        raise ValueError(f"{name} must be on CUDA device {idx}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
-    def __init__(self, device, stream):
+
+def _check(t, name, dtype, shape, idx):
+    """A dense tensor of this type and shape on device idx (None passes). One pass over the attributes: calls
+    of a few tokens are bound by their host side."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, idx)
+
+
+def _index(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return t.get_device()
+
+
+class _On:
+    """The tensors' device and the call's stream: current inside, left as they were behind it."""
+
+    def __init__(self, idx, stream):
         import torch
-        self.cuda, self.device, self.stream, self.back = torch.cuda, device, stream, []
+        self.cuda, self.idx, self.stream, self.back = torch.cuda, idx, stream, []
 
     def __enter__(self):
-        if self.device.index != self.cuda.current_device():
-            self.back.append(self.cuda.device(self.device))
+        if self.idx != self.cuda.current_device():
+            self.back.append(self.cuda.device(self.idx))
         if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError(f"stream on {self.stream.device}, tensors on {self.device}")
+            if self.stream.device_index != self.idx:
+                raise ValueError(f"stream on device {self.stream.device_index}, tensors on {self.idx}")
             self.back.append(self.cuda.stream(self.stream))
         for c in self.back:
             c.__enter__()
@@ -106,21 +129,24 @@ class _On:
             c.__exit__(*e)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device != device):
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+class _Here:
+    """The common case: the current device and its current stream."""
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *e):
+        pass
 
 
-def _dense(dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (t.dtype != dtype or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous {dtype}, got {t.dtype}")
-
-
-def _shape(t, name, *shape):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+def _on(idx, stream):
+    import torch
+    if stream is None and idx == torch._C._cuda_getDevice():
+        return _Here(torch._C._cuda_getCurrentRawStream(idx))
+    return _On(idx, stream)
 
 
 def _rows(t, name):
@@ -131,27 +157,31 @@ def _rows(t, name):
     sn, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    return sn if n > 1 else max(sn, h * d) if n else h * d
+    return sn if n > 1 and sn > h * d else h * d if n <= 1 or sn == h * d else sn
 
 
 def _flag(dtype):
     import torch
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return CONSTANTS["LA_F32"]
-    if dtype != torch.bfloat16:
+    if dtype is not torch.bfloat16:
         raise TypeError(f"tensors must be bfloat16 or float32, got {dtype}")
     return 0
 
 
 def _qkv(q, k, v):
-    """(N, H, Hk, dk, dv, token strides) of a packed call's inputs."""
-    ld = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    (N, Hk, dk), (_, H, dv) = q.shape, v.shape
-    _shape(k, "k", N, Hk, dk)
-    _shape(v, "v", N, H, dv)
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    """(N, H, Hk, dk, dv, token strides, device) of a packed call's inputs."""
+    lq, lk, lv = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    idx, dt = _index(q, "q"), q.dtype
+    N, Hk, dk = q.shape
+    n, H, dv = v.shape
+    if k.shape != q.shape or n != N:
+        raise ValueError(f"k must have q's shape and v as many tokens: {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    if k.dtype is not dt or v.dtype is not dt:
         raise TypeError("q, k and v must have one dtype")
-    return N, H, Hk, dk, dv, ld
+    if k.get_device() != idx or v.get_device() != idx:
+        raise ValueError("q, k and v must be on one device")
+    return N, H, Hk, dk, dv, lq, lk, lv, idx
 
 
 def _run(rc):
@@ -169,35 +199,31 @@ def packed_fwd(q, k, v, cu_seqlens, mode, g=None, S0=None, slots=None, S_final=N
     "linear". q, k [total,Hk,dk], v [total,H,dv] (bf16 or fp32; token stride
     free); cu_seqlens int32 [n+1]; g [H] fp32; S0, S_final [n,H,dk,dv] fp32, or
     a pool [rows,H,dk,dv] with slots int32 [n] (S_final may be S0: updated in
-    place; with slots and no S_final, one is needed to get states back).
+    place; with slots and no S_final, final states are not kept).
     Returns (o, S_final or None)."""
     import torch
-    N, H, Hk, dk, dv, ld = _qkv(q, k, v)
-    dev, f32, i32 = q.device, torch.float32, torch.int32
-    _same_device(dev, q=q, k=k, v=v, cu_seqlens=cu_seqlens, g=g, S0=S0, slots=slots, S_final=S_final, o=o)
-    _dense(i32, cu_seqlens=cu_seqlens, slots=slots)
-    _dense(f32, g=g, S0=S0, S_final=S_final)
-    _dense(q.dtype, o=o)
-    _shape(g, "g", H)
-    _shape(o, "o", N, H, dv)
+    N, H, Hk, dk, dv, lq, lk, lv, idx = _qkv(q, k, v)
+    mid, f32, i32 = _mode(mode, q.dtype), torch.float32, torch.int32
     n = cu_seqlens.numel() - 1
-    _shape(slots, "slots", n)
+    _check(cu_seqlens, "cu_seqlens", i32, (n + 1,), idx)
+    _check(slots, "slots", i32, (n,), idx)
+    _check(g, "g", f32, (H,), idx)
     rows = n
-    for name, t in (("S0", S0), ("S_final", S_final)):
-        if t is not None:
-            _shape(t, name, t.shape[0] if slots is not None else n, H, dk, dv)
-            rows = t.shape[0]
-    if S0 is not None and S_final is not None and S0.shape != S_final.shape:
-        raise ValueError("S0 and S_final must have one shape")
-    with _On(dev, stream) as handle:
+    if slots is not None:
+        pool = S0 if S0 is not None else S_final
+        rows = 0 if pool is None else pool.shape[0]
+    _check(S0, "S0", f32, (rows, H, dk, dv), idx)
+    if not with_state:
+        S_final = None
+    _check(S_final, "S_final", f32, (rows, H, dk, dv), idx)
+    _check(o, "o", q.dtype, (N, H, dv), idx)
+    with _on(idx, stream) as handle:
         if o is None:
-            o = torch.empty((N, H, dv), dtype=q.dtype, device=dev)
-        if not with_state:
-            S_final = None
-        elif S_final is None and slots is None:
-            S_final = torch.empty((n, H, dk, dv), dtype=f32, device=dev)
-        _run(la_packed_fwd(q, k, v, g, o, S0, S_final, cu_seqlens, slots, n, N, max_len, rows, H, Hk, dk, dv, *ld,
-                           _mode(mode, q.dtype), handle))
+            o = q.new_empty((N, H, dv))
+        if with_state and S_final is None and slots is None:
+            S_final = q.new_empty((n, H, dk, dv), dtype=f32)
+        _run(la_packed_fwd(q, k, v, g, o, S0, S_final, cu_seqlens, slots, n, N, max_len, rows, H, Hk, dk, dv, lq, lk,
+                           lv, mid, handle))
     return o, S_final
 
 
@@ -205,23 +231,19 @@ def packed_bwd(q, k, v, dO, cu_seqlens, mode, g=None, S0=None, dS_final=None, wi
     """Backward pass of packed_fwd (la_packed_bwd): dq, dk, dv (dtype of q) and
     dS0 (fp32, or None). dO [total,H,dv]; S0, dS_final [n,H,dk,dv] fp32 or None."""
     import torch
-    N, H, Hk, dk, dv, ld = _qkv(q, k, v)
-    dev, f32 = q.device, torch.float32
-    _same_device(dev, q=q, k=k, v=v, dO=dO, cu_seqlens=cu_seqlens, g=g, S0=S0, dS_final=dS_final)
-    _dense(torch.int32, cu_seqlens=cu_seqlens)
-    _dense(f32, g=g, S0=S0, dS_final=dS_final)
-    _dense(q.dtype, dO=dO)
+    N, H, Hk, dk, dv, lq, lk, lv, idx = _qkv(q, k, v)
+    mid, f32 = _mode(mode, q.dtype), torch.float32
     n = cu_seqlens.numel() - 1
-    _shape(g, "g", H)
-    _shape(dO, "dO", N, H, dv)
-    _shape(S0, "S0", n, H, dk, dv)
-    _shape(dS_final, "dS_final", n, H, dk, dv)
-    with _On(dev, stream) as handle:
-        dq = torch.empty((N, Hk, dk), dtype=q.dtype, device=dev)
-        dk_, dv_ = torch.empty_like(dq), torch.empty((N, H, dv), dtype=q.dtype, device=dev)
-        dS0 = torch.empty((n, H, dk, dv), dtype=f32, device=dev) if with_dS0 else None
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), idx)
+    _check(g, "g", f32, (H,), idx)
+    _check(dO, "dO", q.dtype, (N, H, dv), idx)
+    _check(S0, "S0", f32, (n, H, dk, dv), idx)
+    _check(dS_final, "dS_final", f32, (n, H, dk, dv), idx)
+    with _on(idx, stream) as handle:
+        dq, dk_, dv_ = q.new_empty((N, Hk, dk)), q.new_empty((N, Hk, dk)), q.new_empty((N, H, dv))
+        dS0 = q.new_empty((n, H, dk, dv), dtype=f32) if with_dS0 else None
         _run(la_packed_bwd(q, k, v, g, dO, S0, dS_final, dq, dk_, dv_, dS0, cu_seqlens, n, N, max_len, H, Hk, dk, dv,
-                           *ld, _mode(mode, q.dtype), handle))
+                           lq, lk, lv, mid, handle))
     return dq, dk_, dv_, dS0
 
 
@@ -230,20 +252,16 @@ def packed_step(q, k, v, S, mode, g=None, slots=None, o=None, stream=None):
     [rows,H,dk,dv] fp32, updated in place at slots int32 [n] (None: row i).
     Returns o [n,H,dv]."""
     import torch
-    N, H, Hk, dk, dv, ld = _qkv(q, k, v)
-    dev = q.device
-    _same_device(dev, q=q, k=k, v=v, S=S, g=g, slots=slots, o=o)
-    _dense(torch.float32, S=S, g=g)
-    _dense(torch.int32, slots=slots)
-    _dense(q.dtype, o=o)
-    _shape(g, "g", H)
-    _shape(S, "S", S.shape[0], H, dk, dv)
-    _shape(slots, "slots", N)
-    _shape(o, "o", N, H, dv)
-    with _On(dev, stream) as handle:
+    N, H, Hk, dk, dv, lq, lk, lv, idx = _qkv(q, k, v)
+    mid, rows = _mode(mode, q.dtype), S.shape[0]
+    _check(S, "S", torch.float32, (rows, H, dk, dv), idx)
+    _check(g, "g", torch.float32, (H,), idx)
+    _check(slots, "slots", torch.int32, (N,), idx)
+    _check(o, "o", q.dtype, (N, H, dv), idx)
+    with _on(idx, stream) as handle:
         if o is None:
-            o = torch.empty((N, H, dv), dtype=q.dtype, device=dev)
-        _run(la_packed_step(q, k, v, g, o, S, slots, N, S.shape[0], H, Hk, dk, dv, *ld, _mode(mode, q.dtype), handle))
+            o = q.new_empty((N, H, dv))
+        _run(la_packed_step(q, k, v, g, o, S, slots, N, rows, H, Hk, dk, dv, lq, lk, lv, mid, handle))
     return o
 
 
@@ -267,52 +285,51 @@ def rotary(q, k, pos, freq, sections=None, interleaved=False, inverse=False, sca
     [N/T_out,H,T_out,d]. inverse turns back: the backward pass. Returns (q, k)."""
     import torch
     N, H, d, T, ldq = _tokens_of(q, "q")
-    Hk, ldk = 0, 0
+    idx, dt, Hk, ldk = _index(q, "q"), q.dtype, 0, 0
     if k is not None:
         Nk, Hk, dk, Tk, ldk = _tokens_of(k, "k")
-        if (Nk, dk, Tk) != (N, d, T) or k.dtype != q.dtype:
-            raise ValueError("q and k must agree in tokens, channels, layout and dtype")
-    dev = q.device
-    _same_device(dev, q=q, k=k, pos=pos, freq=freq, q_out=q_out, k_out=k_out)
-    _dense(torch.int32, pos=pos)
-    _dense(torch.float64, freq=freq)
-    _dense(q.dtype, q_out=q_out, k_out=k_out)
-    sections = [freq.numel()] if sections is None else list(sections)
-    if sum(sections) != freq.numel() or not 1 <= len(sections) <= 3:
+        if Nk != N or dk != d or Tk != T or k.dtype is not dt or k.get_device() != idx:
+            raise ValueError("q and k must agree in tokens, channels, layout, dtype and device")
+    pairs = freq.numel()
+    s = (pairs,) if sections is None else tuple(sections)
+    axes = len(s)
+    if sum(s) != pairs or not 1 <= axes <= 3:
         raise ValueError("sections: the pairs of one to three axes, as many as freq has")
-    _shape(pos, "pos", N, len(sections))
-    s = sections + [0] * (3 - len(sections))
+    _check(pos, "pos", torch.int32, (N, axes), idx)
+    _check(freq, "freq", torch.float64, (pairs,), idx)
     if T_out and N % T_out:
         raise ValueError("T_out must divide the tokens")
-    flags = _flag(q.dtype) | (LAYER_CONSTANTS["LA_ROT_INTERLEAVED"] if interleaved else 0) \
+    shape = (N // T_out, H, T_out, d) if T_out else (N, H, d)
+    kshape = (N // T_out, Hk, T_out, d) if T_out else (N, Hk, d)
+    _check(q_out, "q_out", dt, shape, idx)
+    _check(k_out, "k_out", dt, kshape, idx)
+    flags = _flag(dt) | (LAYER_CONSTANTS["LA_ROT_INTERLEAVED"] if interleaved else 0) \
         | (LAYER_CONSTANTS["LA_ROT_INVERSE"] if inverse else 0)
-    with _On(dev, stream) as handle:
-        outs = []
-        for name, heads, t in (("q_out", H, q_out), ("k_out", Hk, k_out)):
-            shape = (N // T_out, heads, T_out, d) if T_out else (N, heads, d)
-            if heads == 0:
-                t = None
-            elif t is None:
-                t = torch.empty(shape, dtype=q.dtype, device=dev)
-            _shape(t, name, *shape)
-            outs.append(t)
-        _run(la_rotary(q, k, outs[0], outs[1], pos, freq, len(sections), *s, N, H, Hk, d, T, T_out, ldq, ldk,
+    with _on(idx, stream) as handle:
+        if q_out is None:
+            q_out = q.new_empty(shape)
+        if k is None:
+            k_out = None
+        elif k_out is None:
+            k_out = q.new_empty(kshape)
+        _run(la_rotary(q, k, q_out, k_out, pos, freq, axes, *(s + (0, 0))[:3], N, H, Hk, d, T, T_out, ldq, ldk,
                        scale_q, scale_k, flags, handle))
-    return outs[0], outs[1]
+    return q_out, k_out
 
 
-def _block(x, w, gate, act, res, scale, w_next, **more):
-    """(N, G, d, T, act id) of an epilogue call."""
+def _block(x, w, gate, act, res, scale, w_next):
+    """(N, G, d, T, act id, device) of an epilogue call."""
     import torch
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     N, G, d, T, _ = _tokens_of(x, "x")
-    _same_device(x.device, x=x, w=w, gate=gate, res=res, scale=scale, w_next=w_next, **more)
-    _dense(x.dtype, x=x, gate=gate, res=res, **more)
-    _dense(torch.float32, w=w, scale=scale, w_next=w_next)
-    for name, t in dict(gate=gate, res=res, **more).items():
-        _shape(t, name, N, G, d)
-    for name, t in (("w", w), ("scale", scale), ("w_next", w_next)):
-        _shape(t, name, d)
-    return N, G, d, T, ACT_IDS[act] if gate is not None else 0
+    idx, dt, f32 = _index(x, "x"), x.dtype, torch.float32
+    _check(gate, "gate", dt, (N, G, d), idx)
+    _check(res, "res", dt, (N, G, d), idx)
+    _check(w, "w", f32, (d,), idx)
+    _check(scale, "scale", f32, (d,), idx)
+    _check(w_next, "w_next", f32, (d,), idx)
+    return N, G, d, T, ACT_IDS[act] if gate is not None else 0, idx
 
 
 def epilogue(x, w=None, gate=None, act="silu", res=None, scale=None, w_next=None, with_next=None, eps=1e-5, out=None,
@@ -321,18 +338,21 @@ def epilogue(x, w=None, gate=None, act="silu", res=None, scale=None, w_next=None
     next = rmsnorm(out) w_next. x [N,G,d] or head-major [B,G,T,d]; gate, res
     [N,G,d]; w, scale, w_next [d] fp32. next is computed with w_next, next or
     with_next. Returns (out, next or None)."""
-    import torch
-    N, G, d, T, a = _block(x, w, gate, act, res, scale, w_next, out=out, next=next)
+    N, G, d, T, a, idx = _block(x, w, gate, act, res, scale, w_next)
     if with_next is None:
         with_next = w_next is not None or next is not None
-    with _On(x.device, stream) as handle:
+    flags = _flag(x.dtype)
+    _check(out, "out", x.dtype, (N, G, d), idx)
+    _check(next, "next", x.dtype, (N, G, d), idx)
+    with _on(idx, stream) as handle:
         if out is None:
-            out = torch.empty((N, G, d), dtype=x.dtype, device=x.device)
-        if with_next and next is None:
-            next = torch.empty((N, G, d), dtype=x.dtype, device=x.device)
-        _run(la_epilogue(x, w, gate, a, res, scale, w_next, out, next if with_next else None, eps, N, G, d, T,
-                         _flag(x.dtype), handle))
-    return out, (next if with_next else None)
+            out = x.new_empty((N, G, d))
+        if not with_next:
+            next = None
+        elif next is None:
+            next = x.new_empty((N, G, d))
+        _run(la_epilogue(x, w, gate, a, res, scale, w_next, out, next, eps, N, G, d, T, flags, handle))
+    return out, next
 
 
 def epilogue_bwd(x, d_out, w=None, gate=None, act="silu", res=None, scale=None, w_next=None, d_next=None, eps=1e-5,
@@ -342,12 +362,15 @@ def epilogue_bwd(x, d_out, w=None, gate=None, act="silu", res=None, scale=None, 
     layout), dgate, dres, dw, dscale, dw_next (None where the forward had no
     such input)."""
     import torch
-    N, G, d, T, a = _block(x, w, gate, act, res, scale, w_next, d_out=d_out, d_next=d_next)
-    with _On(x.device, stream) as handle:
-        wide = lambda t: None if t is None else torch.empty((N, G, d), dtype=x.dtype, device=x.device)  # noqa: E731
-        thin = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-        r = {"dx": torch.empty_like(x), "dgate": wide(gate), "dres": wide(res), "dw": thin(w), "dscale": thin(scale),
-             "dw_next": thin(w_next)}
-        _run(la_epilogue_bwd(x, w, gate, a, res, scale, w_next, d_out, d_next, r["dx"], r["dgate"], r["dres"],
-                             r["dw"], r["dscale"], r["dw_next"], eps, N, G, d, T, _flag(x.dtype), handle))
-    return r
+    N, G, d, T, a, idx = _block(x, w, gate, act, res, scale, w_next)
+    flags = _flag(x.dtype)
+    _check(d_out, "d_out", x.dtype, (N, G, d), idx)
+    _check(d_next, "d_next", x.dtype, (N, G, d), idx)
+    with _on(idx, stream) as handle:
+        wide = (N, G, d)
+        dx, dgate = torch.empty_like(x), None if gate is None else x.new_empty(wide)
+        dres = None if res is None else x.new_empty(wide)
+        dw, dscale, dw_next = (None if t is None else torch.empty_like(t) for t in (w, scale, w_next))
+        _run(la_epilogue_bwd(x, w, gate, a, res, scale, w_next, d_out, d_next, dx, dgate, dres, dw, dscale, dw_next,
+                             eps, N, G, d, T, flags, handle))
+    return {"dx": dx, "dgate": dgate, "dres": dres, "dw": dw, "dscale": dscale, "dw_next": dw_next}
