@@ -12,8 +12,10 @@
 // gamma^(j+1) for Z, chunks from the last to the first. The decay of a head is
 // one number, so every power comes from a table of gamma^0 .. gamma^128.
 //
-// Work. A unit is one segment (up to seg tokens) of one sequence; one CTA takes
-// a unit, a head and 64 value columns. Sequences longer than the segment first
+// Work. A unit is one segment (up to seg tokens) of one sequence; an item of
+// work is a unit, a head and 64 value columns. One CTA a SM takes items from a
+// queue, and the roles below go from one item's last chunk to the next one's
+// first without draining. Sequences longer than the segment first
 // go through the same kernel with STATE set, which only forms each segment's
 // own contribution to the state, and a scan over the segments. Unit u of
 // sequence s are the numbers from floor(cu[s]/seg) + s on: enough for its
@@ -36,11 +38,11 @@
 // Roles, 896 threads. Every group works on its own part of a chunk and hands it
 // on through mbarriers, up to two chunks apart; a group of its own for each
 // step, because the steps are bound by their instructions' latency:
-//   warp 0        TMA loads of X, Y, Z, two stages
+//   warp 0        the queue, and TMA loads of X, Y, Z, two stages
 //   warps 1-3     MMAs: dS and X S; scores (and TMEM); P Z
 //   warps 4-7     state: S <- gamma^n S + dS, its bf16 copy
 //   warps 8-11    output: gamma^(i+1) X S + P Z, to memory by TMA
-//   warps 12-19   Z' high and low
+//   warps 12-19   the tables of powers; Z' high and low
 //   warps 20-27   P, in TMEM over its scores
 // Every wait is bounded; on expiry the CTA raises the status word, all roles
 // leave, copies and MMAs in flight are drained and TMEM is released.
@@ -71,8 +73,15 @@ static_assert(kRegsIssue + kRegsState + kRegsOut + 2 * kRegsP + 2 * kRegsZ <= 7 
 struct Segments {
   int tokens;       // of a segment; 0: every sequence is one unit
   int units;        // sequences, or the numbers units may have
+  int items;        // units * heads * tiles of 64 value columns
+  unsigned *queue;  // next item for a CTA that is done, from zero; null: one item a CTA
   const float *in;  // [unit][H][dk][dv] entering states, or null: S_in by slot
   float *out;       // STATE: the segments' own contributions
+};
+
+// One item of work, decoded by warp 0 for all roles. chunks < 0: no more items.
+struct Item {
+  int t0, t1, chunks, h, v0, u, slot, leaves;
 };
 
 // First unit number of sequence s.
@@ -80,36 +89,60 @@ __device__ __forceinline__ int first_unit(const PackedPass &p, int seg, int s) {
   return min(max(__ldg(p.cu + s), 0), p.total) / seg + s;
 }
 
-// The tokens [t0, t1) of unit u, and its sequence's [a, b). False: no such unit.
-__device__ __forceinline__ bool find_unit(const PackedPass &p, const Segments &sg, int u, int *s, int *a, int *b,
-                                          int *t0, int *t1) {
-  if (sg.tokens == 0) {
-    *s = u;
-    packed_range(p.cu, u, p.total, a, b);
-    *t0 = *a;
-    *t1 = *b;
-    return true;
+// Item w, by a whole warp. False: its unit has nothing to do.
+template <bool STATE>
+__device__ __forceinline__ bool decode(const PackedPass &p, const Segments &sg, int w, int lane, Item &it) {
+  const int vtiles = p.db / 64;
+  it.v0 = w % vtiles * 64;
+  it.h = w / vtiles % p.H;
+  it.u = w / vtiles / p.H;
+  int s = it.u, a, b;
+  if (sg.tokens) {  // the last sequence whose first unit is at most u: 32 at a time
+    int lo = -1, hi = p.n_seq;
+    while (hi - lo > 1) {
+      const int step = (hi - lo - 1 + 31) / 32, i = lo + 1 + lane * step;
+      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && first_unit(p, sg.tokens, i) <= it.u));
+      const int base = lo + 1;
+      if (n > 0) lo = base + (n - 1) * step;
+      hi = min(hi, base + n * step);
+    }
+    if (lo < 0) return false;
+    s = lo;
   }
-  int count = 0;
-  for (int base = 0; base < p.n_seq; base += blockDim.x) {
-    const int i = base + threadIdx.x;
-    count += __syncthreads_count(i < p.n_seq && first_unit(p, sg.tokens, i) <= u);
+  packed_range(p.cu, s, p.total, &a, &b);
+  it.t0 = a;
+  it.t1 = b;
+  if (sg.tokens) {
+    const long long from = (long long)(it.u - first_unit(p, sg.tokens, s)) * sg.tokens;
+    if (from < 0 || (from > 0 && from >= b - a)) return false;
+    it.t0 = a + static_cast<int>(from);
+    it.t1 = min(b, it.t0 + sg.tokens);
   }
-  if (count == 0) return false;
-  *s = count - 1;
-  packed_range(p.cu, *s, p.total, a, b);
-  const long long from = (long long)(u - first_unit(p, sg.tokens, *s)) * sg.tokens;
-  if (from < 0 || (from > 0 && from >= *b - *a)) return false;
-  *t0 = *a + static_cast<int>(from);
-  *t1 = min(*b, *t0 + sg.tokens);
-  return true;
+  it.chunks = (it.t1 - it.t0 + kN - 1) / kN;
+  it.leaves = p.reverse ? it.t0 == a : it.t1 == b;  // the state behind the unit is the sequence's last
+  if (STATE) return !it.leaves;
+  // the state row, or -1: without one, outside the pool, or taken by an earlier sequence
+  it.slot = -1;
+  if ((p.S_in && !sg.in) || (p.S_out && it.leaves)) {
+    int slot = p.slots ? __ldg(p.slots + s) : s;
+    if (slot < 0 || slot >= p.n_slots) slot = -1;
+    if (p.slots && slot >= 0) {
+      int taken = 0;
+#pragma unroll 4
+      for (int j = lane; j < s; j += 32) taken |= __ldg(p.slots + j) == slot;
+      if (__any_sync(0xffffffffu, taken)) slot = -1;
+    }
+    it.slot = slot;
+  }
+  return it.chunks > 0 || (p.S_out && it.slot >= 0);
 }
 
 // Shared memory, in 16 KB tiles (128 rows of 64 bf16, 128-byte swizzle).
 constexpr uint32_t kTile = 16384;
 constexpr uint32_t kSmX = 0, kSmY = kSmX + 4 * kTile, kSmZ = kSmY + 4 * kTile, kSmW = kSmZ + 2 * kTile,
                    kSmS = kSmW + 2 * kTile, kSmO = kSmS + kTile, kSmMisc = kSmO + kTile,
-                   kSmBytes = kSmMisc + 2048 + 1024;
+                   kSmBytes = kSmMisc + 3072;
+constexpr int kRing = 4;  // items decoded ahead
 // TMEM columns: two buffers of scores, over which go P (columns 0..63) and P Z (64..127),
 // two of X S, and dS of Z' high and low.
 constexpr uint32_t kColSc = 0, kColPZ = 64, kColXS = 256, kColD = 384;
@@ -145,45 +178,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ CUtensorMap tm_x,
                  const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_z,
                  const __grid_constant__ CUtensorMap tm_o) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wq = warp & 3;
-  const int vtiles = p.db / 64;
-  const int vt = blockIdx.x % vtiles, h = blockIdx.x / vtiles % p.H, u = blockIdx.x / vtiles / p.H;
-  int s, a, b, t0, t1;
-  if (!find_unit(p, sg, u, &s, &a, &b, &t0, &t1)) return;
-  const bool leaves = p.reverse ? t0 == a : t1 == b;  // the state behind this unit is the sequence's last
-  if (STATE && leaves) return;
-  const bool by_slot = !STATE && (sg.in == nullptr || (leaves && p.S_out));
-  const int slot = by_slot ? packed_slot(p.slots, s, p.n_slots) : -1;
-  const float *src = nullptr;
-  if (!STATE)
-    src = sg.in ? sg.in + ((size_t)u * p.H + h) * p.sized
-                : (p.S_in && slot >= 0 ? p.S_in + ((size_t)slot * p.H + h) * p.sized : nullptr);
-  float *dst = nullptr;
-  if (STATE) dst = sg.out + ((size_t)u * p.H + h) * p.sized;
-  else if (p.S_out && leaves && slot >= 0) dst = p.S_out + ((size_t)slot * p.H + h) * p.sized;
-  const bool src_t = p.in_t && !sg.in;  // the segments' states lie as this pass wants them
-  const int v0 = vt * 64, db = p.db;
-  const float g = p.g ? __ldg(p.g + h) : 0.f;
-  const int chunks = (t1 - t0 + kN - 1) / kN;
-  if (chunks == 0) {  // an empty sequence: its state passes through
-    if (dst && dst != src)
-      for (int i = tid; i < DA * 64; i += kThreads) {
-        const int c = i / 64, v = v0 + i % 64;
-        dst[(size_t)c * db + v] = src ? src[src_t ? (size_t)v * DA + c : (size_t)c * db + v] : 0.f;
-      }
-    return;
-  }
-
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wq = warp & 3, group = warp >> 2;
+  const int db = p.db;
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kSmMisc);
   uint64_t *xy_full = bars, *xy_free = bars + 2, *z_full = bars + 4, *z_free = bars + 6, *sc_full = bars + 8,
-           *p_ready = bars + 10, *w_ready = bars + 12, *o_full = bars + 14, *o_free = bars + 16, *d_full = bars + 18,
-           *d_free = bars + 19, *s_ready = bars + 20, *xs_full = bars + 21, *drain = bars + 22;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 26);
+           *p_ready = bars + 10, *w_ready = bars + 12, *o_full = bars + 14, *o_free = bars + 16, *t_full = bars + 18,
+           *t_free = bars + 20, *d_full = bars + 22, *d_free = bars + 23, *s_ready = bars + 24, *xs_full = bars + 25,
+           *drain = bars + 26, *e_full = bars + 29, *e_free = bars + 29 + kRing;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 29 + 2 * kRing);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  float *pw = reinterpret_cast<float *>(sm + kSmMisc + 256);  // gamma^0 .. gamma^128
-  float *pij = pw + 132;  // [127 + i - j]: the factor of a score, zero where j is not seen from i
+  Item *ring = reinterpret_cast<Item *>(sm + kSmMisc + 384);
+  // Two tables of powers of gamma, of two items' heads: [127 + e] is gamma^e, [0 .. 126] zero
+  // (reversed: [127 - e], and zeros behind), [255] is gamma^128. At [127 + i - j] stands the
+  // factor of a score, zero where j is not seen from i.
+  float *tables = reinterpret_cast<float *>(sm + kSmMisc + 1024);
 
   if (warp == 2) {
     tmem_alloc(tmem_slot, 512);
@@ -200,13 +209,19 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       mbar_init(&w_ready[i], 8);
       mbar_init(&o_full[i], 2);  // X S, P Z
       mbar_init(&o_free[i], 4);
+      mbar_init(&t_full[i], 8);
+      mbar_init(&t_free[i], 12);  // output and P
     }
     mbar_init(d_full, 1);
     mbar_init(d_free, 4);
     mbar_init(s_ready, 4);
     mbar_init(xs_full, 1);
     for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
-    *abort_flag = 0;
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&e_full[i], 1);
+      mbar_init(&e_free[i], STATE ? 13 : 27);  // dS, state, Z' (scores, P Z, output, P)
+    }
+    *abort_flag = (smem_u32(sm) & 1023u) != 0;  // the tiles' swizzle goes by the address: none of them may move
     fence_mbar_init();
   }
   if (DA == 64) {  // channels 64..127 of Y: zero rows of dS
@@ -214,17 +229,11 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       reinterpret_cast<uint4 *>(sm + kSmY + (2 * (i >> 10) + 1) * kTile)[i & 1023] = make_uint4(0, 0, 0, 0);
     fence_proxy_async();
   }
-  for (int i = tid; i <= kN; i += kThreads) pw[i] = decay_power(g, i);
-  for (int i = tid; i < 2 * kN - 1; i += kThreads) {
-    const int e = p.reverse ? 127 - i : i - 127;
-    pij[i] = e >= 0 ? decay_power(g, e) : 0.f;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   const uint32_t tl = tbase + (static_cast<uint32_t>(wq * 32) << 16);
-  auto chunk_at = [&](int j) { return p.reverse ? chunks - 1 - j : j; };
   // The loop is as short as it can be (the status word is raised at the end): the code that all
   // roles run for a chunk has to stay in the SM's instruction cache together. With the waits,
   // products and conversions unrolled in place it did not, and a chunk took three times as long.
@@ -239,103 +248,155 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
   };
   // A group of four warps waits: one lane polls, the others sleep on the group's barrier.
   // With a polling lane in each of 24 warps the polls took more issue slots than the work.
-  const int group = warp >> 2;
   auto wait_group = [&](uint64_t *bar, uint32_t parity) {
     bool ok = true;
-    if (wq == (group & 2) && lane == 0) ok = wait(bar, parity);  // not on the schedulers of the issuing warps 1 and 3
+    if (wq == (group & 2) && lane == 0) ok = wait(bar, parity);  // not on the schedulers of warps 1 and 3
     return group_all(ok, group);
   };
+  // Item k of this CTA, in its ring place; the chunk of its j-th turn.
+  auto item_at = [&](int k) { return ring[k & (kRing - 1)]; };
+  auto chunk_at = [&](const Item &it, int j) { return p.reverse ? it.chunks - 1 - j : j; };
+  auto item_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&e_free[k & (kRing - 1)]);
+  };
+#define LA_ITEM_FULL(k) &e_full[(k) & (kRing - 1)], (k) / kRing
 
+  // In every role: k counts items, n chunks of all items; a chunk's buffers and phases go by n.
   if (warp < 4) {
     regs_down<kRegsIssue>();
-    if (warp == 0 && lane == 0) {
-      // ----------------------------------------------------------- TMA loads
-      prefetch_tmap(&tm_y);
-      prefetch_tmap(&tm_z);
-      if (!STATE) prefetch_tmap(&tm_x);
-      const int xh = h / p.rx, yh = h / p.ry, zh = h / p.rz;
-      int j = 0;
-      for (; j < chunks; ++j) {
-        const int t = t0 + chunk_at(j) * kN, st = j & 1;
-        const uint32_t again = (j >> 1) ^ 1;
-        // Z first: it is the first to be free (behind P Z) and the first to be used (Z')
-        if (!wait(&z_free[st], again)) break;
-        mbar_arrive_expect_tx(&z_full[st], kTile);
-        tma_load_3d(sm + kSmZ + st * kTile, &tm_z, &z_full[st], v0, zh, t);
-        if (!wait(&xy_free[st], again)) break;
-        mbar_arrive_expect_tx(&xy_full[st], DA / 64 * kTile * (STATE ? 1 : 2));
-#pragma unroll
-        for (int k = 0; k < DA / 64; ++k) {
-          tma_load_3d(sm + kSmY + (2 * st + k) * kTile, &tm_y, &xy_full[st], 64 * k, yh, t);
-          if (!STATE) tma_load_3d(sm + kSmX + (2 * st + k) * kTile, &tm_x, &xy_full[st], 64 * k, xh, t);
+    if (warp == 0) {
+      // ------------------------------------------- items, and their TMA loads
+      if (lane == 0) {
+        prefetch_tmap(&tm_y);
+        prefetch_tmap(&tm_z);
+        if (!STATE) prefetch_tmap(&tm_x);
+      }
+      const int vtiles = db / 64;
+      int n = 0;
+      bool ok = true;
+      for (int k = 0, w = blockIdx.x; ok; ++k) {
+        Item it;
+        bool found = false;
+        while (!found && w < sg.items) {
+          found = decode<STATE>(p, sg, w, lane, it);
+          // the item after this one
+          unsigned next = INT_MAX;
+          if (sg.queue && lane == 0) next = gridDim.x + atomicAdd(sg.queue, 1u);
+          w = static_cast<int>(__shfl_sync(0xffffffffu, next, 0));
         }
-        // the chunk after the next into L2; its loads wait for this chunk's products. X and Y
-        // are read by both CTAs of a head of 128 value columns: one of them asks for each
-        if (j + 2 < chunks) {
-          const int t2 = t0 + chunk_at(j + 2) * kN;
-          tma_prefetch_3d(&tm_z, v0, zh, t2);
-#pragma unroll
-          for (int k = 0; k < DA / 64; ++k) {
-            if (vtiles == 1 || vt == 0) tma_prefetch_3d(&tm_y, 64 * k, yh, t2);
-            if (!STATE && (vtiles == 1 || vt == 1)) tma_prefetch_3d(&tm_x, 64 * k, xh, t2);
+        if (!found) it.chunks = -1;
+        int go = 1;
+        if (lane == 0) {
+          go = wait(&e_free[k & (kRing - 1)], k / kRing ^ 1);
+          if (go) {
+            ring[k & (kRing - 1)] = it;
+            mbar_arrive(&e_full[k & (kRing - 1)]);
           }
         }
+        ok = __shfl_sync(0xffffffffu, go, 0) && found;
+        if (lane == 0 && ok) {
+          const int xh = it.h / p.rx, yh = it.h / p.ry, zh = it.h / p.rz, first = n;
+          for (; n < first + it.chunks; ++n) {
+            const int j = n - first, t = it.t0 + chunk_at(it, j) * kN, st = n & 1;
+            const uint32_t again = (n >> 1) ^ 1;
+            // Z first: it is the first to be free (behind P Z) and the first to be used (Z')
+            if (!wait(&z_free[st], again)) break;
+            mbar_arrive_expect_tx(&z_full[st], kTile);
+            tma_load_3d(sm + kSmZ + st * kTile, &tm_z, &z_full[st], it.v0, zh, t);
+            if (!wait(&xy_free[st], again)) {
+              ++n;  // Z of this chunk is on its way
+              break;
+            }
+            mbar_arrive_expect_tx(&xy_full[st], DA / 64 * kTile * (STATE ? 1 : 2));
+#pragma unroll
+            for (int c = 0; c < DA / 64; ++c) {
+              tma_load_3d(sm + kSmY + (2 * st + c) * kTile, &tm_y, &xy_full[st], 64 * c, yh, t);
+              if (!STATE) tma_load_3d(sm + kSmX + (2 * st + c) * kTile, &tm_x, &xy_full[st], 64 * c, xh, t);
+            }
+            // the chunk after the next into L2; its loads wait for this chunk's products. X and Y
+            // are read by both CTAs of a head of 128 value columns: one of them asks for each
+            if (j + 2 < it.chunks) {
+              const int t2 = it.t0 + chunk_at(it, j + 2) * kN;
+              tma_prefetch_3d(&tm_z, it.v0, zh, t2);
+#pragma unroll
+              for (int c = 0; c < DA / 64; ++c) {
+                if (vtiles == 1 || it.v0 == 0) tma_prefetch_3d(&tm_y, 64 * c, yh, t2);
+                if (!STATE && (vtiles == 1 || it.v0 != 0)) tma_prefetch_3d(&tm_x, 64 * c, xh, t2);
+              }
+            }
+          }
+        }
+        __syncwarp();
       }
       // given up: copies still in flight must land before the CTA's memory is released
       // (a barrier that was never armed in its last phase just runs out its wait)
-      if (j < chunks)
-        for (int n = j; n >= 0 && n >= j - 1; --n) {
-          (void)mbar_wait_bounded(&xy_full[n & 1], (n >> 1) & 1, 1u << 16);
-          (void)mbar_wait_bounded(&z_full[n & 1], (n >> 1) & 1, 1u << 16);
+      if (lane == 0 && *abort_flag)
+        for (int m = n; m >= 0 && m >= n - 2; --m) {
+          (void)mbar_wait_bounded(&xy_full[m & 1], (m >> 1) & 1, 1u << 16);
+          (void)mbar_wait_bounded(&z_full[m & 1], (m >> 1) & 1, 1u << 16);
         }
     } else if (!STATE && warp == 2 && lane == 0) {
       // -------------------------------------------------------- MMAs: scores
       constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
       const uint32_t dx = smem_u32(sm + kSmX), dy = smem_u32(sm + kSmY);
-      for (int j = 0; j < chunks; ++j) {
-        const int st = j & 1;
-        const uint32_t stage = 2 * st * kTile;
-        const bool tail = t1 - t0 < (chunk_at(j) + 1) * kN;  // foreign rows of Y are cleared behind Z'
-        if (!wait(&xy_full[st], j >> 1) || (tail && !wait(&w_ready[st], j >> 1)) || !wait(&o_free[st], (j >> 1) ^ 1))
-          break;
-        tc_fence_after();
+      bool ok = true;
+      for (int k = 0, n = 0; ok && wait(LA_ITEM_FULL(k)); ++k) {
+        const Item it = item_at(k);
+        if (it.chunks < 0) break;
+        for (int j = 0; j < it.chunks; ++j, ++n) {
+          const int st = n & 1;
+          const uint32_t stage = 2 * st * kTile;
+          const bool tail = it.t1 - it.t0 < (chunk_at(it, j) + 1) * kN;  // foreign rows of Y are cleared behind Z'
+          ok = wait(&xy_full[st], n >> 1) && (!tail || wait(&w_ready[st], n >> 1)) && wait(&o_free[st], (n >> 1) ^ 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 4
-        for (int k = 0; k < DA / 16; ++k) {
-          const uint32_t off = stage + (k >> 2) * kTile + (k & 3) * 32;
-          mma_bf16(tbase + kColSc + 128 * st, desc(dx + off, 16), desc(dy + off, 16), id_sc, k > 0);
+          for (int c = 0; c < DA / 16; ++c) {
+            const uint32_t off = stage + (c >> 2) * kTile + (c & 3) * 32;
+            mma_bf16(tbase + kColSc + 128 * st, desc(dx + off, 16), desc(dy + off, 16), id_sc, c > 0);
+          }
+          mma_commit(&sc_full[st]);
+          mma_commit(&xy_free[st]);
         }
-        mma_commit(&sc_full[st]);
-        mma_commit(&xy_free[st]);
+        mbar_arrive(&e_free[k & (kRing - 1)]);
       }
       mma_commit(&drain[2]);
       (void)mbar_wait_bounded(&drain[2], 0, kSpin);
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------- MMAs: dS, X S
       constexpr uint32_t id_d = idesc_bf16_f32(128, 128, true, true), id_o = idesc_bf16_f32(128, 64, false, true);
-      const uint32_t dx = smem_u32(sm + kSmX);
+      const uint32_t dx = smem_u32(sm + kSmX), dyt = smem_u32(sm + kSmY), dw = smem_u32(sm + kSmW);
       const uint32_t ds = smem_u32(sm + kSmS);
-      const uint32_t dyt = smem_u32(sm + kSmY);
-      const uint32_t dw = smem_u32(sm + kSmW);
-      for (int j = 0; j < chunks; ++j) {
-        const int st = j & 1;
-        if (!wait(&xy_full[st], j >> 1) || !wait(d_free, j ^ 1) || !wait(&w_ready[st], j >> 1)) break;
-        tc_fence_after();
-#pragma unroll 4
-        for (int k = 0; k < kN / 16; ++k)
-          mma_bf16(tbase + kColD, desc(dyt + 2 * st * kTile + k * 2048, kTile), desc(dw + k * 2048, kTile), id_d, k > 0);
-        mma_commit(d_full);
-        mma_commit(&z_free[st]);
-        if (!STATE) {  // in the time that the next Z' takes
-          if (!wait(&o_free[st], (j >> 1) ^ 1) || !wait(s_ready, j)) break;
+      bool ok = true;
+      for (int k = 0, n = 0; ok && wait(LA_ITEM_FULL(k)); ++k) {
+        const int chunks = item_at(k).chunks;
+        if (chunks < 0) break;
+        for (int j = 0; j < chunks; ++j, ++n) {
+          const int st = n & 1;
+          ok = wait(&xy_full[st], n >> 1) && wait(d_free, n ^ 1) && wait(&w_ready[st], n >> 1);
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll 4
-          for (int k = 0; k < DA / 16; ++k)
-            mma_bf16(tbase + kColXS + 64 * st, desc(dx + 2 * st * kTile + (k >> 2) * kTile + (k & 3) * 32, 16),
-                     desc(ds + k * 2048, kTile), id_o, k > 0);
-          mma_commit(xs_full);
-          mma_commit(&o_full[st]);
+          for (int c = 0; c < kN / 16; ++c)
+            mma_bf16(tbase + kColD, desc(dyt + 2 * st * kTile + c * 2048, kTile), desc(dw + c * 2048, kTile), id_d,
+                     c > 0);
+          mma_commit(d_full);
+          mma_commit(&z_free[st]);
+          if (!STATE) {  // in the time that the next Z' takes
+            ok = wait(&o_free[st], (n >> 1) ^ 1) && wait(s_ready, n);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 4
+            for (int c = 0; c < DA / 16; ++c)
+              mma_bf16(tbase + kColXS + 64 * st, desc(dx + 2 * st * kTile + (c >> 2) * kTile + (c & 3) * 32, 16),
+                       desc(ds + c * 2048, kTile), id_o, c > 0);
+            mma_commit(xs_full);
+            mma_commit(&o_full[st]);
+          }
+          mma_commit(&xy_free[st]);
         }
-        mma_commit(&xy_free[st]);
+        mbar_arrive(&e_free[k & (kRing - 1)]);
       }
       mma_commit(&drain[0]);
       (void)mbar_wait_bounded(&drain[0], 0, kSpin);
@@ -343,18 +404,25 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       // ----------------------------------------------------------- MMAs: P Z
       constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);
       const uint32_t dz = smem_u32(sm + kSmZ);
-      for (int j = 0; j < chunks; ++j) {
-        const int st = j & 1;
-        // (behind Z', Z is there and its foreign rows are clear)
-        if (!wait(&w_ready[st], j >> 1) || !wait(&p_ready[st], j >> 1)) break;
-        tc_fence_after();
+      bool ok = true;
+      for (int k = 0, n = 0; ok && wait(LA_ITEM_FULL(k)); ++k) {
+        const int chunks = item_at(k).chunks;
+        if (chunks < 0) break;
+        for (int j = 0; j < chunks; ++j, ++n) {
+          const int st = n & 1;
+          // (behind Z', Z is there and its foreign rows are clear)
+          ok = wait(&w_ready[st], n >> 1) && wait(&p_ready[st], n >> 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 4
-        for (int k = 0; k < kN / 16; ++k)  // blocks of 32 tokens of P in the order 0, 3, 1, 2
-          mma_bf16_ts(tbase + kColSc + 128 * st + kColPZ,
-                      tbase + kColSc + 128 * st + (0x1320u >> (k & 6) * 2 & 0xf) * 16 + (k & 1) * 8,
-                      desc(dz + st * kTile + k * 2048, kTile), id_o, k > 0);
-        mma_commit(&o_full[st]);
-        mma_commit(&z_free[st]);
+          for (int c = 0; c < kN / 16; ++c)  // blocks of 32 tokens of P in the order 0, 3, 1, 2
+            mma_bf16_ts(tbase + kColSc + 128 * st + kColPZ,
+                        tbase + kColSc + 128 * st + (0x1320u >> (c & 6) * 2 & 0xf) * 16 + (c & 1) * 8,
+                        desc(dz + st * kTile + c * 2048, kTile), id_o, c > 0);
+          mma_commit(&o_full[st]);
+          mma_commit(&z_free[st]);
+        }
+        mbar_arrive(&e_free[k & (kRing - 1)]);
       }
       mma_commit(&drain[1]);
       (void)mbar_wait_bounded(&drain[1], 0, kSpin);
@@ -363,193 +431,263 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
     // ------------------------------------------------------------- the state
     regs_up<kRegsState>();
     const int c = wq * 32 + lane;  // key channel: row of S
-    float S[64];
-    if (src && c < DA) {
-      if (src_t) {
+    bool ok = true;
+    for (int k = 0, n = 0; ok && wait_group(LA_ITEM_FULL(k)); ++k) {
+      const Item it = item_at(k);
+      if (it.chunks < 0) break;
+      const size_t by_unit = ((size_t)it.u * p.H + it.h) * p.sized, by_slot = ((size_t)it.slot * p.H + it.h) * p.sized;
+      const float *src = nullptr;
+      float *dst = nullptr;
+      if (STATE) {
+        dst = sg.out + by_unit;
+      } else {
+        if (sg.in) src = sg.in + by_unit;
+        else if (p.S_in && it.slot >= 0) src = p.S_in + by_slot;
+        if (p.S_out && it.leaves && it.slot >= 0) dst = p.S_out + by_slot;
+      }
+      float S[64];
+      if (src && c < DA) {
+        if (p.in_t && !sg.in) {  // (the segments' states lie as this pass wants them)
 #pragma unroll
-        for (int n = 0; n < 64; ++n) S[n] = src[(size_t)(v0 + n) * DA + c];
+          for (int e = 0; e < 64; ++e) S[e] = src[(size_t)(it.v0 + e) * DA + c];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 t = reinterpret_cast<const float4 *>(src + (size_t)c * db + it.v0)[e];
+            S[4 * e] = t.x; S[4 * e + 1] = t.y; S[4 * e + 2] = t.z; S[4 * e + 3] = t.w;
+          }
+        }
       } else {
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const float4 t = reinterpret_cast<const float4 *>(src + (size_t)c * db + v0)[n];
-          S[4 * n] = t.x; S[4 * n + 1] = t.y; S[4 * n + 2] = t.z; S[4 * n + 3] = t.w;
-        }
+        for (int e = 0; e < 64; ++e) S[e] = 0.f;
       }
-    } else {
+      const float g = p.g ? __ldg(p.g + it.h) : 0.f;
+      const Decay whole(g, kN), part(g, it.t1 - it.t0 - (it.chunks - 1) * kN);
+      for (int j = 0; j < it.chunks; ++j, ++n) {
+        if (!STATE) {  // row c of the bf16 copy, once X S of the chunk before is done with it
+          ok = n == 0 || wait_group(xs_full, n - 1);
+          if (!ok) break;
+          if (c < DA) {
 #pragma unroll
-      for (int n = 0; n < 64; ++n) S[n] = 0.f;
-    }
-    const Decay whole(g, kN), part(g, (t1 - t0) - (chunks - 1) * kN);
-    for (int j = 0; j < chunks; ++j) {
-      if (!STATE) {  // row c of the bf16 copy, once X S of the chunk before is done with it
-        if (j > 0 && !wait_group(xs_full, j - 1)) break;
-        if (c < DA) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4 *>(sm + kSmS + sw128_off(c, 8 * q)) = pack8(S + 8 * q);
+            for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4 *>(sm + kSmS + sw128_off(c, 8 * q)) = pack8(S + 8 * q);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_ready);
         }
-        fence_proxy_async();
+        ok = wait_group(d_full, n);
+        if (!ok) break;
+        tc_fence_after();
+        const Decay decay = chunk_at(it, j) == it.chunks - 1 ? part : whole;
+        // S m (+ S): see Decay
+        const uint64_t small = pair(decay.m, decay.m), one = decay.near ? pair(1.f, 1.f) : 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float d[8], lo[8];
+          tmem_ld8(tl + kColD + 8 * q, d);
+          tmem_ld8(tl + kColD + 64 + 8 * q, lo);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            add2(d + e, d + e, lo + e);
+            fma2(d + e, S + 8 * q + e, small, d + e);
+            fma2(S + 8 * q + e, S + 8 * q + e, one, d + e);
+          }
+        }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_ready);
+        if (lane == 0) mbar_arrive(d_free);
       }
-      if (!wait_group(d_full, j)) break;
-      tc_fence_after();
-      const Decay decay = chunk_at(j) == chunks - 1 ? part : whole;
-      // S m (+ S): see Decay
-      const uint64_t small = pair(decay.m, decay.m), one = decay.near ? pair(1.f, 1.f) : 0;
+      if (ok && dst && c < DA) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        float d[8], lo[8];
-        tmem_ld8(tl + kColD + 8 * q, d);
-        tmem_ld8(tl + kColD + 64 + 8 * q, lo);
-        tmem_wait_ld();
-#pragma unroll
-        for (int n = 0; n < 8; n += 2) {
-          add2(d + n, d + n, lo + n);
-          fma2(d + n, S + 8 * q + n, small, d + n);
-          fma2(S + 8 * q + n, S + 8 * q + n, one, d + n);
-        }
+        for (int e = 0; e < 16; ++e)
+          reinterpret_cast<float4 *>(dst + (size_t)c * db + it.v0)[e] =
+              make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(d_free);
-    }
-    if (dst && c < DA) {
-#pragma unroll
-      for (int n = 0; n < 16; ++n)
-        reinterpret_cast<float4 *>(dst + (size_t)c * db + v0)[n] =
-            make_float4(S[4 * n], S[4 * n + 1], S[4 * n + 2], S[4 * n + 3]);
+      item_done(k);
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ the output
     regs_up<kRegsOut>();
     const int i = wq * 32 + lane;
     uint8_t *ot = sm + kSmO;
-    for (int j = 0; !STATE && j < chunks; ++j) {
-      const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN), t = t0 + cc * kN + i;
-      const float r = pw[p.reverse ? max(rows - 1 - i, 0) : i + 1];
-      const uint64_t rr = pair(r, r);
-      const bool staged = !OF32 && wq * 32 + 32 <= rows;  // all of the warp's rows: through TMA
-      const size_t at = (size_t)t * p.ldo + (size_t)h * db + v0;
-      if (j > 0 && lane == 0) bulk_wait_read<0>();  // the staging rows have been read
-      if (!wait_group(&o_full[st], j >> 1)) break;
-      tc_fence_after();
-      uint4 o[8];
+    bool ok = !STATE;
+    for (int k = 0, n = 0, m = 0; ok && wait_group(LA_ITEM_FULL(k)); ++k) {
+      const Item it = item_at(k);
+      if (it.chunks < 0) break;
+      const float *tab = tables + 256 * (m & 1);
+      if (it.chunks > 0 && !wait_group(&t_full[m & 1], m >> 1)) break;
+      for (int j = 0; j < it.chunks; ++j, ++n) {
+        const int cc = chunk_at(it, j), st = n & 1, rows = min(kN, it.t1 - it.t0 - cc * kN), t = it.t0 + cc * kN + i;
+        // gamma^(i+1), reversed gamma^(rows-1-i)
+        const float r = tab[p.reverse ? 127 - max(rows - 1 - i, 0) : 128 + i];
+        const uint64_t rr = pair(r, r);
+        const bool staged = !OF32 && wq * 32 + 32 <= rows;  // all of the warp's rows: through TMA
+        const size_t at = (size_t)t * p.ldo + (size_t)it.h * db + it.v0;
+        if (n > 0 && lane == 0) bulk_wait_read<0>();  // the staging rows have been read
+        ok = wait_group(&o_full[st], n >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint4 o[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float xs[16], pz[16];
-        tmem_ld16(tl + kColXS + 64 * st + 16 * q, xs);
-        tmem_ld16(tl + kColSc + 128 * st + kColPZ + 16 * q, pz);
-        tmem_wait_ld();
+        for (int q = 0; q < 4; ++q) {
+          float xs[16], pz[16];
+          tmem_ld16(tl + kColXS + 64 * st + 16 * q, xs);
+          tmem_ld16(tl + kColSc + 128 * st + kColPZ + 16 * q, pz);
+          tmem_wait_ld();
 #pragma unroll
-        for (int n = 0; n < 16; n += 2) fma2(xs + n, xs + n, rr, pz + n);
-        if constexpr (OF32) {
-          if (i < rows)
+          for (int e = 0; e < 16; e += 2) fma2(xs + e, xs + e, rr, pz + e);
+          if constexpr (OF32) {
+            if (i < rows)
 #pragma unroll
-            for (int n = 0; n < 16; n += 4)
-              reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[4 * q + n / 4] =
-                  make_float4(xs[n], xs[n + 1], xs[n + 2], xs[n + 3]);
-        } else {
-          o[2 * q] = pack8(xs);
-          o[2 * q + 1] = pack8(xs + 8);
+              for (int e = 0; e < 16; e += 4)
+                reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[4 * q + e / 4] =
+                    make_float4(xs[e], xs[e + 1], xs[e + 2], xs[e + 3]);
+          } else {
+            o[2 * q] = pack8(xs);
+            o[2 * q + 1] = pack8(xs + 8);
+          }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free[st]);
-      if constexpr (!OF32) {
-        // the staging tile, or straight to memory
-        uint8_t *to = staged ? ot : reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + at);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (i < rows) *reinterpret_cast<uint4 *>(to + (staged ? sw128_off(i, 8 * q) : 16u * q)) = o[q];
-        if (staged) fence_proxy_async();
+        tc_fence_before();
         __syncwarp();
-        if (staged && lane == 0) {
-          tma_store_3d(&tm_o, ot + wq * 32 * 128, v0, h, t);
-          bulk_commit();
+        if (lane == 0) mbar_arrive(&o_free[st]);
+        if constexpr (!OF32) {
+          // the staging tile, or straight to memory
+          uint8_t *to = staged ? ot : reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + at);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (i < rows) *reinterpret_cast<uint4 *>(to + (staged ? sw128_off(i, 8 * q) : 16u * q)) = o[q];
+          if (staged) fence_proxy_async();
+          __syncwarp();
+          if (staged && lane == 0) {
+            tma_store_3d(&tm_o, ot + wq * 32 * 128, it.v0, it.h, t);
+            bulk_commit();
+          }
         }
       }
+      if (it.chunks > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t_free[m & 1]);
+        ++m;
+      }
+      item_done(k);
     }
     if (!STATE && lane == 0) bulk_wait<0>();
   } else if (warp < 20) {
-    // -------------------------------------------------------- Z' high and low
+    // ----------------------------------------- tables, and Z' high and low
     regs_down<kRegsZ>();
     const int half = (warp - 12) >> 2, i = wq * 32 + lane;  // columns 32*half .. of row i
-    for (int j = 0; j < chunks; ++j) {
-      const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN);
-      const bool mine = i < rows;
-      if (!wait_group(&z_full[st], j >> 1)) break;
-      uint8_t *zt = sm + kSmZ + st * kTile, *wt = sm + kSmW;
-      if (rows < kN) {  // foreign rows of Y and Z
-        if (!wait_group(&xy_full[st], j >> 1)) break;
-        if (!mine)
+    bool ok = true;
+    for (int k = 0, n = 0, m = 0; ok && wait_group(LA_ITEM_FULL(k)); ++k) {
+      const Item it = item_at(k);
+      if (it.chunks < 0) break;
+      const float *tab = tables + 256 * (m & 1);
+      if (it.chunks > 0) {
+        if (!STATE && !wait_group(&t_free[m & 1], (m >> 1) ^ 1)) break;
+        const float g = p.g ? __ldg(p.g + it.h) : 0.f;
+        const int at = half * 128 + i, e = at == 255 ? kN : p.reverse ? 127 - at : at - 127;
+        tables[256 * (m & 1) + at] = e >= 0 ? decay_power(g, e) : 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t_full[m & 1]);
+        if (!wait_group(&t_full[m & 1], m >> 1)) break;
+        ++m;
+      }
+      for (int j = 0; j < it.chunks; ++j, ++n) {
+        const int cc = chunk_at(it, j), st = n & 1, rows = min(kN, it.t1 - it.t0 - cc * kN);
+        const bool mine = i < rows;
+        ok = wait_group(&z_full[st], n >> 1);
+        if (!ok) break;
+        uint8_t *zt = sm + kSmZ + st * kTile, *wt = sm + kSmW;
+        if (rows < kN) {  // foreign rows of Y and Z
+          ok = wait_group(&xy_full[st], n >> 1);
+          if (!ok) break;
+          if (!mine)
 #pragma unroll 1
-          for (int q = 4 * half; q < 8 * (1 + DA / 64); q += (q & 3) == 3 ? 5 : 1)
-            *reinterpret_cast<uint4 *>((q < 8 ? zt : sm + kSmY + 2 * st * kTile + ((q >> 3) - 1) * kTile) +
-                                       sw128_off(i, 8 * (q & 7))) = make_uint4(0, 0, 0, 0);
+            for (int q = 4 * half; q < 8 * (1 + DA / 64); q += (q & 3) == 3 ? 5 : 1)
+              *reinterpret_cast<uint4 *>((q < 8 ? zt : sm + kSmY + 2 * st * kTile + ((q >> 3) - 1) * kTile) +
+                                         sw128_off(i, 8 * (q & 7))) = make_uint4(0, 0, 0, 0);
+        }
+        // gamma^(rows-1-j), reversed gamma^(j+1)
+        const float w = mine ? tab[p.reverse ? (i == 127 ? 255 : 126 - i) : 126 + rows - i] : 0.f;
+        const uint64_t ww = pair(w, w), minus = pair(-1.f, -1.f);
+        uint4 hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hi[e] = *reinterpret_cast<const uint4 *>(zt + sw128_off(i, 8 * (4 * half + e)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float f[8], f2[8];
+          unpack8(hi[e], f);
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) mul2(f + c, f + c, ww);
+          hi[e] = pack8(f);
+          unpack8(hi[e], f2);
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) fma2(f + c, f2 + c, minus, f + c);
+          lo[e] = pack8(f);
+        }
+        // the buffer itself is free once the dS before has been formed
+        ok = n == 0 || wait_group(d_full, n - 1);
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          *reinterpret_cast<uint4 *>(wt + sw128_off(i, 8 * (4 * half + e))) = hi[e];
+          *reinterpret_cast<uint4 *>(wt + kTile + sw128_off(i, 8 * (4 * half + e))) = lo[e];
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_ready[st]);
       }
-      const float w = mine ? pw[p.reverse ? i + 1 : rows - 1 - i] : 0.f;
-      const uint64_t ww = pair(w, w), minus = pair(-1.f, -1.f);
-      uint4 hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) hi[e] = *reinterpret_cast<const uint4 *>(zt + sw128_off(i, 8 * (4 * half + e)));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float f[8], f2[8];
-        unpack8(hi[e], f);
-#pragma unroll
-        for (int n = 0; n < 8; n += 2) mul2(f + n, f + n, ww);
-        hi[e] = pack8(f);
-        unpack8(hi[e], f2);
-#pragma unroll
-        for (int n = 0; n < 8; n += 2) fma2(f + n, f2 + n, minus, f + n);
-        lo[e] = pack8(f);
-      }
-      // the buffer itself is free once the dS before has been formed
-      if (j > 0 && !wait_group(d_full, j - 1)) break;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        *reinterpret_cast<uint4 *>(wt + sw128_off(i, 8 * (4 * half + e))) = hi[e];
-        *reinterpret_cast<uint4 *>(wt + kTile + sw128_off(i, 8 * (4 * half + e))) = lo[e];
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&w_ready[st]);
+      item_done(k);
     }
   } else {
     // ------------------------------------------------------------------- P
     const int half = (warp - 20) >> 2, i = wq * 32 + lane;
-    for (int j = 0; !STATE && j < chunks; ++j) {
-      const int cc = chunk_at(j), st = j & 1, rows = min(kN, t1 - t0 - cc * kN);
-      if (!wait_group(&sc_full[st], j >> 1)) break;
-      tc_fence_after();
-      // blocks of 32 columns against the warp's 32 rows
+    bool ok = !STATE;
+    for (int k = 0, n = 0, m = 0; ok && wait_group(LA_ITEM_FULL(k)); ++k) {
+      const int chunks = item_at(k).chunks;
+      if (chunks < 0) break;
+      const float *tab = tables + 256 * (m & 1) + 127 + i;
+      if (chunks > 0 && !wait_group(&t_full[m & 1], m >> 1)) break;
+      for (int j = 0; j < chunks; ++j, ++n) {
+        const int st = n & 1;
+        ok = wait_group(&sc_full[st], n >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        // blocks of 32 columns against the warp's 32 rows
 #pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        const int kb = half ? 1 + k : 3 * k, j0 = 32 * kb;  // half 0: the first and the last block
-        const uint32_t sc = tl + kColSc + 128 * st + j0, pt = tl + kColSc + 128 * st + 32 * half + 16 * k;
-        float f[32];
-        if (p.reverse ? kb < wq : kb > wq) {  // nothing of the block is seen
+        for (int c = 0; c < 2; ++c) {
+          const int kb = half ? 1 + c : 3 * c, j0 = 32 * kb;  // half 0: the first and the last block
+          const uint32_t sc = tl + kColSc + 128 * st + j0, pt = tl + kColSc + 128 * st + 32 * half + 16 * c;
+          float f[32];
+          if (p.reverse ? kb < wq : kb > wq) {  // nothing of the block is seen
 #pragma unroll
-          for (int n = 0; n < 16; ++n) f[n] = 0.f;
-        } else {
-          tmem_ld32(sc, f);
-          tmem_wait_ld();
-          const float *e = pij + 127 + i - j0;
+            for (int e = 0; e < 16; ++e) f[e] = 0.f;
+          } else {
+            tmem_ld32(sc, f);
+            tmem_wait_ld();
+            const float *at = tab - j0;
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            mul2(f + 2 * n, f + 2 * n, pair(e[-2 * n], e[-2 * n - 1]));
-            f[n] = __uint_as_float(pack_bf16(f[2 * n], f[2 * n + 1]));
+            for (int e = 0; e < 16; ++e) {
+              mul2(f + 2 * e, f + 2 * e, pair(at[-2 * e], at[-2 * e - 1]));
+              f[e] = __uint_as_float(pack_bf16(f[2 * e], f[2 * e + 1]));
+            }
           }
+          tmem_st16(pt, f);
         }
-        tmem_st16(pt, f);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[st]);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_ready[st]);
+      if (chunks > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t_free[m & 1]);
+        ++m;
+      }
+      item_done(k);
     }
   }
+#undef LA_ITEM_FULL
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -620,7 +758,7 @@ cudaError_t launch_as(const PackedPass &p, const Segments &sg, const Maps &m, cu
   auto kernel = packed_tc_kernel<DA, STATE, OF32>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmBytes);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(sg.units) * p.H * (p.db / 64);
+  const int grid = std::min(sg.items, std::max(1, sm_count()));
   kernel<<<grid, kThreads, kSmBytes, stream>>>(p, sg, m.x, m.y, m.z, m.o);
   return cudaGetLastError();
 }
@@ -663,32 +801,45 @@ int launch_packed_tc(const PackedPass &p, cudaStream_t stream) {
   const long long sms = std::max(1, sm_count());
   const int longest = p.max_len > 0 ? std::min(p.max_len, p.total) : p.total;
   const long long share = ((long long)p.total * p.H * (p.db / 64) + sms - 1) / sms;  // tokens of a CTA
-  Segments sg = {0, p.n_seq, nullptr, nullptr};
+  Segments sg = {0, p.n_seq, 0, nullptr, nullptr, nullptr};
   if (longest > 2 * kN && longest > share + share / 2) {
     long long seg = (share + kN - 1) / kN * kN;
     seg = std::max<long long>(seg, 2 * kN);
-    if (seg < longest) sg = {static_cast<int>(seg), static_cast<int>(p.total / seg) + p.n_seq, nullptr, nullptr};
+    if (seg < longest) {
+      sg.tokens = static_cast<int>(seg);
+      sg.units = static_cast<int>(p.total / seg) + p.n_seq;
+    }
   }
-  const long long ctas = (long long)sg.units * p.H * (p.db / 64);
-  if (ctas > INT_MAX) {
+  const long long items = (long long)sg.units * p.H * (p.db / 64);
+  if (items > INT_MAX / 2) {
     set_error("packed retention: n_seq * H too large");
     return LA_ERR_INVALID_ARG;
   }
-  float *ws = nullptr;
+  sg.items = static_cast<int>(items);
+  // workspace: a queue for each of the two kernels, then the segments' states
+  uint8_t *ws = nullptr;
   cudaError_t e = cudaSuccess;
-  if (sg.tokens) {
+  const size_t head = 256, states = sg.tokens ? (size_t)sg.units * p.H * p.sized * 4 : 0;
+  if (items > sms || sg.tokens) {
     cudaMemPool_t pool = library_pool();
     if (!pool) return fail("could not create the workspace pool", cudaGetLastError());
-    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), (size_t)sg.units * p.H * p.sized * 4, pool, stream);
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), head + states, pool, stream);
     if (e != cudaSuccess) return fail("workspace allocation failed", e);
-    sg.out = ws;
+    e = cudaMemsetAsync(ws, 0, 8, stream);
+  }
+  unsigned *queue = reinterpret_cast<unsigned *>(ws);
+  if (e == cudaSuccess && sg.tokens) {
+    sg.queue = queue;
+    sg.out = reinterpret_cast<float *>(ws + head);
     e = launch<true>(p, sg, m, stream);
     if (e == cudaSuccess) {
-      segment_scan_kernel<<<dim3(p.n_seq, p.H, (p.sized / 4 + 255) / 256), 256, 0, stream>>>(p, sg.tokens, sg.units, ws);
+      segment_scan_kernel<<<dim3(p.n_seq, p.H, (p.sized / 4 + 255) / 256), 256, 0, stream>>>(p, sg.tokens, sg.units,
+                                                                                             sg.out);
       e = cudaGetLastError();
     }
-    sg.in = ws;
+    sg.in = sg.out;
   }
+  sg.queue = queue ? queue + 1 : nullptr;
   if (e == cudaSuccess) e = launch<false>(p, sg, m, stream);
   if (ws) {
     const cudaError_t f = cudaFreeAsync(ws, stream);
