@@ -14,12 +14,12 @@
 //
 // Work. A unit is one segment (up to seg tokens) of one sequence; an item of
 // work is a unit, a head and 64 value columns. One CTA a SM takes items from a
-// queue, and the roles below go from one item's last chunk to the next one's
-// first without draining. Sequences longer than the segment first
+// queue, the longest first, and the roles below go from one item's last chunk to
+// the next one's first without draining. Sequences longer than the segment first
 // go through the same kernel with STATE set, which only forms each segment's
 // own contribution to the state, and a scan over the segments. Unit u of
 // sequence s are the numbers from floor(cu[s]/seg) + s on: enough for its
-// segments, increasing in s, and known without a table.
+// segments, and increasing in s.
 //
 // The state stays in registers: every chunk's dS is formed in a TMEM tile of
 // its own and added by float32 FMAs, gamma^n - 1 carrying the decay. Adding in
@@ -31,22 +31,24 @@
 // errors are of the order of the output's own rounding.
 //
 // Out-of-sequence rows: a tile may reach into the next sequence or behind the
-// last token. The foreign rows of Y and Z are cleared in shared memory before
-// they are multiplied, so that whatever they hold (NaN included) stays out;
-// foreign rows of X reach only output rows that are not written.
+// last token. The foreign rows of Z, and of Y once its scores are formed, are
+// cleared in shared memory, and the foreign columns of the scores dropped by
+// selection, so that whatever they hold (NaN included) stays out; foreign rows
+// of X reach only output rows that are not written.
 //
 // Roles, 896 threads. Every group works on its own part of a chunk and hands it
 // on through mbarriers, up to two chunks apart; a group of its own for each
 // step, because the steps are bound by their instructions' latency:
-//   warp 0        the queue, and TMA loads of X, Y, Z, two stages
+//   warp 0        the queue, tables of powers, TMA loads of X, Y, Z, two stages
 //   warps 1-3     MMAs: dS and X S; scores (and TMEM); P Z
 //   warps 4-7     state: S <- gamma^n S + dS, its bf16 copy
 //   warps 8-11    output: gamma^(i+1) X S + P Z, to memory by TMA
-//   warps 12-19   the tables of powers; Z' high and low
+//   warps 12-19   Z' high and low
 //   warps 20-27   P, in TMEM over its scores
 // Every wait is bounded; on expiry the CTA raises the status word, all roles
 // leave, copies and MMAs in flight are drained and TMEM is released.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "la_f32x2.cuh"
@@ -70,71 +72,102 @@ constexpr uint32_t kSpin = 1u << 22;     // polls before a wait gives up (tens o
 constexpr int kRegsIssue = 56, kRegsState = 104, kRegsOut = 88, kRegsP = 72, kRegsZ = 56;
 static_assert(kRegsIssue + kRegsState + kRegsOut + 2 * kRegsP + 2 * kRegsZ <= 7 * 72, "register split");
 
-struct Segments {
-  int tokens;       // of a segment; 0: every sequence is one unit
-  int units;        // sequences, or the numbers units may have
-  int items;        // units * heads * tiles of 64 value columns
-  unsigned *queue;  // next item for a CTA that is done, from zero; null: one item a CTA
-  const float *in;  // [unit][H][dk][dv] entering states, or null: S_in by slot
-  float *out;       // STATE: the segments' own contributions
+// A unit as the plan writes it: tokens [t0, t1), its number, and 2 * state row + (the state
+// behind it is its sequence's last); state row -1: none.
+struct Unit {
+  int t0, t1, u, row;
 };
 
-// One item of work, decoded by warp 0 for all roles. chunks < 0: no more items.
+struct Segments {
+  int tokens;        // of a segment; 0: every sequence is one unit
+  int units;         // sequences, or the numbers units may have
+  const Unit *plan;  // units with something to do, the longest first, or null: unit u is sequence u, one item a CTA
+  const int *count;  // how many
+  unsigned *queue;   // next item for a CTA that is done, from zero
+  const float *in;   // [unit][H][dk][dv] entering states, or null: S_in by row
+  float *out;        // STATE: the segments' own contributions
+};
+
+// One item of work: a unit, a head and 64 value columns. chunks < 0: no more items.
 struct Item {
   int t0, t1, chunks, h, v0, u, slot, leaves;
 };
 
 // First unit number of sequence s.
 __device__ __forceinline__ int first_unit(const PackedPass &p, int seg, int s) {
-  return min(max(__ldg(p.cu + s), 0), p.total) / seg + s;
+  return seg ? min(max(__ldg(p.cu + s), 0), p.total) / seg + s : s;
 }
 
-// Item w, by a whole warp. False: its unit has nothing to do.
-template <bool STATE>
-__device__ __forceinline__ bool decode(const PackedPass &p, const Segments &sg, int w, int lane, Item &it) {
-  const int vtiles = p.db / 64;
-  it.v0 = w % vtiles * 64;
-  it.h = w / vtiles % p.H;
-  it.u = w / vtiles / p.H;
-  int s = it.u, a, b;
-  if (sg.tokens) {  // the last sequence whose first unit is at most u: 32 at a time
-    int lo = -1, hi = p.n_seq;
-    while (hi - lo > 1) {
-      const int step = (hi - lo - 1 + 31) / 32, i = lo + 1 + lane * step;
-      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && first_unit(p, sg.tokens, i) <= it.u));
-      const int base = lo + 1;
-      if (n > 0) lo = base + (n - 1) * step;
-      hi = min(hi, base + n * step);
+__device__ __forceinline__ int chunks_of(int tokens) { return (tokens + kN - 1) / kN; }
+
+// Where a long walk is left for the end the other SMs wait for it: the plan
+// lists the units from the longest down (a counting sort over their chunks; the
+// order of equal ones is arbitrary, and no result goes by it). One CTA; clears
+// the queues on the way.
+constexpr int kPlanThreads = 1024, kBuckets = 1024;
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedPass p, int seg, int units, unsigned *head,
+                                                            int *owner, Unit *plan) {
+  __shared__ int first[kBuckets];
+  __shared__ int warp_sum[32];
+  const int tid = threadIdx.x;
+  if (tid < 2) head[tid] = 0;
+  first[tid] = 0;
+  const bool rows = p.S_in || p.S_out;
+  if (rows && p.slots) {  // of sequences that name the same row the first one has it
+    for (int i = tid; i < p.n_seq; i += kPlanThreads) {
+      const int slot = __ldg(p.slots + i);
+      if (slot >= 0 && slot < p.n_slots) owner[slot] = INT_MAX;
     }
-    if (lo < 0) return false;
-    s = lo;
-  }
-  packed_range(p.cu, s, p.total, &a, &b);
-  it.t0 = a;
-  it.t1 = b;
-  if (sg.tokens) {
-    const long long from = (long long)(it.u - first_unit(p, sg.tokens, s)) * sg.tokens;
-    if (from < 0 || (from > 0 && from >= b - a)) return false;
-    it.t0 = a + static_cast<int>(from);
-    it.t1 = min(b, it.t0 + sg.tokens);
-  }
-  it.chunks = (it.t1 - it.t0 + kN - 1) / kN;
-  it.leaves = p.reverse ? it.t0 == a : it.t1 == b;  // the state behind the unit is the sequence's last
-  if (STATE) return !it.leaves;
-  // the state row, or -1: without one, outside the pool, or taken by an earlier sequence
-  it.slot = -1;
-  if ((p.S_in && !sg.in) || (p.S_out && it.leaves)) {
-    int slot = p.slots ? __ldg(p.slots + s) : s;
-    if (slot < 0 || slot >= p.n_slots) slot = -1;
-    if (p.slots && slot >= 0) {
-      int taken = 0;
-#pragma unroll 4
-      for (int j = lane; j < s; j += 32) taken |= __ldg(p.slots + j) == slot;
-      if (__any_sync(0xffffffffu, taken)) slot = -1;
+    __syncthreads();
+    for (int i = tid; i < p.n_seq; i += kPlanThreads) {
+      const int slot = __ldg(p.slots + i);
+      if (slot >= 0 && slot < p.n_slots) atomicMin(owner + slot, i);
     }
-    it.slot = slot;
   }
-  return it.chunks > 0 || (p.S_out && it.slot >= 0);
+  __syncthreads();
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int i = tid; i < p.n_seq; i += kPlanThreads) {
+      int a, b;
+      packed_range(p.cu, i, p.total, &a, &b);
+      const int n = seg ? max(1, (b - a + seg - 1) / seg) : 1, u0 = first_unit(p, seg, i);
+      int row = -1;
+      if (rows) {
+        row = p.slots ? __ldg(p.slots + i) : i;
+        if (row < 0 || row >= p.n_slots || (p.slots && *const_cast<volatile int *>(owner + row) != i)) row = -1;
+      }
+      if (b == a && !(p.S_out && row >= 0)) continue;  // nothing to do
+      if (u0 + n > units) continue;                    // only where cu_seqlens is not what it should be
+      for (int k = 0; k < n; ++k) {
+        const int t0 = a + k * seg, t1 = seg ? min(b, t0 + seg) : b;
+        const int bucket = kBuckets - 1 - min(chunks_of(t1 - t0), kBuckets - 1);
+        const int at = atomicAdd(first + bucket, 1);
+        if (pass) plan[at] = {t0, t1, u0 + k, 2 * row + (p.reverse ? k == 0 : k == n - 1)};
+      }
+    }
+    __syncthreads();
+    if (pass) break;
+    // exclusive prefix sums of the buckets
+    int v = first[tid], x = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if ((tid & 31) >= o) x += y;
+    }
+    if ((tid & 31) == 31) warp_sum[tid >> 5] = x;
+    __syncthreads();
+    if (tid < 32) {
+      int y = warp_sum[tid];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (tid >= o) y += z;
+      }
+      warp_sum[tid] = y;
+    }
+    __syncthreads();
+    x += tid >= 32 ? warp_sum[(tid >> 5) - 1] : 0;
+    first[tid] = x - v;
+    if (tid == kPlanThreads - 1) head[2] = x;
+    __syncthreads();
+  }
 }
 
 // Shared memory, in 16 KB tiles (128 rows of 64 bf16, 128-byte swizzle).
@@ -142,7 +175,7 @@ constexpr uint32_t kTile = 16384;
 constexpr uint32_t kSmX = 0, kSmY = kSmX + 4 * kTile, kSmZ = kSmY + 4 * kTile, kSmW = kSmZ + 2 * kTile,
                    kSmS = kSmW + 2 * kTile, kSmO = kSmS + kTile, kSmMisc = kSmO + kTile,
                    kSmBytes = kSmMisc + 3072;
-constexpr int kRing = 4;  // items decoded ahead
+constexpr int kRing = 4;  // items known ahead
 // TMEM columns: two buffers of scores, over which go P (columns 0..63) and P Z (64..127),
 // two of X S, and dS of Z' high and low.
 constexpr uint32_t kColSc = 0, kColPZ = 64, kColXS = 256, kColD = 384;
@@ -209,8 +242,8 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       mbar_init(&w_ready[i], 8);
       mbar_init(&o_full[i], 2);  // X S, P Z
       mbar_init(&o_free[i], 4);
-      mbar_init(&t_full[i], 8);
-      mbar_init(&t_free[i], 12);  // output and P
+      mbar_init(&t_full[i], 1);
+      mbar_init(&t_free[i], STATE ? 8 : 20);  // Z' (output, P)
     }
     mbar_init(d_full, 1);
     mbar_init(d_free, 4);
@@ -272,22 +305,67 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
         prefetch_tmap(&tm_z);
         if (!STATE) prefetch_tmap(&tm_x);
       }
-      const int vtiles = db / 64;
-      int n = 0;
+      const int vtiles = db / 64, per = vtiles * p.H;
+      const int items = sg.plan ? *sg.count * per : gridDim.x;
+      int n = 0, m = 0;
       bool ok = true;
-      for (int k = 0, w = blockIdx.x; ok; ++k) {
+      int w = blockIdx.x;
+      Unit un = {};
+      if (sg.plan && w < items) un = sg.plan[w / per];
+      auto advance = [&] {  // the item after this one, by lane 0
+        w = INT_MAX;
+        if (sg.plan) {
+          w = gridDim.x + static_cast<int>(atomicAdd(sg.queue, 1u));
+          if (w < items) un = sg.plan[w / per];
+        }
+      };
+      auto share = [&] {
+        w = __shfl_sync(0xffffffffu, w, 0);
+        un.t0 = __shfl_sync(0xffffffffu, un.t0, 0);
+        un.t1 = __shfl_sync(0xffffffffu, un.t1, 0);
+        un.u = __shfl_sync(0xffffffffu, un.u, 0);
+        un.row = __shfl_sync(0xffffffffu, un.row, 0);
+      };
+      for (int k = 0; ok; ++k) {
+        // a sequence's last state is not needed from the state kernel: the main one forms it
+        while (STATE && w < items && (un.row & 1)) {
+          if (lane == 0) advance();
+          share();
+        }
         Item it;
-        bool found = false;
-        while (!found && w < sg.items) {
-          found = decode<STATE>(p, sg, w, lane, it);
-          // the item after this one
-          unsigned next = INT_MAX;
-          if (sg.queue && lane == 0) next = gridDim.x + atomicAdd(sg.queue, 1u);
-          w = static_cast<int>(__shfl_sync(0xffffffffu, next, 0));
+        bool found = w < items;
+        if (found) {
+          if (!sg.plan) {  // the only item of this CTA
+            const int u = w / per;
+            packed_range(p.cu, u, p.total, &un.t0, &un.t1);
+            int slot = -1;
+            if (p.S_in || p.S_out) {
+              slot = p.slots ? __ldg(p.slots + u) : u;
+              if (slot < 0 || slot >= p.n_slots) slot = -1;
+              int taken = 0;
+              if (p.slots && slot >= 0)
+                for (int j = lane; j < u; j += 32) taken |= __ldg(p.slots + j) == slot;
+              if (__any_sync(0xffffffffu, taken)) slot = -1;
+            }
+            un.u = u;
+            un.row = 2 * slot + 1;
+          }
+          it.t0 = un.t0;
+          it.t1 = un.t1;
+          it.chunks = chunks_of(un.t1 - un.t0);
+          it.v0 = w % vtiles * 64;
+          it.h = w / vtiles % p.H;
+          it.u = un.u;
+          it.slot = un.row >> 1;
+          it.leaves = un.row & 1;
         }
         if (!found) it.chunks = -1;
         int go = 1;
         if (lane == 0) {
+          // the state that the item starts from, into L2: its reader comes to it between two items
+          if (found && !STATE && (sg.in || (p.S_in && it.slot >= 0)) && it.v0 == 0)
+            bulk_prefetch_l2((sg.in ? sg.in + (size_t)it.u * p.H * p.sized : p.S_in + (size_t)it.slot * p.H * p.sized) +
+                                 (size_t)it.h * p.sized, p.sized * 4);
           go = wait(&e_free[k & (kRing - 1)], k / kRing ^ 1);
           if (go) {
             ring[k & (kRing - 1)] = it;
@@ -295,6 +373,20 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
           }
         }
         ok = __shfl_sync(0xffffffffu, go, 0) && found;
+        if (ok && it.chunks > 0) {  // the table of the item's head
+          if (lane == 0) go = wait(&t_free[m & 1], (m >> 1) ^ 1);
+          ok = __shfl_sync(0xffffffffu, go, 0);
+          if (!ok) break;
+          const float g = p.g ? __ldg(p.g + it.h) : 0.f;
+#pragma unroll 4
+          for (int at = lane; at < 256; at += 32) {
+            const int e = at == 255 ? kN : p.reverse ? 127 - at : at - 127;
+            tables[256 * (m & 1) + at] = e >= 0 ? decay_power(g, e) : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&t_full[m & 1]);
+          ++m;
+        }
         if (lane == 0 && ok) {
           const int xh = it.h / p.rx, yh = it.h / p.ry, zh = it.h / p.rz, first = n;
           for (; n < first + it.chunks; ++n) {
@@ -314,6 +406,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
               tma_load_3d(sm + kSmY + (2 * st + c) * kTile, &tm_y, &xy_full[st], 64 * c, yh, t);
               if (!STATE) tma_load_3d(sm + kSmX + (2 * st + c) * kTile, &tm_x, &xy_full[st], 64 * c, xh, t);
             }
+            if (j == 0) advance();  // under the first chunk's loads
             // the chunk after the next into L2; its loads wait for this chunk's products. X and Y
             // are read by both CTAs of a head of 128 value columns: one of them asks for each
             if (j + 2 < it.chunks) {
@@ -327,14 +420,15 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
             }
           }
         }
-        __syncwarp();
+        if (lane == 0 && ok && it.chunks == 0) advance();
+        share();
       }
       // given up: copies still in flight must land before the CTA's memory is released
       // (a barrier that was never armed in its last phase just runs out its wait)
       if (lane == 0 && *abort_flag)
-        for (int m = n; m >= 0 && m >= n - 2; --m) {
-          (void)mbar_wait_bounded(&xy_full[m & 1], (m >> 1) & 1, 1u << 16);
-          (void)mbar_wait_bounded(&z_full[m & 1], (m >> 1) & 1, 1u << 16);
+        for (int i = n; i >= 0 && i >= n - 2; --i) {
+          (void)mbar_wait_bounded(&xy_full[i & 1], (i >> 1) & 1, 1u << 16);
+          (void)mbar_wait_bounded(&z_full[i & 1], (i >> 1) & 1, 1u << 16);
         }
     } else if (!STATE && warp == 2 && lane == 0) {
       // -------------------------------------------------------- MMAs: scores
@@ -342,13 +436,12 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       const uint32_t dx = smem_u32(sm + kSmX), dy = smem_u32(sm + kSmY);
       bool ok = true;
       for (int k = 0, n = 0; ok && wait(LA_ITEM_FULL(k)); ++k) {
-        const Item it = item_at(k);
-        if (it.chunks < 0) break;
-        for (int j = 0; j < it.chunks; ++j, ++n) {
+        const int chunks = item_at(k).chunks;
+        if (chunks < 0) break;
+        for (int j = 0; j < chunks; ++j, ++n) {
           const int st = n & 1;
           const uint32_t stage = 2 * st * kTile;
-          const bool tail = it.t1 - it.t0 < (chunk_at(it, j) + 1) * kN;  // foreign rows of Y are cleared behind Z'
-          ok = wait(&xy_full[st], n >> 1) && (!tail || wait(&w_ready[st], n >> 1)) && wait(&o_free[st], (n >> 1) ^ 1);
+          ok = wait(&xy_full[st], n >> 1) && wait(&o_free[st], (n >> 1) ^ 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 4
@@ -574,7 +667,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
     }
     if (!STATE && lane == 0) bulk_wait<0>();
   } else if (warp < 20) {
-    // ----------------------------------------- tables, and Z' high and low
+    // -------------------------------------------------------- Z' high and low
     regs_down<kRegsZ>();
     const int half = (warp - 12) >> 2, i = wq * 32 + lane;  // columns 32*half .. of row i
     bool ok = true;
@@ -583,14 +676,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       if (it.chunks < 0) break;
       const float *tab = tables + 256 * (m & 1);
       if (it.chunks > 0) {
-        if (!STATE && !wait_group(&t_free[m & 1], (m >> 1) ^ 1)) break;
-        const float g = p.g ? __ldg(p.g + it.h) : 0.f;
-        const int at = half * 128 + i, e = at == 255 ? kN : p.reverse ? 127 - at : at - 127;
-        tables[256 * (m & 1) + at] = e >= 0 ? decay_power(g, e) : 0.f;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&t_full[m & 1]);
         if (!wait_group(&t_full[m & 1], m >> 1)) break;
-        ++m;
       }
       for (int j = 0; j < it.chunks; ++j, ++n) {
         const int cc = chunk_at(it, j), st = n & 1, rows = min(kN, it.t1 - it.t0 - cc * kN);
@@ -599,7 +685,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
         if (!ok) break;
         uint8_t *zt = sm + kSmZ + st * kTile, *wt = sm + kSmW;
         if (rows < kN) {  // foreign rows of Y and Z
-          ok = wait_group(&xy_full[st], n >> 1);
+          ok = wait_group(&xy_full[st], n >> 1) && (STATE || wait_group(&sc_full[st], n >> 1));  // Y's scores are formed
           if (!ok) break;
           if (!mine)
 #pragma unroll 1
@@ -637,6 +723,11 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
         __syncwarp();
         if (lane == 0) mbar_arrive(&w_ready[st]);
       }
+      if (it.chunks > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t_free[m & 1]);
+        ++m;
+      }
       item_done(k);
     }
   } else {
@@ -644,12 +735,13 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
     const int half = (warp - 20) >> 2, i = wq * 32 + lane;
     bool ok = !STATE;
     for (int k = 0, n = 0, m = 0; ok && wait_group(LA_ITEM_FULL(k)); ++k) {
-      const int chunks = item_at(k).chunks;
+      const Item it = item_at(k);
+      const int chunks = it.chunks;
       if (chunks < 0) break;
       const float *tab = tables + 256 * (m & 1) + 127 + i;
       if (chunks > 0 && !wait_group(&t_full[m & 1], m >> 1)) break;
       for (int j = 0; j < chunks; ++j, ++n) {
-        const int st = n & 1;
+        const int st = n & 1, rows = it.t1 - it.t0 - chunk_at(it, j) * kN;
         ok = wait_group(&sc_full[st], n >> 1);
         if (!ok) break;
         tc_fence_after();
@@ -667,8 +759,13 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
             tmem_wait_ld();
             const float *at = tab - j0;
 #pragma unroll
+            for (int e = 0; e < 16; ++e) mul2(f + 2 * e, f + 2 * e, pair(at[-2 * e], at[-2 * e - 1]));
+            if (j0 + 32 > rows) {  // foreign columns, by selection: their scores may be anything
+#pragma unroll
+              for (int e = 0; e < 32; ++e) f[e] = j0 + e < rows ? f[e] : 0.f;
+            }
+#pragma unroll
             for (int e = 0; e < 16; ++e) {
-              mul2(f + 2 * e, f + 2 * e, pair(at[-2 * e], at[-2 * e - 1]));
               f[e] = __uint_as_float(pack_bf16(f[2 * e], f[2 * e + 1]));
             }
           }
@@ -749,6 +846,9 @@ bool make_token_map(CUtensorMap *m, const void *base, int d, int heads, int toke
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr double kSplitCost = 1.6;   // a split pass against an unsplit one of the same tokens a CTA
+constexpr int kSplitTokens = 12 * kN;  // what its further launches cost, in tokens of a walk
+
 struct Maps {
   CUtensorMap x, y, z, o;
 };
@@ -756,9 +856,18 @@ struct Maps {
 template <int DA, bool STATE, bool OF32>
 cudaError_t launch_as(const PackedPass &p, const Segments &sg, const Maps &m, cudaStream_t stream) {
   auto kernel = packed_tc_kernel<DA, STATE, OF32>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmBytes);
+  // once for each device
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(sg.items, std::max(1, sm_count()));
+  if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
+  }
+  const long long items = (long long)sg.units * p.H * (p.db / 64);
+  const int grid = static_cast<int>(std::min<long long>(items, std::max(1, sm_count())));
   kernel<<<grid, kThreads, kSmBytes, stream>>>(p, sg, m.x, m.y, m.z, m.o);
   return cudaGetLastError();
 }
@@ -795,16 +904,16 @@ int launch_packed_tc(const PackedPass &p, cudaStream_t stream) {
     set_error("packed retention: tensor map encoding failed");
     return LA_ERR_CUDA;
   }
-  // Sequences are split into segments where whole ones would leave the GPU to
-  // a few long walks: the second reading of Y and Z, and the states' way through
-  // memory, cost about 0.4 of a pass.
+  // Sequences are split into segments where whole ones would leave the GPU to a
+  // few long walks. Unsplit the pass takes as long as its longest sequence; split
+  // it takes its share of the whole, and on top the second reading of Y and Z,
+  // the states' way through memory and two more launches.
   const long long sms = std::max(1, sm_count());
   const int longest = p.max_len > 0 ? std::min(p.max_len, p.total) : p.total;
   const long long share = ((long long)p.total * p.H * (p.db / 64) + sms - 1) / sms;  // tokens of a CTA
-  Segments sg = {0, p.n_seq, 0, nullptr, nullptr, nullptr};
-  if (longest > 2 * kN && longest > share + share / 2) {
-    long long seg = (share + kN - 1) / kN * kN;
-    seg = std::max<long long>(seg, 2 * kN);
+  Segments sg = {0, p.n_seq, nullptr, nullptr, nullptr, nullptr, nullptr};
+  if (longest > kSplitCost * share + kSplitTokens) {
+    const long long seg = std::max<long long>((share + kN - 1) / kN * kN, 2 * kN);
     if (seg < longest) {
       sg.tokens = static_cast<int>(seg);
       sg.units = static_cast<int>(p.total / seg) + p.n_seq;
@@ -815,31 +924,37 @@ int launch_packed_tc(const PackedPass &p, cudaStream_t stream) {
     set_error("packed retention: n_seq * H too large");
     return LA_ERR_INVALID_ARG;
   }
-  sg.items = static_cast<int>(items);
-  // workspace: a queue for each of the two kernels, then the segments' states
+  // workspace: the plan's counters, the owners of the state rows, the plan, the segments' states
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const size_t owners = up(p.slots && (p.S_in || p.S_out) ? (size_t)p.n_slots * 4 : 0),
+               plan = up((size_t)sg.units * sizeof(Unit)),
+               states = sg.tokens ? (size_t)sg.units * p.H * p.sized * 4 : 0;
   uint8_t *ws = nullptr;
   cudaError_t e = cudaSuccess;
-  const size_t head = 256, states = sg.tokens ? (size_t)sg.units * p.H * p.sized * 4 : 0;
   if (items > sms || sg.tokens) {
     cudaMemPool_t pool = library_pool();
     if (!pool) return fail("could not create the workspace pool", cudaGetLastError());
-    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), head + states, pool, stream);
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), 256 + owners + plan + states, pool, stream);
     if (e != cudaSuccess) return fail("workspace allocation failed", e);
-    e = cudaMemsetAsync(ws, 0, 8, stream);
-  }
-  unsigned *queue = reinterpret_cast<unsigned *>(ws);
-  if (e == cudaSuccess && sg.tokens) {
-    sg.queue = queue;
-    sg.out = reinterpret_cast<float *>(ws + head);
-    e = launch<true>(p, sg, m, stream);
-    if (e == cudaSuccess) {
-      segment_scan_kernel<<<dim3(p.n_seq, p.H, (p.sized / 4 + 255) / 256), 256, 0, stream>>>(p, sg.tokens, sg.units,
-                                                                                             sg.out);
-      e = cudaGetLastError();
+    unsigned *head = reinterpret_cast<unsigned *>(ws);
+    Unit *units = reinterpret_cast<Unit *>(ws + 256 + owners);
+    plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, sg.tokens, sg.units, head, reinterpret_cast<int *>(ws + 256), units);
+    e = cudaGetLastError();
+    sg.plan = units;
+    sg.count = reinterpret_cast<const int *>(head + 2);
+    sg.queue = head;
+    if (e == cudaSuccess && sg.tokens) {
+      sg.out = reinterpret_cast<float *>(ws + 256 + owners + plan);
+      e = launch<true>(p, sg, m, stream);
+      if (e == cudaSuccess) {
+        segment_scan_kernel<<<dim3(p.n_seq, p.H, (p.sized / 4 + 255) / 256), 256, 0, stream>>>(p, sg.tokens, sg.units,
+                                                                                               sg.out);
+        e = cudaGetLastError();
+      }
+      sg.in = sg.out;
     }
-    sg.in = sg.out;
+    sg.queue = head + 1;
   }
-  sg.queue = queue ? queue + 1 : nullptr;
   if (e == cudaSuccess) e = launch<false>(p, sg, m, stream);
   if (ws) {
     const cudaError_t f = cudaFreeAsync(ws, stream);
