@@ -213,6 +213,10 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
                  const __grid_constant__ CUtensorMap tm_o) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wq = warp & 3, group = warp >> 2;
+  if ((smem_u32(sm) & 1023u) != 0) {  // the tiles' swizzle goes by the address: not met, as there is no static part
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
   const int db = p.db;
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kSmMisc);
   uint64_t *xy_full = bars, *xy_free = bars + 2, *z_full = bars + 4, *z_free = bars + 6, *sc_full = bars + 8,
@@ -254,7 +258,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       mbar_init(&e_full[i], 1);
       mbar_init(&e_free[i], STATE ? 13 : 27);  // dS, state, Z' (scores, P Z, output, P)
     }
-    *abort_flag = (smem_u32(sm) & 1023u) != 0;  // the tiles' swizzle goes by the address: none of them may move
+    *abort_flag = 0;
     fence_mbar_init();
   }
   if (DA == 64) {  // channels 64..127 of Y: zero rows of dS
@@ -267,17 +271,26 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   const uint32_t tl = tbase + (static_cast<uint32_t>(wq * 32) << 16);
-  // The loop is as short as it can be (the status word is raised at the end): the code that all
-  // roles run for a chunk has to stay in the SM's instruction cache together. With the waits,
-  // products and conversions unrolled in place it did not, and a chunk took three times as long.
+  // The loop is as short as it can be: the code that all roles run for a chunk has to stay in the
+  // SM's instruction cache together. With the waits, products and conversions unrolled in place
+  // it did not, and a chunk took three times as long. A role whose wait runs out leaves, and the
+  // others run out after it.
   auto wait = [&](uint64_t *bar, uint32_t parity) {
-#pragma unroll 1
-    for (uint32_t i = 0; i < kSpin; ++i) {
-      if (mbar_try_wait(bar, parity & 1)) return true;
-      if (*abort_flag) return false;
-    }
-    *abort_flag = 1;
-    return false;
+    uint32_t left;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmov.u32 %0, %3;\n\t"
+        "LA_POLL:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra LA_DONE;\n\t"
+        "sub.u32 %0, %0, 1;\n\t"
+        "setp.ne.u32 p, %0, 0;\n\t"
+        "@p bra LA_POLL;\n\t"
+        "LA_DONE:\n\t}"
+        : "=&r"(left)
+        : "r"(smem_u32(bar)), "r"(parity & 1), "n"(kSpin)
+        : "memory");
+    if (left == 0) *abort_flag = 1;
+    return left != 0;
   };
   // A group of four warps waits: one lane polls, the others sleep on the group's barrier.
   // With a polling lane in each of 24 warps the polls took more issue slots than the work.
