@@ -50,8 +50,11 @@ int check_packing(const char *fn, const int *cu, const int *slots, int n_seq, in
 }
 
 // float32 and calls without a token go to the walk, bfloat16 to the tensor cores.
-int run_pass(const PackedPass &p, cudaStream_t stream) {
-  return p.f32 || p.total == 0 ? launch_packed_walk(p, stream) : launch_packed_tc(p, stream);
+int run_passes(const PackedPass *p, int passes, cudaStream_t stream) {
+  if (!p->f32 && p->total > 0) return launch_packed_tc(p, passes, stream);
+  int rc = LA_OK;
+  for (int i = 0; i < passes && rc == LA_OK; ++i) rc = launch_packed_walk(p[i], stream);
+  return rc;
 }
 
 }  // namespace
@@ -88,7 +91,7 @@ int la_packed_fwd(const void *q, const void *k, const void *v, const float *g, v
   p.cu = cu_seqlens; p.slots = slots; p.n_seq = n_seq; p.total = total; p.n_slots = n_slots; p.H = H;
   p.g = g; p.f32 = p.out_f32 = (mode & LA_F32) ? 1 : 0;
   p.status = status; p.max_len = max_len;
-  return run_pass(p, reinterpret_cast<cudaStream_t>(stream));
+  return run_passes(&p, 1, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, const void *dO,
@@ -122,7 +125,7 @@ int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, c
       set_error("%s: could not create the workspace pool: %s", fn, cudaGetErrorString(cudaGetLastError()));
       return LA_ERR_CUDA;
     }
-    const size_t bytes = (size_t)total * H * dk * 4;
+    const size_t bytes = (size_t)2 * total * H * dk * 4;  // of dq and dk
     const cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&parts), bytes, pool, s);
     if (e != cudaSuccess) {
       set_error("%s: workspace allocation of %zu bytes failed: %s", fn, bytes, cudaGetErrorString(e));
@@ -134,40 +137,33 @@ int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, c
   c.sized = dk * dv;
   c.cu = cu_seqlens; c.n_seq = n_seq; c.total = total; c.n_slots = n_seq; c.H = H;
   c.g = g; c.f32 = f32; c.status = status; c.max_len = max_len;
-  auto shared_out = [&](PackedPass &p, void *dst) {
-    p.out = parts ? parts : dst;
+  float *parts_of[2] = {parts, parts ? parts + (size_t)total * H * dk : nullptr};
+  auto shared_out = [&](PackedPass &p, int i, void *dst) {
+    p.out = parts ? parts_of[i] : dst;
     p.ldo = parts ? (long long)H * dk : (long long)Hk * dk;
     p.out_f32 = parts ? 1 : f32;
   };
-  PackedPass p = c;  // dq
-  p.x = dO; p.ldx = ldd; p.rx = 1;
-  p.y = v; p.ldy = ldv; p.ry = 1;
-  p.z = k; p.ldz = ldk; p.rz = share;
-  p.da = dv; p.db = dk; p.S_in = S0; p.in_t = 1;
-  shared_out(p, dq);
-  rc = run_pass(p, s);
-  if (rc == LA_OK && parts) rc = launch_head_sum(parts, dq, f32, total, Hk, share, dk, s);
-  if (rc == LA_OK) {
-    p = c;  // dk
-    p.reverse = 1;
-    p.x = v; p.ldx = ldv; p.rx = 1;
-    p.y = dO; p.ldy = ldd; p.ry = 1;
-    p.z = q; p.ldz = ldq; p.rz = share;
-    p.da = dv; p.db = dk; p.S_in = dS_final; p.in_t = 1;
-    shared_out(p, dk_out);
-    rc = run_pass(p, s);
-    if (rc == LA_OK && parts) rc = launch_head_sum(parts, dk_out, f32, total, Hk, share, dk, s);
-  }
-  if (rc == LA_OK) {
-    p = c;  // dv and dS0
-    p.reverse = 1;
-    p.x = k; p.ldx = ldk; p.rx = share;
-    p.y = q; p.ldy = ldq; p.ry = share;
-    p.z = dO; p.ldz = ldd; p.rz = 1;
-    p.da = dk; p.db = dv; p.S_in = dS_final; p.S_out = dS0;
-    p.out = dv_out; p.ldo = ldd; p.out_f32 = f32;
-    rc = run_pass(p, s);
-  }
+  PackedPass p[3] = {c, c, c};
+  p[0].x = dO; p[0].ldx = ldd; p[0].rx = 1;  // dq
+  p[0].y = v; p[0].ldy = ldv; p[0].ry = 1;
+  p[0].z = k; p[0].ldz = ldk; p[0].rz = share;
+  p[0].da = dv; p[0].db = dk; p[0].S_in = S0; p[0].in_t = 1;
+  shared_out(p[0], 0, dq);
+  p[1].reverse = 1;  // dk
+  p[1].x = v; p[1].ldx = ldv; p[1].rx = 1;
+  p[1].y = dO; p[1].ldy = ldd; p[1].ry = 1;
+  p[1].z = q; p[1].ldz = ldq; p[1].rz = share;
+  p[1].da = dv; p[1].db = dk; p[1].S_in = dS_final; p[1].in_t = 1;
+  shared_out(p[1], 1, dk_out);
+  p[2].reverse = 1;  // dv and dS0
+  p[2].x = k; p[2].ldx = ldk; p[2].rx = share;
+  p[2].y = q; p[2].ldy = ldq; p[2].ry = share;
+  p[2].z = dO; p[2].ldz = ldd; p[2].rz = 1;
+  p[2].da = dk; p[2].db = dv; p[2].S_in = dS_final; p[2].S_out = dS0;
+  p[2].out = dv_out; p[2].ldo = ldd; p[2].out_f32 = f32;
+  rc = run_passes(p, 3, s);
+  if (parts && rc == LA_OK) rc = launch_head_sum(parts_of[0], dq, f32, total, Hk, share, dk, s);
+  if (parts && rc == LA_OK) rc = launch_head_sum(parts_of[1], dk_out, f32, total, Hk, share, dk, s);
   if (parts) {
     const cudaError_t e = cudaFreeAsync(parts, s);
     if (rc == LA_OK && e != cudaSuccess) {

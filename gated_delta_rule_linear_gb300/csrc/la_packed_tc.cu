@@ -231,6 +231,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
   // factor of a score, zero where j is not seen from i.
   float *tables = reinterpret_cast<float *>(sm + kSmMisc + 1024);
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // see launch_packed_tc
   if (warp == 2) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -802,7 +803,11 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tbase, 512);
-  if (tid == 0 && *abort_flag) atomicOr(p.status, kStatusTimeout);
+  if (tid == 0) {
+    if (*abort_flag) atomicOr(p.status, kStatusTimeout);
+    // behind an independent pass that this one may have run beside: not done before it is
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
 }
 
 // The entering state of every segment from the segments' own contributions, in
@@ -859,15 +864,12 @@ bool make_token_map(CUtensorMap *m, const void *base, int d, int heads, int toke
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr double kSplitCost = 1.6;   // a split pass against an unsplit one of the same tokens a CTA
-constexpr int kSplitTokens = 12 * kN;  // what its further launches cost, in tokens of a walk
-
 struct Maps {
   CUtensorMap x, y, z, o;
 };
 
 template <int DA, bool STATE, bool OF32>
-cudaError_t launch_as(const PackedPass &p, const Segments &sg, const Maps &m, cudaStream_t stream) {
+cudaError_t launch_as(const PackedPass &p, const Segments &sg, const Maps &m, bool beside, cudaStream_t stream) {
   auto kernel = packed_tc_kernel<DA, STATE, OF32>;
   // once for each device
   static std::atomic<bool> done[64];
@@ -881,39 +883,54 @@ cudaError_t launch_as(const PackedPass &p, const Segments &sg, const Maps &m, cu
   }
   const long long items = (long long)sg.units * p.H * (p.db / 64);
   const int grid = static_cast<int>(std::min<long long>(items, std::max(1, sm_count())));
-  kernel<<<grid, kThreads, kSmBytes, stream>>>(p, sg, m.x, m.y, m.z, m.o);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmBytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, sg, m.x, m.y, m.z, m.o);
 }
 
 template <bool STATE>
-cudaError_t launch(const PackedPass &p, const Segments &sg, const Maps &m, cudaStream_t stream) {
+cudaError_t launch(const PackedPass &p, const Segments &sg, const Maps &m, bool beside, cudaStream_t stream) {
   if constexpr (!STATE)
     if (p.out_f32)
-      return p.da == 64 ? launch_as<64, false, true>(p, sg, m, stream) : launch_as<128, false, true>(p, sg, m, stream);
-  return p.da == 64 ? launch_as<64, STATE, false>(p, sg, m, stream) : launch_as<128, STATE, false>(p, sg, m, stream);
+      return p.da == 64 ? launch_as<64, false, true>(p, sg, m, beside, stream) : launch_as<128, false, true>(p, sg, m, beside, stream);
+  return p.da == 64 ? launch_as<64, STATE, false>(p, sg, m, beside, stream) : launch_as<128, STATE, false>(p, sg, m, beside, stream);
 }
+
+// A split pass against an unsplit one of as many tokens a CTA, and what its further launches cost in
+// tokens of a walk (24 ragged sequences of 12001 tokens, backward: 0.206 ms with 4 chunks, 0.218 with 12).
+constexpr double kSplitCost = 1.6;
+constexpr int kSplitTokens = 4 * kN;
 
 int fail(const char *what, cudaError_t e) {
   set_error("packed retention: %s: %s", what, cudaGetErrorString(e));
   return LA_ERR_CUDA;
 }
 
-}  // namespace
-
-int launch_packed_tc(const PackedPass &p, cudaStream_t stream) {
-  if (!encode_fn()) {
-    set_error("packed retention: cuTensorMapEncodeTiled is unavailable");
-    return LA_ERR_CUDA;
-  }
+// One pass with what it is launched with.
+struct Ready {
   Maps m;
-  if (!make_token_map(&m.x, p.x, p.da, p.H / p.rx, p.total, p.ldx, kN) ||
-      !make_token_map(&m.y, p.y, p.da, p.H / p.ry, p.total, p.ldy, kN) ||
-      !make_token_map(&m.z, p.z, p.db, p.H / p.rz, p.total, p.ldz, kN)) {
+  Segments sg;
+  size_t owners, plan, states;  // bytes of its workspace behind 256 of counters; plan 0: none
+};
+
+// Maps, split and workspace of a pass; an LA_ERR_* code where it cannot run.
+int make_ready(const PackedPass &p, Ready *r) {
+  if (!make_token_map(&r->m.x, p.x, p.da, p.H / p.rx, p.total, p.ldx, kN) ||
+      !make_token_map(&r->m.y, p.y, p.da, p.H / p.ry, p.total, p.ldy, kN) ||
+      !make_token_map(&r->m.z, p.z, p.db, p.H / p.rz, p.total, p.ldz, kN)) {
     set_error("packed retention: tensor map encoding failed");
     return LA_ERR_CUDA;
   }
-  m.o = m.x;
-  if (!p.out_f32 && !make_token_map(&m.o, p.out, p.db, p.H, p.total, p.ldo, 32)) {
+  r->m.o = r->m.x;
+  if (!p.out_f32 && !make_token_map(&r->m.o, p.out, p.db, p.H, p.total, p.ldo, 32)) {
     set_error("packed retention: tensor map encoding failed");
     return LA_ERR_CUDA;
   }
@@ -924,51 +941,86 @@ int launch_packed_tc(const PackedPass &p, cudaStream_t stream) {
   const long long sms = std::max(1, sm_count());
   const int longest = p.max_len > 0 ? std::min(p.max_len, p.total) : p.total;
   const long long share = ((long long)p.total * p.H * (p.db / 64) + sms - 1) / sms;  // tokens of a CTA
-  Segments sg = {0, p.n_seq, nullptr, nullptr, nullptr, nullptr, nullptr};
+  r->sg = {0, p.n_seq, nullptr, nullptr, nullptr, nullptr, nullptr};
   if (longest > kSplitCost * share + kSplitTokens) {
     const long long seg = std::max<long long>((share + kN - 1) / kN * kN, 2 * kN);
     if (seg < longest) {
-      sg.tokens = static_cast<int>(seg);
-      sg.units = static_cast<int>(p.total / seg) + p.n_seq;
+      r->sg.tokens = static_cast<int>(seg);
+      r->sg.units = static_cast<int>(p.total / seg) + p.n_seq;
     }
   }
-  const long long items = (long long)sg.units * p.H * (p.db / 64);
+  const long long items = (long long)r->sg.units * p.H * (p.db / 64);
   if (items > INT_MAX / 2) {
     set_error("packed retention: n_seq * H too large");
     return LA_ERR_INVALID_ARG;
   }
-  // workspace: the plan's counters, the owners of the state rows, the plan, the segments' states
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  const size_t owners = up(p.slots && (p.S_in || p.S_out) ? (size_t)p.n_slots * 4 : 0),
-               plan = up((size_t)sg.units * sizeof(Unit)),
-               states = sg.tokens ? (size_t)sg.units * p.H * p.sized * 4 : 0;
+  r->owners = r->plan = r->states = 0;
+  if (items > sms || r->sg.tokens) {
+    r->owners = up(p.slots && (p.S_in || p.S_out) ? (size_t)p.n_slots * 4 : 0);
+    r->plan = up((size_t)r->sg.units * sizeof(Unit));
+    r->states = r->sg.tokens ? (size_t)r->sg.units * p.H * p.sized * 4 : 0;
+  }
+  return LA_OK;
+}
+
+}  // namespace
+
+// The passes do not depend on each other. Each phase of all of them is launched
+// back to back, and the tensor-core kernels behind the first may begin before the
+// one in front of them is done (programmatic launch): the SMs that its queue has
+// no more work for take the next pass's, instead of waiting for its last items.
+int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream) {
+  if (!encode_fn()) {
+    set_error("packed retention: cuTensorMapEncodeTiled is unavailable");
+    return LA_ERR_CUDA;
+  }
+  Ready r[3];
+  size_t bytes = 0;
+  for (int i = 0; i < passes; ++i) {
+    const int rc = make_ready(p[i], &r[i]);
+    if (rc != LA_OK) return rc;
+    if (r[i].plan) bytes += 256 + r[i].owners + r[i].plan + r[i].states;
+  }
   uint8_t *ws = nullptr;
   cudaError_t e = cudaSuccess;
-  if (items > sms || sg.tokens) {
+  if (bytes) {
     cudaMemPool_t pool = library_pool();
     if (!pool) return fail("could not create the workspace pool", cudaGetLastError());
-    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), 256 + owners + plan + states, pool, stream);
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes, pool, stream);
     if (e != cudaSuccess) return fail("workspace allocation failed", e);
-    unsigned *head = reinterpret_cast<unsigned *>(ws);
-    Unit *units = reinterpret_cast<Unit *>(ws + 256 + owners);
-    plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, sg.tokens, sg.units, head, reinterpret_cast<int *>(ws + 256), units);
-    e = cudaGetLastError();
-    sg.plan = units;
-    sg.count = reinterpret_cast<const int *>(head + 2);
-    sg.queue = head;
-    if (e == cudaSuccess && sg.tokens) {
-      sg.out = reinterpret_cast<float *>(ws + 256 + owners + plan);
-      e = launch<true>(p, sg, m, stream);
-      if (e == cudaSuccess) {
-        segment_scan_kernel<<<dim3(p.n_seq, p.H, (p.sized / 4 + 255) / 256), 256, 0, stream>>>(p, sg.tokens, sg.units,
-                                                                                               sg.out);
-        e = cudaGetLastError();
-      }
-      sg.in = sg.out;
-    }
-    sg.queue = head + 1;
   }
-  if (e == cudaSuccess) e = launch<false>(p, sg, m, stream);
+  // counters, owners of the state rows, plan, segments' states of each pass
+  uint8_t *at = ws;
+  for (int i = 0; i < passes && e == cudaSuccess; ++i) {
+    if (!r[i].plan) continue;
+    unsigned *head = reinterpret_cast<unsigned *>(at);
+    Unit *plan = reinterpret_cast<Unit *>(at + 256 + r[i].owners);
+    plan_kernel<<<1, kPlanThreads, 0, stream>>>(p[i], r[i].sg.tokens, r[i].sg.units, head,
+                                                reinterpret_cast<int *>(at + 256), plan);
+    e = cudaGetLastError();
+    r[i].sg.plan = plan;
+    r[i].sg.count = reinterpret_cast<const int *>(head + 2);
+    r[i].sg.queue = head;
+    if (r[i].sg.tokens) r[i].sg.out = reinterpret_cast<float *>(at + 256 + r[i].owners + r[i].plan);
+    at += 256 + r[i].owners + r[i].plan + r[i].states;
+  }
+  bool beside = false;
+  for (int i = 0; i < passes && e == cudaSuccess; ++i) {
+    if (!r[i].sg.tokens) continue;
+    e = launch<true>(p[i], r[i].sg, r[i].m, beside, stream);
+    beside = true;
+  }
+  for (int i = 0; i < passes && e == cudaSuccess; ++i) {
+    if (r[i].sg.tokens) {
+      segment_scan_kernel<<<dim3(p[i].n_seq, p[i].H, (p[i].sized / 4 + 255) / 256), 256, 0, stream>>>(
+          p[i], r[i].sg.tokens, r[i].sg.units, r[i].sg.out);
+      e = cudaGetLastError();
+      r[i].sg.in = r[i].sg.out;
+    }
+    if (r[i].plan) ++r[i].sg.queue;  // the main kernel's own
+  }
+  for (int i = 0; i < passes && e == cudaSuccess; ++i) e = launch<false>(p[i], r[i].sg, r[i].m, i > 0, stream);
   if (ws) {
     const cudaError_t f = cudaFreeAsync(ws, stream);
     if (e == cudaSuccess) e = f;
