@@ -138,6 +138,7 @@ int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, c
   c.cu = cu_seqlens; c.n_seq = n_seq; c.total = total; c.n_slots = n_seq; c.H = H;
   c.g = g; c.f32 = f32; c.status = status; c.max_len = max_len;
   float *parts_of[2] = {parts, parts ? parts + (size_t)total * H * dk : nullptr};
+  void *summed[2] = {dq, dk_out};
   auto shared_out = [&](PackedPass &p, int i, void *dst) {
     p.out = parts ? parts_of[i] : dst;
     p.ldo = parts ? (long long)H * dk : (long long)Hk * dk;
@@ -162,8 +163,7 @@ int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, c
   p[2].da = dk; p[2].db = dv; p[2].S_in = dS_final; p[2].S_out = dS0;
   p[2].out = dv_out; p[2].ldo = ldd; p[2].out_f32 = f32;
   rc = run_passes(p, 3, s);
-  if (parts && rc == LA_OK) rc = launch_head_sum(parts_of[0], dq, f32, total, Hk, share, dk, s);
-  if (parts && rc == LA_OK) rc = launch_head_sum(parts_of[1], dk_out, f32, total, Hk, share, dk, s);
+  if (parts && rc == LA_OK) rc = launch_head_sums(parts_of, summed, f32, total, Hk, share, dk, s);
   if (parts) {
     const cudaError_t e = cudaFreeAsync(parts, s);
     if (rc == LA_OK && e != cudaSuccess) {

@@ -98,8 +98,9 @@ struct Decay {
 int launch_packed_walk(const PackedPass &p, cudaStream_t stream);
 // Up to three passes that do not depend on each other.
 int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream);
-// dst[n][hk][d] = sum over the `share` heads of src float32 [n][hk * share][d]
-int launch_head_sum(const float *src, void *dst, int f32, int N, int Hk, int share, int d, cudaStream_t stream);
+// dst[i][n][hk][d] = sum over the `share` heads of src[i] float32 [n][hk * share][d], for both i
+int launch_head_sums(const float *const src[2], void *const dst[2], int f32, int N, int Hk, int share, int d,
+                     cudaStream_t stream);
 
 struct PackedStep {
   const void *q, *k, *v;

@@ -72,8 +72,8 @@ constexpr uint32_t kSpin = 1u << 22;     // polls before a wait gives up (tens o
 constexpr int kRegsIssue = 56, kRegsState = 104, kRegsOut = 88, kRegsP = 72, kRegsZ = 56;
 static_assert(kRegsIssue + kRegsState + kRegsOut + 2 * kRegsP + 2 * kRegsZ <= 7 * 72, "register split");
 
-// A unit as the plan writes it: tokens [t0, t1), its number, and 2 * state row + (the state
-// behind it is its sequence's last); state row -1: none.
+// A unit as the plan writes it: tokens [t0, t1), its number, and 4 * state row + 2 * (it is all of
+// its sequence) + (the state behind it is its sequence's last); state row -1: none.
 struct Unit {
   int t0, t1, u, row;
 };
@@ -84,13 +84,13 @@ struct Segments {
   const Unit *plan;  // units with something to do, the longest first, or null: unit u is sequence u, one item a CTA
   const int *count;  // how many
   unsigned *queue;   // next item for a CTA that is done, from zero
-  const float *in;   // [unit][H][dk][dv] entering states, or null: S_in by row
+  const float *in;   // [unit][H][dk][dv] entering states of split sequences; the others': S_in by row
   float *out;        // STATE: the segments' own contributions
 };
 
 // One item of work: a unit, a head and 64 value columns. chunks < 0: no more items.
 struct Item {
-  int t0, t1, chunks, h, v0, u, slot, leaves;
+  int t0, t1, chunks, h, v0, u, slot, leaves, whole;
 };
 
 // First unit number of sequence s.
@@ -102,11 +102,25 @@ __device__ __forceinline__ int chunks_of(int tokens) { return (tokens + kN - 1) 
 
 // Where a long walk is left for the end the other SMs wait for it: the plan
 // lists the units from the longest down (a counting sort over their chunks; the
-// order of equal ones is arbitrary, and no result goes by it). One CTA; clears
-// the queues on the way.
+// order of equal ones is arbitrary, and no result goes by it). One CTA a pass;
+// clears the queues on the way.
 constexpr int kPlanThreads = 1024, kBuckets = 1024;
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedPass p, int seg, int units, unsigned *head,
-                                                            int *owner, Unit *plan) {
+struct PlanJob {
+  PackedPass p;
+  int seg, units;
+  unsigned *head;
+  int *owner;
+  Unit *plan;
+};
+struct PlanJobs {
+  PlanJob job[3];
+};
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs) {
+  const PackedPass &p = jobs.job[blockIdx.x].p;
+  const int seg = jobs.job[blockIdx.x].seg, units = jobs.job[blockIdx.x].units;
+  unsigned *head = jobs.job[blockIdx.x].head;
+  int *owner = jobs.job[blockIdx.x].owner;
+  Unit *plan = jobs.job[blockIdx.x].plan;
   __shared__ int first[kBuckets];
   __shared__ int warp_sum[32];
   const int tid = threadIdx.x;
@@ -141,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PackedPass p, 
         const int t0 = a + k * seg, t1 = seg ? min(b, t0 + seg) : b;
         const int bucket = kBuckets - 1 - min(chunks_of(t1 - t0), kBuckets - 1);
         const int at = atomicAdd(first + bucket, 1);
-        if (pass) plan[at] = {t0, t1, u0 + k, 2 * row + (p.reverse ? k == 0 : k == n - 1)};
+        if (pass) plan[at] = {t0, t1, u0 + k, 4 * row + 2 * (n == 1) + (p.reverse ? k == 0 : k == n - 1)};
       }
     }
     __syncthreads();
@@ -362,7 +376,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
               if (__any_sync(0xffffffffu, taken)) slot = -1;
             }
             un.u = u;
-            un.row = 2 * slot + 1;
+            un.row = 4 * slot + 3;
           }
           it.t0 = un.t0;
           it.t1 = un.t1;
@@ -370,15 +384,16 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
           it.v0 = w % vtiles * 64;
           it.h = w / vtiles % p.H;
           it.u = un.u;
-          it.slot = un.row >> 1;
+          it.slot = un.row >> 2;
+          it.whole = un.row >> 1 & 1;
           it.leaves = un.row & 1;
         }
         if (!found) it.chunks = -1;
         int go = 1;
         if (lane == 0) {
           // the state that the item starts from, into L2: its reader comes to it between two items
-          if (found && !STATE && (sg.in || (p.S_in && it.slot >= 0)) && it.v0 == 0)
-            bulk_prefetch_l2((sg.in ? sg.in + (size_t)it.u * p.H * p.sized : p.S_in + (size_t)it.slot * p.H * p.sized) +
+          if (found && !STATE && (!it.whole || (p.S_in && it.slot >= 0)) && it.v0 == 0)
+            bulk_prefetch_l2((!it.whole ? sg.in + (size_t)it.u * p.H * p.sized : p.S_in + (size_t)it.slot * p.H * p.sized) +
                                  (size_t)it.h * p.sized, p.sized * 4);
           go = wait(&e_free[k & (kRing - 1)], k / kRing ^ 1);
           if (go) {
@@ -548,13 +563,13 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
       if (STATE) {
         dst = sg.out + by_unit;
       } else {
-        if (sg.in) src = sg.in + by_unit;
+        if (!it.whole) src = sg.in + by_unit;
         else if (p.S_in && it.slot >= 0) src = p.S_in + by_slot;
         if (p.S_out && it.leaves && it.slot >= 0) dst = p.S_out + by_slot;
       }
       float S[64];
       if (src && c < DA) {
-        if (p.in_t && !sg.in) {  // (the segments' states lie as this pass wants them)
+        if (p.in_t && it.whole) {  // (the segments' states lie as this pass wants them)
 #pragma unroll
           for (int e = 0; e < 64; ++e) S[e] = src[(size_t)(it.v0 + e) * DA + c];
         } else {
@@ -819,7 +834,7 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(const PackedPass p, i
   const int slot = packed_slot(p.slots, s, p.n_slots);
   if (e >= p.sized) return;
   const int n = max(1, (b - a + seg - 1) / seg), u0 = first_unit(p, seg, s);
-  if (u0 + n > units) return;  // only where cu_seqlens is not what it should be
+  if (n == 1 || u0 + n > units) return;  // whole sequences read S_in; the second only where cu_seqlens is not what it should be
   const float g = p.g ? __ldg(p.g + h) : 0.f;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (p.S_in && slot >= 0) {
@@ -992,18 +1007,22 @@ int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream) {
   }
   // counters, owners of the state rows, plan, segments' states of each pass
   uint8_t *at = ws;
-  for (int i = 0; i < passes && e == cudaSuccess; ++i) {
+  PlanJobs jobs = {};
+  int planned = 0;
+  for (int i = 0; i < passes; ++i) {
     if (!r[i].plan) continue;
     unsigned *head = reinterpret_cast<unsigned *>(at);
     Unit *plan = reinterpret_cast<Unit *>(at + 256 + r[i].owners);
-    plan_kernel<<<1, kPlanThreads, 0, stream>>>(p[i], r[i].sg.tokens, r[i].sg.units, head,
-                                                reinterpret_cast<int *>(at + 256), plan);
-    e = cudaGetLastError();
+    jobs.job[planned++] = {p[i], r[i].sg.tokens, r[i].sg.units, head, reinterpret_cast<int *>(at + 256), plan};
     r[i].sg.plan = plan;
     r[i].sg.count = reinterpret_cast<const int *>(head + 2);
     r[i].sg.queue = head;
     if (r[i].sg.tokens) r[i].sg.out = reinterpret_cast<float *>(at + 256 + r[i].owners + r[i].plan);
     at += 256 + r[i].owners + r[i].plan + r[i].states;
+  }
+  if (planned) {
+    plan_kernel<<<planned, kPlanThreads, 0, stream>>>(jobs);
+    e = cudaGetLastError();
   }
   bool beside = false;
   for (int i = 0; i < passes && e == cudaSuccess; ++i) {

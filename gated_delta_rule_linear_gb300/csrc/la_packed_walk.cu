@@ -82,8 +82,11 @@ __global__ void __launch_bounds__(128) packed_walk_kernel(const PackedPass p) {
 
 // Gradients of shared heads: the float32 parts of the heads that use one.
 template <typename T>
-__global__ void __launch_bounds__(256) head_sum_kernel(const float *__restrict__ src, T *__restrict__ dst,
+__global__ void __launch_bounds__(256) head_sum_kernel(const float *__restrict__ src0, T *__restrict__ dst0,
+                                                       const float *__restrict__ src1, T *__restrict__ dst1,
                                                        long long quads, int share, int d) {
+  const float *src = blockIdx.y ? src1 : src0;
+  T *dst = blockIdx.y ? dst1 : dst0;
   const int dq = d / 4;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < quads; i += gridDim.x * 256LL) {
     const long long row = i / dq;  // (token, shared head)
@@ -122,15 +125,18 @@ int launch_packed_walk(const PackedPass &p, cudaStream_t stream) {
   return LA_OK;
 }
 
-int launch_head_sum(const float *src, void *dst, int f32, int N, int Hk, int share, int d, cudaStream_t stream) {
+int launch_head_sums(const float *const src[2], void *const dst[2], int f32, int N, int Hk, int share, int d,
+                     cudaStream_t stream) {
   const long long quads = (long long)N * Hk * (d / 4);
   if (quads == 0) return LA_OK;
   const long long want = (quads + 255) / 256;
-  const int grid = static_cast<int>(want < 16384 ? want : 16384);
+  const dim3 grid(static_cast<unsigned>(want < 16384 ? want : 16384), 2);
   if (f32)
-    head_sum_kernel<<<grid, 256, 0, stream>>>(src, static_cast<float *>(dst), quads, share, d);
+    head_sum_kernel<<<grid, 256, 0, stream>>>(src[0], static_cast<float *>(dst[0]), src[1], static_cast<float *>(dst[1]),
+                                              quads, share, d);
   else
-    head_sum_kernel<<<grid, 256, 0, stream>>>(src, static_cast<__nv_bfloat16 *>(dst), quads, share, d);
+    head_sum_kernel<<<grid, 256, 0, stream>>>(src[0], static_cast<__nv_bfloat16 *>(dst[0]), src[1],
+                                              static_cast<__nv_bfloat16 *>(dst[1]), quads, share, d);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("la_packed_bwd: head sum launch failed: %s", cudaGetErrorString(e));
