@@ -163,7 +163,7 @@ int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, c
   p[2].da = dk; p[2].db = dv; p[2].S_in = dS_final; p[2].S_out = dS0;
   p[2].out = dv_out; p[2].ldo = ldd; p[2].out_f32 = f32;
   rc = run_passes(p, 3, s);
-  if (parts && rc == LA_OK) rc = launch_head_sums(parts_of, summed, f32, total, Hk, share, dk, s);
+  if (parts && rc == LA_OK) rc = launch_head_sums(parts_of, summed, f32, cu_seqlens, n_seq, total, Hk, share, dk, s);
   if (parts) {
     const cudaError_t e = cudaFreeAsync(parts, s);
     if (rc == LA_OK && e != cudaSuccess) {

@@ -99,8 +99,9 @@ int launch_packed_walk(const PackedPass &p, cudaStream_t stream);
 // Up to three passes that do not depend on each other.
 int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream);
 // dst[i][n][hk][d] = sum over the `share` heads of src[i] float32 [n][hk * share][d], for both i
-int launch_head_sums(const float *const src[2], void *const dst[2], int f32, int N, int Hk, int share, int d,
-                     cudaStream_t stream);
+// and the tokens n of the sequences
+int launch_head_sums(const float *const src[2], void *const dst[2], int f32, const int *cu, int n_seq, int total,
+                     int Hk, int share, int d, cudaStream_t stream);
 
 struct PackedStep {
   const void *q, *k, *v;

@@ -80,18 +80,21 @@ __global__ void __launch_bounds__(128) packed_walk_kernel(const PackedPass p) {
     for (int c = 0; c < R; ++c) p.S_out[sbase + (size_t)(c0 + c) * p.db + col] = S[c];
 }
 
-// Gradients of shared heads: the float32 parts of the heads that use one.
+// Gradients of shared heads: the float32 parts of the heads that use one. Tokens in front of
+// the first sequence and behind the last have no parts, and their rows stay as they are.
 template <typename T>
 __global__ void __launch_bounds__(256) head_sum_kernel(const float *__restrict__ src0, T *__restrict__ dst0,
                                                        const float *__restrict__ src1, T *__restrict__ dst1,
-                                                       long long quads, int share, int d) {
+                                                       const int *__restrict__ cu, int n_seq, int total,
+                                                       int heads, int share, int d) {
   const float *src = blockIdx.y ? src1 : src0;
   T *dst = blockIdx.y ? dst1 : dst0;
   const int dq = d / 4;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < quads; i += gridDim.x * 256LL) {
-    const long long row = i / dq;  // (token, shared head)
+  const long long a = min(max(__ldg(cu), 0), total), b = min(max(__ldg(cu + n_seq), 0), total), row = (long long)heads * dq;
+  for (long long i = a * row + blockIdx.x * 256LL + threadIdx.x; i < b * row; i += gridDim.x * 256LL) {
+    const long long at = i / dq;  // (token, shared head)
     const int c = static_cast<int>(i % dq);
-    const float4 *s = reinterpret_cast<const float4 *>(src + row * share * d) + c;
+    const float4 *s = reinterpret_cast<const float4 *>(src + at * share * d) + c;
     float4 t = __ldcs(s);
     for (int j = 1; j < share; ++j) {
       const float4 u = __ldcs(s + (size_t)j * dq);
@@ -125,18 +128,18 @@ int launch_packed_walk(const PackedPass &p, cudaStream_t stream) {
   return LA_OK;
 }
 
-int launch_head_sums(const float *const src[2], void *const dst[2], int f32, int N, int Hk, int share, int d,
-                     cudaStream_t stream) {
-  const long long quads = (long long)N * Hk * (d / 4);
+int launch_head_sums(const float *const src[2], void *const dst[2], int f32, const int *cu, int n_seq, int total,
+                     int Hk, int share, int d, cudaStream_t stream) {
+  const long long quads = (long long)total * Hk * (d / 4);
   if (quads == 0) return LA_OK;
   const long long want = (quads + 255) / 256;
   const dim3 grid(static_cast<unsigned>(want < 16384 ? want : 16384), 2);
   if (f32)
     head_sum_kernel<<<grid, 256, 0, stream>>>(src[0], static_cast<float *>(dst[0]), src[1], static_cast<float *>(dst[1]),
-                                              quads, share, d);
+                                              cu, n_seq, total, Hk, share, d);
   else
     head_sum_kernel<<<grid, 256, 0, stream>>>(src[0], static_cast<__nv_bfloat16 *>(dst[0]), src[1],
-                                              static_cast<__nv_bfloat16 *>(dst[1]), quads, share, d);
+                                              static_cast<__nv_bfloat16 *>(dst[1]), cu, n_seq, total, Hk, share, d);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("la_packed_bwd: head sum launch failed: %s", cudaGetErrorString(e));

@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 
 #include "la_layer_internal.h"
+#include "la_sm100.cuh"
 
 namespace la {
 namespace {
@@ -73,6 +74,14 @@ template <typename T, int V, bool IL>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p, const RotaryDiv by, int tokens) {
   extern __shared__ float2 turn[];  // [tokens][P] cos, sin
   const int P = p.s0 + p.s1 + p.s2, n0 = blockIdx.x * tokens, m = min(tokens, p.N - n0);
+  // the rows into L2 under the sines; a token's heads are one run of bytes
+  if (V > 1 && p.T_in == 0 && (int)threadIdx.x < 2 * m) {
+    const bool is_k = threadIdx.x & 1;
+    if (!is_k || p.k)
+      sm100::bulk_prefetch_l2(static_cast<const T *>(is_k ? p.k : p.q) +
+                                  (size_t)(n0 + (threadIdx.x >> 1)) * (is_k ? p.ldk : p.ldq),
+                              (is_k ? p.Hk : p.H) * p.d * static_cast<int>(sizeof(T)));
+  }
   for (int i = threadIdx.x; i < m * P; i += kThreads) {
     uint32_t n, c;
     by.P.split(i, n, c);

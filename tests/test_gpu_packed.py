@@ -191,6 +191,39 @@ def test_backward_of_long_sequences(max_len):
     check_bwd([2500, 3, 0, 900], 2, 1, 64, 64, BF, max_len=max_len, seed=5)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2)])
+def test_rows_of_no_sequence(H, Hk, dtype):
+    # tokens in front of the first sequence and behind the last: read by nobody, written by nobody
+    front, lens, back, dk, dv = 37, [150, 0, 90], 45, 64, 64
+    q, k, v, dO, S0, dS = draw(lens, H, Hk, dk, dv, dtype, 23, front + back)
+    rows = slice(front, front + sum(lens))
+    for t in (q, k, v, dO):
+        t[:front] = t[front + sum(lens):] = float("nan")
+    c = cu(lens) + front
+    g = gammas(H)
+    N = len(q)
+    args = up(q, k, v, dO)
+    outs = [torch.full((N, Hk, dk), 5.0, dtype=dtype, device="cuda") for _ in range(2)]
+    outs += [torch.full((N, H, dv), 5.0, dtype=dtype, device="cuda") for _ in range(2)]
+    dS0 = torch.empty(3, H, dk, dv, device="cuda")
+    mode = la.MODE_IDS["retnet"] | (la.LA_F32 if dtype == F32 else 0)
+    ld = (Hk * dk, Hk * dk, H * dv)
+    stream = torch.cuda.current_stream().cuda_stream
+    dg, dS0_in, dS_in = up(g, S0, dS)
+    assert la.la_packed_bwd(*args[:3], dg, args[3], dS0_in, dS_in, outs[0], outs[1], outs[2], dS0, c, 3, N, 0, H, Hk, dk,
+                            dv, *ld, mode, stream) == 0
+    assert la.la_packed_fwd(*args[:3], dg, outs[3], dS0_in, None, c, None, 3, N, 0, 3, H, Hk, dk, dv, *ld, mode, stream) == 0
+    done()
+    inner = [t[rows] for t in (q, k, v, dO)]
+    want = retention_bwd(*inner, g, lens, S0, dS)[:3] + (retention(*inner[:3], g, lens, S0)[0],)
+    size = retention_bwd(*inner, g, lens, S0, dS, positive=True)[:3] + (
+        retention(*inner[:3], g, lens, S0, positive=True)[0],)
+    for name, t, a, b in zip(("dq", "dk", "dv", "o"), outs, want, size):
+        assert (t[:front] == 5.0).all() and (t[front + sum(lens):] == 5.0).all(), name
+        hold(t[rows], a, packed_bound(a, b, 150, dtype), name)
+
+
 def test_backward_against_differences():
     # the linear map's gradient against the forward itself, in float32: L = <dO, o> + <dS, S_final> is
     # linear in each input, so a step of any size is exact up to rounding
