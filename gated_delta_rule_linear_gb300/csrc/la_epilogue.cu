@@ -355,7 +355,8 @@ template <typename T> __device__ __forceinline__ void put_pair(uint4 &u, int j, 
 // (twice: for the sums, for the gradients): with the row's values in registers
 // as float32 the next row's loads did not fit beside them, and without those in
 // flight the kernel waited for memory (0.46 ms against TIME on 32768 x 2048).
-template <typename T, int V, int NV>
+// GATE: 0 none, 1 silu, 2 sigmoid; NEXT: with the next norm's gradient; -1: as the arguments say.
+template <typename T, int V, int NV, int GATE, int NEXT>
 __global__ void __launch_bounds__(512, 1) epilogue_bwd_kernel(const EpilogueParams p, const XRows xr, int tpr,
                                                               float *part) {
   namespace q = f32x2;
@@ -366,7 +367,8 @@ __global__ void __launch_bounds__(512, 1) epilogue_bwd_kernel(const EpiloguePara
   const float inv_d = 1.f / static_cast<float>(d);
   int turn = 0;
   auto col = [&](int i) { return (i * tpr + lane) * V; };
-  const bool with_next = p.d_next != nullptr, with_res = p.res && with_next, silu = p.act == LA_ACT_SILU;
+  const bool with_next = NEXT < 0 ? p.d_next != nullptr : NEXT != 0, with_res = p.res && with_next;
+  const bool gated = GATE < 0 ? p.gate != nullptr : GATE != 0, silu = GATE < 0 ? p.act == LA_ACT_SILU : GATE == 1;
   uint64_t ws[E2], wn[E2], as[E2], an[E2];  // w scale, w_next; sums of tot a n and d_next m
 #pragma unroll
   for (int i = 0; i < E2; ++i) {
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(512, 1) epilogue_bwd_kernel(const EpiloguePara
     for (int i = 0; i < NV; ++i) {
       if (col(i) >= d) continue;
       nx[i].load(static_cast<const T *>(p.x) + xat + col(i));
-      if (p.gate) na[i].load(static_cast<const T *>(p.gate) + at + col(i));
+      if (gated) na[i].load(static_cast<const T *>(p.gate) + at + col(i));
       if (with_res) no[i].load(static_cast<const T *>(p.res) + at + col(i));
       if (p.d_out) ng[i].load(static_cast<const T *>(p.d_out) + at + col(i));
       if (with_next) nn[i].load(static_cast<const T *>(p.d_next) + at + col(i));
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(512, 1) epilogue_bwd_kernel(const EpiloguePara
   };
   // value and slope of the gate
   auto gate = [&](uint64_t a2, uint64_t &slope) {
-    if (!p.gate) {
+    if (!gated) {
       slope = 0;
       return q::pair(1.f, 1.f);
     }
@@ -593,12 +595,28 @@ cudaError_t launch(const EpilogueParams &p, const Shape &s, float *part, cudaStr
 #define LA_GO(v, n)                                                                              \
   do {                                                                                           \
     if constexpr (BWD && v > 1)                                                                  \
-      epilogue_bwd_kernel<T, v, n><<<s.blocks, s.threads, 0, stream>>>(p, xr, s.tpr, part);      \
+      epilogue_bwd_kernel<T, v, n, -1, -1><<<s.blocks, s.threads, 0, stream>>>(p, xr, s.tpr, part); \
     else                                                                                         \
       epilogue_kernel<T, v, n, BWD><<<s.blocks, s.threads, 0, stream>>>(p, xr, s.tpr, part);     \
   } while (0)
+  if constexpr (BWD)
+    if (s.wide && s.nv == 1) {
+#define LA_BWD(g, n) epilogue_bwd_kernel<T, V, 1, g, n><<<s.blocks, s.threads, 0, stream>>>(p, xr, s.tpr, part)
+      const int gate = !p.gate ? 0 : p.act == LA_ACT_SILU ? 1 : 2;
+      if (p.d_next) {
+        if (gate == 0) LA_BWD(0, 1);
+        else if (gate == 1) LA_BWD(1, 1);
+        else LA_BWD(2, 1);
+      } else {
+        if (gate == 0) LA_BWD(0, 0);
+        else if (gate == 1) LA_BWD(1, 0);
+        else LA_BWD(2, 0);
+      }
+#undef LA_BWD
+      return cudaGetLastError();
+    }
   if (s.wide) {
-    if (s.nv == 1) LA_GO(V, 1);
+    if (!BWD && s.nv == 1) LA_GO(V, 1);
     else if (s.nv == 2) LA_GO(V, 2);
     else if (s.nv == 4) LA_GO(V, 4);
     else LA_GO(V, 8);
