@@ -17,6 +17,13 @@
 // them. The backward adds its weight gradients up in registers over the rows a
 // thread sees, writes one partial a CTA, and a second kernel adds the partials
 // in order: no atomics, the same sums every run.
+//
+// Measured on GB300 (6.78 TB/s copy): per-head norm and silu gate of 65536 x 16
+// heads of 128, bf16, head-major x: 0.156 ms, 5.15 TB/s; with the 96 registers a
+// thread that the compiler takes unasked, 0.193 (too few threads a SM to cover
+// memory: hence 64 at one load a thread). Backward with residual, scale, sigmoid
+// gate and next norm on 32768 x 2048: 0.270 ms, 3.97 TB/s, bound by issue (about
+// 80 instructions for two channels) and its 2 CTAs of 256 a SM.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -354,7 +361,7 @@ template <typename T> __device__ __forceinline__ void put_pair(uint4 &u, int j, 
 // was loaded and every value is formed again, pair by pair, where it is needed
 // (twice: for the sums, for the gradients): with the row's values in registers
 // as float32 the next row's loads did not fit beside them, and without those in
-// flight the kernel waited for memory (0.46 ms against TIME on 32768 x 2048).
+// flight the kernel waited for memory (0.46 ms against 0.27 on 32768 x 2048).
 // GATE: 0 none, 1 silu, 2 sigmoid; NEXT: with the next norm's gradient; -1: as the arguments say.
 template <typename T, int V, int NV, int GATE, int NEXT>
 __global__ void __launch_bounds__(512, 1) epilogue_bwd_kernel(const EpilogueParams p, const XRows xr, int tpr,

@@ -6,7 +6,8 @@
 // the rows w*da/4 .. of column l. Tokens come 16 at a time through shared
 // memory; every warp's partial of out_t over its rows goes to shared memory and
 // is added up once per block of tokens. The walk is bound by its own serial
-// chain, about da/2 FMAs a token and warp, not by memory.
+// chain, about da/2 FMAs a token and warp, not by memory (4 x 16384 tokens of 16
+// heads of 128: 7.9 ms, 0.48 us a token).
 #include <cuda_bf16.h>
 
 #include "la_layer_internal.h"

@@ -57,6 +57,11 @@ extern "C" {
  *   mode    LA_LINEAR or LA_RETNET, bfloat16 q, k, v, o, or float32 with
  *           | LA_F32. Other modes of la.h: LA_ERR_UNSUPPORTED.
  *
+ * bfloat16 runs chunkwise on the tensor cores, float32 token by token on the
+ * CUDA cores. Workspace from the library's pool where the heads and sequences
+ * are more than the SMs or a sequence is long: 16 bytes a sequence or segment,
+ * 4*n_slots with slots, and for split sequences 4*H*dk*dv a segment.
+ *
  * Inputs are finite: a NaN or infinity at a token may reach every token of the
  * same sequence; never another sequence, whatever the neighbours hold.
  */
@@ -83,6 +88,9 @@ int la_packed_fwd(const void *q, const void *k, const void *v, const float *g, v
  *           dtype; rows of tokens in no sequence are not written
  *   dS0     float32 [n_seq][H][dk][dv] or NULL (not computed)
  *   Outputs overlap no input. 16-byte alignment for every tensor.
+ * Runs as three passes of la_packed_fwd's kernel with the tensors' places
+ * exchanged (dk, dv: from the last token to the first), each with that
+ * function's workspace, and with shared heads another 8*total*H*dk bytes.
  */
 int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, const void *dO,
                   const float *S0, const float *dS_final, void *dq, void *dk_out, void *dv_out, float *dS0,

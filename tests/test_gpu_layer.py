@@ -262,6 +262,27 @@ def test_epilogue_bwd_is_the_same_every_run_and_on_many_rows():
     hold(a["dw"], dw, 2.0 ** -15 * size, "dw")
 
 
+def test_offsets_past_32_bits():
+    # 2^24 rows of 128 channels: the last rows' elements lie behind 2^31
+    n, tail, d = 1 << 24, 5, 128
+    gen = torch.Generator().manual_seed(9)
+    x, gate = (torch.randn(tail, 1, d, generator=gen).to(BF) for _ in range(2))
+    big = [torch.zeros(n + tail, 1, d, dtype=BF, device="cuda") for _ in range(2)]
+    for t, r in zip(big, (x, gate)):
+        t[n:] = r.cuda()
+    out, _ = la.epilogue(big[0], gate=big[1])
+    want, _ = block(x.double(), None, gate.double(), "silu", None, None, None, 1e-5)
+    hold(out[n:], want, HALF[BF] * want.abs() + 2.0 ** -17 * want.abs(), "out")
+    dx = la.epilogue_bwd(big[0], big[1], gate=big[1])["dx"]
+    alone = la.epilogue_bwd(x.cuda(), gate.cuda(), gate=gate.cuda())["dx"]
+    assert torch.equal(dx[n:], alone)
+    pos = torch.zeros(n + tail, 1, dtype=torch.int32, device="cuda")
+    pos[n:, 0] = torch.arange(7, 7 + tail)
+    freq = spectrum([64])
+    turned_x, _ = la.rotary(big[0], None, pos, freq.cuda())
+    hold_turned(turned_x[n:], x, pos[n:].cpu(), freq, [64], False, False, 1.0)
+
+
 # ------------------------------------------------------------- a whole layer
 
 @pytest.mark.parametrize("dtype", [BF, F32])

@@ -387,3 +387,48 @@ def test_the_same_every_run():
     a = la.packed_bwd(*x, cu(lens), "retnet", g=g)
     for _ in range(3):
         assert all(torch.equal(p, q) for p, q in zip(a, la.packed_bwd(*x, cu(lens), "retnet", g=g)))
+
+
+def test_offsets_past_32_bits():
+    # 2^24 tokens of 128 channels: the last sequence's elements lie behind 2^31
+    n, tail, d = 1 << 24, 150, 128
+    N = n + tail
+    q, k, v, dO, S0, dS = draw([tail], 1, 1, d, d, BF, 24)
+    big = [torch.zeros(N, 1, d, dtype=BF, device="cuda") for _ in range(4)]
+    for t, x in zip(big, (q, k, v, dO)):
+        t[n:] = x.cuda()
+    step = n // 64
+    c = torch.tensor([i * step for i in range(65)] + [N], dtype=torch.int32).cuda()
+    g = gammas(1)
+    o, S = la.packed_fwd(*big[:3], c, "retnet", g=g.cuda())
+    args, size_args = (q, k, v, g, [tail]), dict(positive=True)
+    want, Sw = retention(*args)
+    size, Ss = retention(*args, **size_args)
+    hold(o[n:], want, packed_bound(want, size, tail, BF), "o")
+    hold(S[64:], Sw, state_bound(Ss, tail, BF), "S_final")
+    assert (o[:n].view(-1, 1 << 20).float().abs().amax(1) == 0).all()
+    del o
+    got = la.packed_bwd(*big, c, "retnet", g=g.cuda())
+    done()
+    want = retention_bwd(q, k, v, dO, g, [tail])
+    size = retention_bwd(q, k, v, dO, g, [tail], positive=True)
+    for name, a, b, e in zip(("dq", "dk", "dv"), got, want, size):
+        hold(a[n:], b, packed_bound(b, e, tail, BF), name)
+
+
+def test_many_short_sequences():
+    # more sequences than a CTA's threads, lengths 0 to 3, and a pool of states in another order
+    gen = torch.Generator().manual_seed(25)
+    lens = torch.randint(0, 4, (1500,), generator=gen).tolist()
+    q, k, v, _, S0, _ = draw(lens, 1, 1, 64, 64, BF, 25)
+    slots = torch.randperm(1600, generator=gen)[:1500].to(torch.int32)
+    pool = torch.zeros(1600, 1, 64, 64)
+    pool[slots.long()] = S0
+    dev = pool.cuda()
+    g = gammas(1)
+    o, S = la.packed_fwd(*up(q, k, v), cu(lens), "retnet", g=g.cuda(), S0=dev, S_final=dev, slots=slots.cuda())
+    done()
+    want, Sw = retention(q, k, v, g, lens, S0)
+    size, Ss = retention(q, k, v, g, lens, S0, positive=True)
+    hold(o, want, packed_bound(want, size, 3, BF), "o")
+    hold(S.cpu()[slots.long()], Sw, state_bound(Ss, 3, BF), "S")
