@@ -129,24 +129,17 @@ class _On:
             c.__exit__(*e)
 
 
-class _Here:
-    """The common case: the current device and its current stream."""
-
-    def __init__(self, handle):
-        self.handle = handle
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *e):
-        pass
-
-
-def _on(idx, stream):
+def _launch(idx, stream, body):
+    """body(stream handle) on the tensors' device: at once where that and the stream are current already."""
     import torch
     if stream is None and idx == torch._C._cuda_getDevice():
-        return _Here(torch._C._cuda_getCurrentRawStream(idx))
-    return _On(idx, stream)
+        return body(torch._C._cuda_getCurrentRawStream(idx))
+    with _On(idx, stream) as handle:
+        return body(handle)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rows(t, name):
@@ -184,7 +177,8 @@ def _qkv(q, k, v):
     return N, H, Hk, dk, dv, lq, lk, lv, idx
 
 
-def _run(rc):
+def _run(name, *args):
+    rc = (_fns.get(name) or _fn(name))(*args)
     if rc != 0:
         raise LAError(rc, la_last_error())
 
@@ -217,14 +211,17 @@ def packed_fwd(q, k, v, cu_seqlens, mode, g=None, S0=None, slots=None, S_final=N
         S_final = None
     _check(S_final, "S_final", f32, (rows, H, dk, dv), idx)
     _check(o, "o", q.dtype, (N, H, dv), idx)
-    with _on(idx, stream) as handle:
-        if o is None:
-            o = q.new_empty((N, H, dv))
-        if with_state and S_final is None and slots is None:
-            S_final = q.new_empty((n, H, dk, dv), dtype=f32)
-        _run(la_packed_fwd(q, k, v, g, o, S0, S_final, cu_seqlens, slots, n, N, max_len, rows, H, Hk, dk, dv, lq, lk,
-                           lv, mid, handle))
-    return o, S_final
+
+    def body(handle):
+        out = q.new_empty((N, H, dv)) if o is None else o
+        state = S_final
+        if with_state and state is None and slots is None:
+            state = q.new_empty((n, H, dk, dv), dtype=f32)
+        _run("la_packed_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(g), out.data_ptr(), _at(S0), _at(state),
+             cu_seqlens.data_ptr(), _at(slots), n, N, max_len, rows, H, Hk, dk, dv, lq, lk, lv, mid, handle)
+        return out, state
+
+    return _launch(idx, stream, body)
 
 
 def packed_bwd(q, k, v, dO, cu_seqlens, mode, g=None, S0=None, dS_final=None, with_dS0=True, max_len=0, stream=None):
@@ -239,12 +236,16 @@ def packed_bwd(q, k, v, dO, cu_seqlens, mode, g=None, S0=None, dS_final=None, wi
     _check(dO, "dO", q.dtype, (N, H, dv), idx)
     _check(S0, "S0", f32, (n, H, dk, dv), idx)
     _check(dS_final, "dS_final", f32, (n, H, dk, dv), idx)
-    with _on(idx, stream) as handle:
+
+    def body(handle):
         dq, dk_, dv_ = q.new_empty((N, Hk, dk)), q.new_empty((N, Hk, dk)), q.new_empty((N, H, dv))
         dS0 = q.new_empty((n, H, dk, dv), dtype=f32) if with_dS0 else None
-        _run(la_packed_bwd(q, k, v, g, dO, S0, dS_final, dq, dk_, dv_, dS0, cu_seqlens, n, N, max_len, H, Hk, dk, dv,
-                           lq, lk, lv, mid, handle))
-    return dq, dk_, dv_, dS0
+        _run("la_packed_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(g), dO.data_ptr(), _at(S0), _at(dS_final),
+             dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), _at(dS0), cu_seqlens.data_ptr(), n, N, max_len, H, Hk, dk,
+             dv, lq, lk, lv, mid, handle)
+        return dq, dk_, dv_, dS0
+
+    return _launch(idx, stream, body)
 
 
 def packed_step(q, k, v, S, mode, g=None, slots=None, o=None, stream=None):
@@ -258,11 +259,14 @@ def packed_step(q, k, v, S, mode, g=None, slots=None, o=None, stream=None):
     _check(g, "g", torch.float32, (H,), idx)
     _check(slots, "slots", torch.int32, (N,), idx)
     _check(o, "o", q.dtype, (N, H, dv), idx)
-    with _on(idx, stream) as handle:
-        if o is None:
-            o = q.new_empty((N, H, dv))
-        _run(la_packed_step(q, k, v, g, o, S, slots, N, rows, H, Hk, dk, dv, lq, lk, lv, mid, handle))
-    return o
+
+    def body(handle):
+        out = q.new_empty((N, H, dv)) if o is None else o
+        _run("la_packed_step", q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(g), out.data_ptr(), S.data_ptr(), _at(slots),
+             N, rows, H, Hk, dk, dv, lq, lk, lv, mid, handle)
+        return out
+
+    return _launch(idx, stream, body)
 
 
 def _tokens_of(t, name):
@@ -305,16 +309,15 @@ def rotary(q, k, pos, freq, sections=None, interleaved=False, inverse=False, sca
     _check(k_out, "k_out", dt, kshape, idx)
     flags = _flag(dt) | (LAYER_CONSTANTS["LA_ROT_INTERLEAVED"] if interleaved else 0) \
         | (LAYER_CONSTANTS["LA_ROT_INVERSE"] if inverse else 0)
-    with _on(idx, stream) as handle:
-        if q_out is None:
-            q_out = q.new_empty(shape)
-        if k is None:
-            k_out = None
-        elif k_out is None:
-            k_out = q.new_empty(kshape)
-        _run(la_rotary(q, k, q_out, k_out, pos, freq, axes, *(s + (0, 0))[:3], N, H, Hk, d, T, T_out, ldq, ldk,
-                       scale_q, scale_k, flags, handle))
-    return q_out, k_out
+
+    def body(handle):
+        a = q.new_empty(shape) if q_out is None else q_out
+        b = None if k is None else q.new_empty(kshape) if k_out is None else k_out
+        _run("la_rotary", q.data_ptr(), _at(k), a.data_ptr(), _at(b), pos.data_ptr(), freq.data_ptr(), axes,
+             *(s + (0, 0))[:3], N, H, Hk, d, T, T_out, ldq, ldk, scale_q, scale_k, flags, handle)
+        return a, b
+
+    return _launch(idx, stream, body)
 
 
 def _block(x, w, gate, act, res, scale, w_next):
@@ -344,15 +347,15 @@ def epilogue(x, w=None, gate=None, act="silu", res=None, scale=None, w_next=None
     flags = _flag(x.dtype)
     _check(out, "out", x.dtype, (N, G, d), idx)
     _check(next, "next", x.dtype, (N, G, d), idx)
-    with _on(idx, stream) as handle:
-        if out is None:
-            out = x.new_empty((N, G, d))
-        if not with_next:
-            next = None
-        elif next is None:
-            next = x.new_empty((N, G, d))
-        _run(la_epilogue(x, w, gate, a, res, scale, w_next, out, next, eps, N, G, d, T, flags, handle))
-    return out, next
+
+    def body(handle):
+        o = x.new_empty((N, G, d)) if out is None else out
+        n = None if not with_next else x.new_empty((N, G, d)) if next is None else next
+        _run("la_epilogue", x.data_ptr(), _at(w), _at(gate), a, _at(res), _at(scale), _at(w_next), o.data_ptr(), _at(n),
+             eps, N, G, d, T, flags, handle)
+        return o, n
+
+    return _launch(idx, stream, body)
 
 
 def epilogue_bwd(x, d_out, w=None, gate=None, act="silu", res=None, scale=None, w_next=None, d_next=None, eps=1e-5,
@@ -366,11 +369,15 @@ def epilogue_bwd(x, d_out, w=None, gate=None, act="silu", res=None, scale=None, 
     flags = _flag(x.dtype)
     _check(d_out, "d_out", x.dtype, (N, G, d), idx)
     _check(d_next, "d_next", x.dtype, (N, G, d), idx)
-    with _on(idx, stream) as handle:
+
+    def body(handle):
         wide = (N, G, d)
         dx, dgate = torch.empty_like(x), None if gate is None else x.new_empty(wide)
         dres = None if res is None else x.new_empty(wide)
         dw, dscale, dw_next = (None if t is None else torch.empty_like(t) for t in (w, scale, w_next))
-        _run(la_epilogue_bwd(x, w, gate, a, res, scale, w_next, d_out, d_next, dx, dgate, dres, dw, dscale, dw_next,
-                             eps, N, G, d, T, flags, handle))
-    return {"dx": dx, "dgate": dgate, "dres": dres, "dw": dw, "dscale": dscale, "dw_next": dw_next}
+        _run("la_epilogue_bwd", x.data_ptr(), _at(w), _at(gate), a, _at(res), _at(scale), _at(w_next), _at(d_out),
+             _at(d_next), dx.data_ptr(), _at(dgate), _at(dres), _at(dw), _at(dscale), _at(dw_next), eps, N, G, d, T, flags,
+             handle)
+        return {"dx": dx, "dgate": dgate, "dres": dres, "dw": dw, "dscale": dscale, "dw_next": dw_next}
+
+    return _launch(idx, stream, body)

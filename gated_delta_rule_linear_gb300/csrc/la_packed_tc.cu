@@ -931,10 +931,12 @@ cudaError_t launch(const PackedPass &p, const Segments &sg, const Maps &m, bool 
   return p.da == 64 ? launch_as<64, STATE, false>(p, sg, m, beside, stream) : launch_as<128, STATE, false>(p, sg, m, beside, stream);
 }
 
-// A split pass against an unsplit one of as many tokens a CTA, and what its further launches cost in
-// tokens of a walk (24 ragged sequences of 12001 tokens, backward: 0.206 ms with 4 chunks, 0.218 with 12).
+// What a split costs: a factor on the pass, and for each pass its further launches, in tokens of a
+// walk. Measured (microseconds, unsplit / split, one sequence of T tokens, 8 heads of 128): forward
+// T = 2048 36 / 40, 3000 50 / 42, 4096 62 / 46, 8192 115 / 57; 2 x 4096 tokens of 16 heads 69 / 88.
+// Backward T = 4096 65 / 106, 8192 122 / 135: its passes overlap, and fill the GPU without a split.
 constexpr double kSplitCost = 1.6;
-constexpr int kSplitTokens = 4 * kN;
+constexpr int kSplitTokens = 16 * kN;
 
 int fail(const char *what, cudaError_t e) {
   set_error("packed retention: %s: %s", what, cudaGetErrorString(e));
@@ -948,8 +950,9 @@ struct Ready {
   size_t owners, plan, states;  // bytes of its workspace behind 256 of counters; plan 0: none
 };
 
-// Maps, split and workspace of a pass; an LA_ERR_* code where it cannot run.
-int make_ready(const PackedPass &p, Ready *r) {
+// Maps, split and workspace of a pass, of passes with `share` tokens for each SM
+// together; an LA_ERR_* code where it cannot run.
+int make_ready(const PackedPass &p, int passes, long long share, Ready *r) {
   if (!make_token_map(&r->m.x, p.x, p.da, p.H / p.rx, p.total, p.ldx, kN) ||
       !make_token_map(&r->m.y, p.y, p.da, p.H / p.ry, p.total, p.ldy, kN) ||
       !make_token_map(&r->m.z, p.z, p.db, p.H / p.rz, p.total, p.ldz, kN)) {
@@ -962,15 +965,15 @@ int make_ready(const PackedPass &p, Ready *r) {
     return LA_ERR_CUDA;
   }
   // Sequences are split into segments where whole ones would leave the GPU to a
-  // few long walks. Unsplit the pass takes as long as its longest sequence; split
-  // it takes its share of the whole, and on top the second reading of Y and Z,
-  // the states' way through memory and two more launches.
+  // few long walks. Unsplit the passes take as long as the longest sequence or
+  // their share of the whole; split they take that share, and on top the second
+  // reading of Y and Z, the states' way through memory and two more launches.
   const long long sms = std::max(1, sm_count());
   const int longest = p.max_len > 0 ? std::min(p.max_len, p.total) : p.total;
-  const long long share = ((long long)p.total * p.H * (p.db / 64) + sms - 1) / sms;  // tokens of a CTA
   r->sg = {0, p.n_seq, nullptr, nullptr, nullptr, nullptr, nullptr};
-  if (longest > kSplitCost * share + kSplitTokens) {
-    const long long seg = std::max<long long>((share + kN - 1) / kN * kN, 2 * kN);
+  if (longest > kSplitCost * share + kSplitTokens * passes) {
+    const long long own = ((long long)p.total * p.H * (p.db / 64) + sms - 1) / sms;
+    const long long seg = std::max<long long>((own + kN - 1) / kN * kN, 2 * kN);
     if (seg < longest) {
       r->sg.tokens = static_cast<int>(seg);
       r->sg.units = static_cast<int>(p.total / seg) + p.n_seq;
@@ -1004,8 +1007,11 @@ int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream) {
   }
   Ready r[3];
   size_t bytes = 0;
+  long long share = 0;
+  for (int i = 0; i < passes; ++i) share += (long long)p[i].total * p[i].H * (p[i].db / 64);
+  share /= std::max(1, sm_count());
   for (int i = 0; i < passes; ++i) {
-    const int rc = make_ready(p[i], &r[i]);
+    const int rc = make_ready(p[i], passes, share, &r[i]);
     if (rc != LA_OK) return rc;
     if (r[i].plan) bytes += 256 + r[i].owners + r[i].plan + r[i].states;
   }

@@ -389,6 +389,29 @@ def test_the_same_every_run():
         assert all(torch.equal(p, q) for p, q in zip(a, la.packed_bwd(*x, cu(lens), "retnet", g=g)))
 
 
+@pytest.mark.parametrize("H,Hk,dk,dv", [(1, 1, 64, 64), (2, 1, 64, 128)])
+def test_backward_of_split_sequences(H, Hk, dk, dv):
+    # long enough that all three passes go by segments
+    check_bwd([8200, 0, 300], H, Hk, dk, dv, BF, seed=26)
+
+
+def test_split_sequences_with_a_pool():
+    lens, H, dk, dv = [3300, 40, 0, 2900], 2, 128, 64
+    q, k, v, _, _, _ = draw(lens, H, 1, dk, dv, BF, 27)
+    pool = torch.randn(6, H, dk, dv, generator=torch.Generator().manual_seed(28))
+    slots = torch.tensor([5, 2, 0, 2], dtype=torch.int32)  # the last one names the second one's row
+    g = gammas(H)
+    start = torch.stack([pool[5], pool[2], pool[0], torch.zeros(H, dk, dv)])
+    S = pool.cuda()
+    o, _ = la.packed_fwd(*up(q, k, v), cu(lens), "retnet", g=g.cuda(), S0=S, S_final=S, slots=slots.cuda())
+    done()
+    want, Sw = retention(q, k, v, g, lens, start)
+    size, Ss = retention(q, k, v, g, lens, start, positive=True)
+    hold(o, want, packed_bound(want, size, 3300, BF), "o")
+    hold(S[[5, 2, 0]], Sw[:3], state_bound(Ss[:3], 3300, BF), "S")
+    assert torch.equal(S[[1, 3, 4]].cpu(), pool[[1, 3, 4]])
+
+
 def test_offsets_past_32_bits():
     # 2^24 tokens of 128 channels: the last sequence's elements lie behind 2^31
     n, tail, d = 1 << 24, 150, 128
