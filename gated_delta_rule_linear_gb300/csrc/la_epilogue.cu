@@ -22,8 +22,8 @@
 // heads of 128, bf16, head-major x: 0.156 ms, 5.15 TB/s; with the 96 registers a
 // thread that the compiler takes unasked, 0.193 (too few threads a SM to cover
 // memory: hence 64 at one load a thread). Backward with residual, scale, sigmoid
-// gate and next norm on 32768 x 2048: 0.270 ms, 3.97 TB/s, bound by issue (about
-// 80 instructions for two channels) and its 2 CTAs of 256 a SM.
+// gate and next norm on 32768 x 2048: 0.252 ms, 4.26 TB/s, bound by issue (about
+// 160 instructions for two channels and both sums) and its 512 threads a SM.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -361,7 +361,7 @@ template <typename T> __device__ __forceinline__ void put_pair(uint4 &u, int j, 
 // was loaded and every value is formed again, pair by pair, where it is needed
 // (twice: for the sums, for the gradients): with the row's values in registers
 // as float32 the next row's loads did not fit beside them, and without those in
-// flight the kernel waited for memory (0.46 ms against 0.27 on 32768 x 2048).
+// flight the kernel waited for memory (0.46 ms against 0.31 on 32768 x 2048).
 // GATE: 0 none, 1 silu, 2 sigmoid; NEXT: with the next norm's gradient; -1: as the arguments say.
 template <typename T, int V, int NV, int GATE, int NEXT>
 __global__ void __launch_bounds__(512, 1) epilogue_bwd_kernel(const EpilogueParams p, const XRows xr, int tpr,
@@ -563,8 +563,10 @@ __global__ void __launch_bounds__(256) partial_sum_kernel(const float *__restric
   }
 }
 
-// CTAs of a SM's share of a grid; the partials of the backward's sums are one a CTA.
-constexpr int kPerSm = 8;
+// Threads of a SM's share of the grid: as many as its registers hold at once. More CTAs only load
+// the weights again and, in the backward, leave more partials to add up (with 2048 threads their
+// sum took 20 of 270 us on 32768 x 2048; with 512 it takes 10 of 252).
+constexpr int kForward = 1024, kBackward = 512;
 
 struct Shape {
   int tpr, nv, threads, blocks;
@@ -575,7 +577,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 // As few threads a row as hold it with one load each, up to 512; rows of up to
 // 64 threads share a CTA of 128.
-Shape shape_of(const EpilogueParams &p) {
+Shape shape_of(const EpilogueParams &p, int resident) {
   Shape s;
   const int V = p.f32 ? 4 : 8;
   s.wide = p.d % V == 0;
@@ -589,7 +591,7 @@ Shape shape_of(const EpilogueParams &p) {
   while (s.tpr * s.nv < loads) s.nv *= 2;
   s.threads = s.tpr < 128 ? 128 : s.tpr;
   const long long rows = (long long)p.N * p.G, rpb = s.threads / s.tpr;
-  const long long most = (long long)sm_count() * std::max(1, std::min(kPerSm, 2048 / s.threads));
+  const long long most = (long long)sm_count() * std::max(1, resident / s.threads);
   const long long want = (rows + rpb - 1) / rpb;
   s.blocks = static_cast<int>(want < most ? want : most);
   return s;
@@ -644,7 +646,7 @@ int fail(const char *fn, const char *what, cudaError_t e) {
 }  // namespace
 
 int launch_epilogue(const EpilogueParams &p, cudaStream_t stream) {
-  const Shape s = shape_of(p);
+  const Shape s = shape_of(p, kForward);
   const cudaError_t e = p.f32 ? launch<float, false>(p, s, nullptr, stream)
                               : launch<__nv_bfloat16, false>(p, s, nullptr, stream);
   return e == cudaSuccess ? LA_OK : fail("la_epilogue", "launch failed", e);
@@ -652,7 +654,7 @@ int launch_epilogue(const EpilogueParams &p, cudaStream_t stream) {
 
 int launch_epilogue_bwd(const EpilogueParams &p, cudaStream_t stream) {
   const char *fn = "la_epilogue_bwd";
-  const Shape s = shape_of(p);
+  const Shape s = shape_of(p, kBackward);
   void *part = nullptr;
   cudaError_t e;
   const bool sums = p.dw || p.dscale || p.dw_next;

@@ -184,7 +184,7 @@ int la_epilogue(const void *x, const float *w, const void *gate, int act, const 
  * d_next if the forward had it, and not read without d_next. Sums over tokens
  * run in a fixed order: the results do not change from run to run. Outputs may
  * not overlap inputs, except dres = d_out. Uses workspace from the library's pool
- * (up to 16*SMs*d*4 bytes) for dw, dscale and dw_next. Other arguments as la_epilogue.
+ * (up to 8*SMs*d*4 bytes) for dw, dscale and dw_next. Other arguments as la_epilogue.
  */
 int la_epilogue_bwd(const void *x, const float *w, const void *gate, int act, const void *res,
                     const float *scale, const float *w_next, const void *d_out, const void *d_next, void *dx,
