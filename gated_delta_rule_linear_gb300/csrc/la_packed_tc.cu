@@ -652,7 +652,7 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
         // gamma^(i+1), reversed gamma^(rows-1-i)
         const float r = tab[p.reverse ? 127 - max(rows - 1 - i, 0) : 128 + i];
         const uint64_t rr = pair(r, r);
-        const bool staged = !OF32 && wq * 32 + 32 <= rows;  // all of the warp's rows: through TMA
+        const bool staged = wq * 32 + 32 <= rows;  // all of the warp's rows: through TMA
         const size_t at = (size_t)t * p.ldo + (size_t)it.h * db + it.v0;
         if (n > 0 && lane == 0) bulk_wait_read<0>();  // the staging rows have been read
         ok = wait_group(&o_full[st], n >> 1);
@@ -667,12 +667,25 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; e += 2) fma2(xs + e, xs + e, rr, pz + e);
-          if constexpr (OF32) {
-            if (i < rows)
+          if constexpr (OF32) {  // 32 columns at a time: a row of the staging tile
+            uint8_t *to = staged ? ot : reinterpret_cast<uint8_t *>(static_cast<float *>(p.out) + at + 32 * (q >> 1));
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[4 * q + e / 4] =
-                    make_float4(xs[e], xs[e + 1], xs[e + 2], xs[e + 3]);
+            for (int e = 0; e < 4; ++e) {
+              const int c = 4 * (q & 1) + e;  // 16 bytes of the row
+              if (i < rows)
+                *reinterpret_cast<float4 *>(to + (staged ? sw128_off(i, 8 * c) : 16u * c)) =
+                    make_float4(xs[4 * e], xs[4 * e + 1], xs[4 * e + 2], xs[4 * e + 3]);
+            }
+            if (q & 1) {
+              if (staged) fence_proxy_async();
+              __syncwarp();
+              if (staged && lane == 0) {
+                tma_store_3d(&tm_o, ot + wq * 32 * 128, it.v0 + 16 * (q - 1), it.h, t);
+                bulk_commit();
+                if (q == 1) bulk_wait_read<0>();
+              }
+              __syncwarp();
+            }
           } else {
             o[2 * q] = pack8(xs);
             o[2 * q + 1] = pack8(xs + 8);
@@ -881,13 +894,15 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(const PackedPass p, i
   }
 }
 
-// [tokens][heads][d] with a token stride, boxes of 64 channels x 1 head x rows.
-bool make_token_map(CUtensorMap *m, const void *base, int d, int heads, int tokens, long long ld, int rows) {
+// [tokens][heads][d] with a token stride, boxes of 128 bytes of channels x 1 head x rows.
+bool make_token_map(CUtensorMap *m, const void *base, bool f32, int d, int heads, int tokens, long long ld, int rows) {
+  const cuuint64_t e = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, es[3] = {1, 1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t strides[2] = {(cuuint64_t)d * e, (cuuint64_t)ld * e};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / e), 1, (cuuint32_t)rows}, es[3] = {1, 1, 1};
+  return g_encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -953,14 +968,13 @@ struct Ready {
 // Maps, split and workspace of a pass, of passes with `share` tokens for each SM
 // together; an LA_ERR_* code where it cannot run.
 int make_ready(const PackedPass &p, int passes, long long share, Ready *r) {
-  if (!make_token_map(&r->m.x, p.x, p.da, p.H / p.rx, p.total, p.ldx, kN) ||
-      !make_token_map(&r->m.y, p.y, p.da, p.H / p.ry, p.total, p.ldy, kN) ||
-      !make_token_map(&r->m.z, p.z, p.db, p.H / p.rz, p.total, p.ldz, kN)) {
+  if (!make_token_map(&r->m.x, p.x, false, p.da, p.H / p.rx, p.total, p.ldx, kN) ||
+      !make_token_map(&r->m.y, p.y, false, p.da, p.H / p.ry, p.total, p.ldy, kN) ||
+      !make_token_map(&r->m.z, p.z, false, p.db, p.H / p.rz, p.total, p.ldz, kN)) {
     set_error("packed retention: tensor map encoding failed");
     return LA_ERR_CUDA;
   }
-  r->m.o = r->m.x;
-  if (!p.out_f32 && !make_token_map(&r->m.o, p.out, p.db, p.H, p.total, p.ldo, 32)) {
+  if (!make_token_map(&r->m.o, p.out, p.out_f32, p.db, p.H, p.total, p.ldo, 32)) {
     set_error("packed retention: tensor map encoding failed");
     return LA_ERR_CUDA;
   }
