@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs)
         const int t0 = a + k * seg, t1 = seg ? min(b, t0 + seg) : b;
         const int bucket = kBuckets - 1 - min(chunks_of(t1 - t0), kBuckets - 1);
         const int at = atomicAdd(first + bucket, 1);
-        if (pass) plan[at] = {t0, t1, u0 + k, 4 * row + 2 * (n == 1) + (p.reverse ? k == 0 : k == n - 1)};
+        // (more than `units` only where sequences overlap, as they should not)
+        if (pass && at < units) plan[at] = {t0, t1, u0 + k, 4 * row + 2 * (n == 1) + (p.reverse ? k == 0 : k == n - 1)};
       }
     }
     __syncthreads();
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs)
     __syncthreads();
     x += tid >= 32 ? warp_sum[(tid >> 5) - 1] : 0;
     first[tid] = x - v;
-    if (tid == kPlanThreads - 1) head[2] = x;
+    if (tid == kPlanThreads - 1) head[2] = min(x, units);
     __syncthreads();
   }
 }

@@ -412,6 +412,31 @@ def test_split_sequences_with_a_pool():
     assert torch.equal(S[[1, 3, 4]].cpu(), pool[[1, 3, 4]])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lengths_that_are_not_what_they_should_be(dtype):
+    # bounds outside the tokens are clamped, a decreasing one makes an empty sequence: [0,300), none, [100,700), none
+    q, k, v, dO, _, _ = draw([700], 2, 1, 64, 64, dtype, 29)
+    c = torch.tensor([-7, 300, 100, 2000, 650], dtype=torch.int32).cuda()
+    g = gammas(2)
+    args = up(q, k, v, dO)
+    o, S = la.packed_fwd(*args[:3], c, "retnet", g=g.cuda())
+    got = la.packed_bwd(*args, c, "retnet", g=g.cuda())
+    done()
+    part = (q[100:], k[100:], v[100:], g, [600])
+    want, size = (retention(*part, positive=p)[0][200:] for p in (False, True))
+    hold(o[300:], want, packed_bound(want, size, 600, dtype), "o")  # rows of one sequence only
+    assert (S[[1, 3]] == 0).all() and all(t.shape for t in got)
+    # the same long sequence several times over: more segments than there is room for
+    n = 6000
+    q, k, v, dO, _, _ = draw([n], 1, 1, 64, 64, dtype, 30)
+    args = up(q, k, v, dO)
+    again = torch.tensor([0, n, 0, n, 0, n], dtype=torch.int32).cuda()
+    la.packed_fwd(*args[:3], again, "retnet", g=g[:1].cuda())
+    la.packed_bwd(*args, again, "retnet", g=g[:1].cuda())
+    done()
+    check_fwd([1500, 1], 1, 1, 64, 64, dtype, seed=31)
+
+
 def test_offsets_past_32_bits():
     # 2^24 tokens of 128 channels: the last sequence's elements lie behind 2^31
     n, tail, d = 1 << 24, 150, 128
