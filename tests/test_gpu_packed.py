@@ -368,6 +368,33 @@ def test_streams_and_graphs():
     done()
 
 
+@pytest.mark.parametrize("lens,H,Hk", [([130, 70, 1], 64, 32), ([8200, 300], 1, 1)])
+def test_captured_with_workspaces(lens, H, Hk):
+    # calls that plan and split their work, captured: allocations, overlapping passes and head sums replayed
+    a, b = (up(*draw(lens, H, Hk, 64, 64, BF, seed)[:4]) for seed in (32, 33))
+    g, c = gammas(H).cuda(), cu(lens)
+
+    def both(x):
+        o, S = la.packed_fwd(*x[:3], c, "retnet", g=g)
+        return [o, S, *la.packed_bwd(*x, c, "retnet", g=g)]
+
+    want = {0: both(a), 1: both(b)}
+    live = [t.clone() for t in a]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = both(live)
+    for k, x in ((1, b), (0, a), (1, b)):
+        for t, u in zip(live, x):
+            t.copy_(u)
+        graph.replay()
+        eager = both(a)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(res, want[k]))
+        assert all(torch.equal(p, q) for p, q in zip(eager, want[0]))
+    done()
+
+
 def test_a_stream_argument():
     lens, H = [300], 2
     x = up(*draw(lens, H, 2, 64, 64, BF, 21)[:3])
