@@ -2,6 +2,7 @@
 // the workspaces of the layer operators.
 #include <climits>
 #include <cmath>
+#include <initializer_list>
 
 #include "la_layer_internal.h"
 
@@ -10,6 +11,18 @@ using namespace la;
 namespace {
 
 bool at(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// An output that is one of the inputs, or another output. (Tensors that overlap in part are not looked for.)
+bool same(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    for (const void *i : ins)
+      if (*o == i) return true;
+    for (auto u = outs.begin(); u != o; ++u)
+      if (*o == *u) return true;
+  }
+  return false;
+}
 
 int bad(const char *fn, const char *what) {
   set_error("%s: %s", fn, what);
@@ -77,6 +90,7 @@ int la_packed_fwd(const void *q, const void *k, const void *v, const float *g, v
     return bad(fn, "tensors must be 16-byte aligned");
   if ((S0 || S_final) && (n_slots < 0 || (!slots && n_slots < n_seq)))
     return bad(fn, "n_slots must be >= 0, and >= n_seq without slots");
+  if (total > 0 && same({o}, {q, k, v})) return bad(fn, "o must not be an input");
   unsigned *status = status_word();
   if (!status) {
     set_error("%s: no CUDA device available (%s)", fn, cudaGetErrorString(cudaGetLastError()));
@@ -110,6 +124,8 @@ int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, c
   const void *all[] = {q, k, v, dO, S0, dS_final, dq, dk_out, dv_out, dS0};
   for (const void *t : all)
     if (!at(t, 16)) return bad(fn, "tensors must be 16-byte aligned");
+  if ((total > 0 && same({dq, dk_out, dv_out}, {q, k, v, dO})) || same({dS0}, {S0, dS_final}))
+    return bad(fn, "outputs must not be inputs, nor one another");
   unsigned *status = status_word();
   if (!status) {
     set_error("%s: no CUDA device available (%s)", fn, cudaGetErrorString(cudaGetLastError()));
@@ -188,6 +204,7 @@ int la_packed_step(const void *q, const void *k, const void *v, const float *g, 
   if (!q || !k || !v || !o || !S) return bad(fn, "q, k, v, o and S are required");
   if (!at(q, 16) || !at(k, 16) || !at(v, 16) || !at(o, 16) || !at(S, 16) || !at(slots, 4))
     return bad(fn, "tensors must be 16-byte aligned, slots 4-byte aligned");
+  if (same({o}, {q, k, v})) return bad(fn, "o must not be an input");
   const PackedStep p = {q, k, v, o, S, g, slots, n, n_slots, H, Hk, dk, dv, (mode & LA_F32) ? 1 : 0, ldq, ldk, ldv};
   return launch_packed_step(p, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -224,6 +241,8 @@ int la_rotary(const void *q, const void *k, void *q_out, void *k_out, const int 
   const bool same_k = T_in == T_out && (T_in || ldk == (long long)Hk * d);
   if ((q == q_out && !same_q) || (k && k == k_out && !same_k))
     return bad(fn, "an output may be its input only with the same layout and strides");
+  if (same({q_out, k_out}, {}) || (k && (q_out == k || k_out == q)))
+    return bad(fn, "q_out and k_out are two tensors, and not each other's input");
   RotaryParams p = {q, k, q_out, k_out, pos, freq, n_axes, s0, s1, s2, N, H, k ? Hk : 0, d, T_in, T_out,
                     ldq, k ? ldk : 0, scale_q, scale_k, (flags & LA_ROT_INTERLEAVED) ? 1 : 0,
                     (flags & LA_ROT_INVERSE) ? 1 : 0, (flags & LA_F32) ? 1 : 0};
@@ -294,6 +313,9 @@ int la_epilogue_bwd(const void *x, const float *w, const void *gate, int act, co
   if (!x || (!d_out && !d_next)) return bad(fn, "x and one of d_out and d_next are required");
   if (dgate && !gate) return bad(fn, "dgate needs gate");
   if ((dw_next || w_next) && !d_next) return bad(fn, "w_next and dw_next need d_next");
+  if (same({dx, dgate, dres}, {x, gate, res, d_next}) || same({dx, dgate}, {d_out}) ||
+      same({dw, dscale, dw_next}, {w, scale, w_next}))
+    return bad(fn, "outputs must not be inputs, nor one another; dres may be d_out");
   return launch_epilogue_bwd(p, s);
 }
 

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs)
 constexpr uint32_t kTile = 16384;
 constexpr uint32_t kSmX = 0, kSmY = kSmX + 4 * kTile, kSmZ = kSmY + 4 * kTile, kSmW = kSmZ + 2 * kTile,
                    kSmS = kSmW + 2 * kTile, kSmO = kSmS + kTile, kSmMisc = kSmO + kTile,
-                   kSmBytes = kSmMisc + 3072;
+                   kSmBytes = kSmMisc + 3 * 1024;
 constexpr int kRing = 4;  // items known ahead
 // TMEM columns: two buffers of scores, over which go P (columns 0..63) and P Z (64..127),
 // two of X S, and dS of Z' high and low.

@@ -175,7 +175,7 @@ cudaError_t launch(const RotaryParams &p, cudaStream_t stream) {
   while (tokens < 8 && (long long)tokens * items * heads < 8 * kThreads && p.N / (2 * tokens) >= 8 * sms) tokens *= 2;
   const RotaryDiv by = {FastDiv(items), FastDiv(heads), FastDiv(p.T_in > 0 ? p.T_in : 1),
                         FastDiv(p.T_out > 0 ? p.T_out : 1), FastDiv(P)};
-  const int grid = (p.N + tokens - 1) / tokens;
+  const int grid = (p.N - 1) / tokens + 1;  // N >= 1, up to INT_MAX
   const size_t smem = (size_t)tokens * P * sizeof(float2);
   if (wide && p.interleaved) rotary_kernel<T, V, true><<<grid, kThreads, smem, stream>>>(p, by, tokens);
   else if (wide) rotary_kernel<T, V, false><<<grid, kThreads, smem, stream>>>(p, by, tokens);

@@ -38,7 +38,8 @@ extern "C" {
  *   v       [total][H][dv] token-major, token stride ldv; value head h uses
  *           query/key head h / (H / Hk) (H a multiple of Hk)
  *   g       float32 [H], log gamma_h (LA_RETNET), or NULL (LA_LINEAR)
- *   o       [total][H][dv], dense; rows of tokens in no sequence are not written
+ *   o       [total][H][dv], dense, overlaps no input; rows of tokens in no
+ *           sequence are not written
  *   cu_seqlens  int32 [n_seq + 1], device: sequence s is the tokens
  *           cu_seqlens[s] .. cu_seqlens[s+1] - 1; non-decreasing within
  *           [0, total] (values outside are clamped: memory-safe, not an
@@ -87,7 +88,7 @@ int la_packed_fwd(const void *q, const void *k, const void *v, const float *g, v
  *   dq, dk_out [total][Hk][dk]; dv_out [total][H][dv]: outputs, dense, input
  *           dtype; rows of tokens in no sequence are not written
  *   dS0     float32 [n_seq][H][dk][dv] or NULL (not computed)
- *   Outputs overlap no input. 16-byte alignment for every tensor.
+ *   Outputs overlap no input and not each other. 16-byte alignment for every tensor.
  * Runs as three passes of la_packed_fwd's kernel with the tensors' places
  * exchanged (dk, dv: from the last token to the first), each with that
  * function's workspace, and with shared heads another 8*total*H*dk bytes.
@@ -103,7 +104,7 @@ int la_packed_bwd(const void *q, const void *k, const void *v, const float *g, c
  * place, and o_i = S^T q_i.
  *
  *   q, k    [n][Hk][dk], v [n][H][dv] token-major (strides ldq, ldk, ldv);
- *   o       [n][H][dv] dense
+ *   o       [n][H][dv] dense, overlaps no input
  *   S       float32 [n_slots][H][dk][dv], 16-byte aligned
  *   slots   int32 [n], device, or NULL (row i; then n <= n_slots). A slot
  *           outside [0, n_slots) is a padding row: o_i = 0, no state is
@@ -129,7 +130,8 @@ int la_packed_step(const void *q, const void *k, const void *v, const float *g, 
  *           T_in = 0: token-major inputs (token strides ldq, ldk);
  *           T_in > 0: head-major inputs [N/T_in][heads][T_in][d] (ld* ignored)
  *           T_out likewise for the dense outputs; N a multiple of T_in, T_out.
- *           An output may be its input if both have the same layout and strides.
+ *           An output may be its own input if both have the same layout and
+ *           strides; outputs do not overlap otherwise.
  *   pos     int32 [N][n_axes], device; any int32 value
  *   freq    float64 [P], device: radians per position. Angles are formed in
  *           64-bit fixed point, so far positions keep float32 accuracy.

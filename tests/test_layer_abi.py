@@ -173,6 +173,35 @@ def test_epilogue_bwd_refusals(kw, code):
                                     flags=0, stream=None), kw, code)
 
 
+SHAPE = dict(H=4, Hk=2, dk=128, dv=128, ldq=256, ldk=256, ldv=512, mode=0, stream=None)
+APART = {
+    "la_packed_fwd": dict(q=A, k=2 * A, v=3 * A, g=None, o=4 * A, S0=5 * A, S_final=5 * A, cu_seqlens=6 * A, slots=None,
+                          n_seq=3, total=64, max_len=0, n_slots=3, **SHAPE),
+    "la_packed_bwd": dict(q=A, k=2 * A, v=3 * A, g=None, dO=4 * A, S0=5 * A, dS_final=6 * A, dq=7 * A, dk_out=8 * A,
+                          dv_out=9 * A, dS0=10 * A, cu_seqlens=11 * A, n_seq=3, total=64, max_len=0, **SHAPE),
+    "la_packed_step": dict(q=A, k=2 * A, v=3 * A, g=None, o=4 * A, S=5 * A, slots=None, n=4, n_slots=4, **SHAPE),
+    "la_rotary": dict(q=A, k=2 * A, q_out=3 * A, k_out=4 * A, pos=5 * A, freq=6 * A, n_axes=1, s0=32, s1=0, s2=0, N=8,
+                      H=1, Hk=1, d=64, T_in=0, T_out=0, ldq=64, ldk=64, scale_q=1.0, scale_k=1.0, flags=0, stream=None),
+    "la_epilogue_bwd": dict(x=A, w=2 * A, gate=3 * A, act=0, res=4 * A, scale=5 * A, w_next=6 * A, d_out=7 * A,
+                            d_next=8 * A, dx=9 * A, dgate=10 * A, dres=11 * A, dw=12 * A, dscale=13 * A, dw_next=14 * A,
+                            eps=1e-5, N=8, G=2, d=64, T=0, flags=0, stream=None),
+}
+
+
+@pytest.mark.parametrize("fn,out,other", [
+    ("la_packed_fwd", "o", "q"), ("la_packed_fwd", "o", "k"), ("la_packed_fwd", "o", "v"),
+    ("la_packed_bwd", "dq", "q"), ("la_packed_bwd", "dk_out", "v"), ("la_packed_bwd", "dv_out", "dO"),
+    ("la_packed_bwd", "dq", "dk_out"), ("la_packed_bwd", "dS0", "dS_final"), ("la_packed_bwd", "dS0", "S0"),
+    ("la_packed_step", "o", "q"), ("la_packed_step", "o", "v"),
+    ("la_rotary", "q_out", "k"), ("la_rotary", "k_out", "q"), ("la_rotary", "q_out", "k_out"),
+    ("la_epilogue_bwd", "dx", "x"), ("la_epilogue_bwd", "dx", "d_out"), ("la_epilogue_bwd", "dgate", "gate"),
+    ("la_epilogue_bwd", "dres", "d_next"), ("la_epilogue_bwd", "dres", "dx"), ("la_epilogue_bwd", "dw", "w"),
+    ("la_epilogue_bwd", "dscale", "dw_next"),
+])
+def test_an_output_is_no_input(fn, out, other):
+    refused(fn, APART[fn], {out: APART[fn][other]}, "LA_ERR_INVALID_ARG")
+
+
 def test_wrappers_refuse_cpu_tensors():
     import torch
     x = torch.zeros(4, 2, 64)
