@@ -81,8 +81,10 @@ __global__ void __launch_bounds__(128) packed_walk_kernel(const PackedPass p) {
     for (int c = 0; c < R; ++c) p.S_out[sbase + (size_t)(c0 + c) * p.db + col] = S[c];
 }
 
-// Gradients of shared heads: the float32 parts of the heads that use one. Tokens in front of
-// the first sequence and behind the last have no parts, and their rows stay as they are.
+// Gradients of shared heads: the float32 parts of the heads that use one. Tokens of no sequence have
+// no parts, and their rows stay as they are. The sequences in use are one run of tokens, and what is
+// behind them empty, a padded batch's zeros included: cu_seqlens does not fall before the last of
+// them. Where it does, every sequence is summed for itself.
 template <typename T>
 __global__ void __launch_bounds__(256) head_sum_kernel(const float *__restrict__ src0, T *__restrict__ dst0,
                                                        const float *__restrict__ src1, T *__restrict__ dst1,
@@ -91,22 +93,39 @@ __global__ void __launch_bounds__(256) head_sum_kernel(const float *__restrict__
   const float *src = blockIdx.y ? src1 : src0;
   T *dst = blockIdx.y ? dst1 : dst0;
   const int dq = d / 4;
-  const long long a = min(max(__ldg(cu), 0), total), b = min(max(__ldg(cu + n_seq), 0), total), row = (long long)heads * dq;
-  for (long long i = a * row + blockIdx.x * 256LL + threadIdx.x; i < b * row; i += gridDim.x * 256LL) {
-    const long long at = i / dq;  // (token, shared head)
-    const int c = static_cast<int>(i % dq);
-    const float4 *s = reinterpret_cast<const float4 *>(src + at * share * d) + c;
-    float4 t = __ldcs(s);
-    for (int j = 1; j < share; ++j) {
-      const float4 u = __ldcs(s + (size_t)j * dq);
-      t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+  const long long row = (long long)heads * dq;
+  auto sum = [&](int a, int b) {
+    for (long long i = a * row + blockIdx.x * 256LL + threadIdx.x; i < b * row; i += gridDim.x * 256LL) {
+      const long long at = i / dq;  // (token, shared head)
+      const int c = static_cast<int>(i % dq);
+      const float4 *s = reinterpret_cast<const float4 *>(src + at * share * d) + c;
+      float4 t = __ldcs(s);
+      for (int j = 1; j < share; ++j) {
+        const float4 u = __ldcs(s + (size_t)j * dq);
+        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+      }
+      if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4 *>(dst)[i] = t;
+      } else {
+        __nv_bfloat162 u[2] = {__floats2bfloat162_rn(t.x, t.y), __floats2bfloat162_rn(t.z, t.w)};
+        reinterpret_cast<uint2 *>(dst)[i] = *reinterpret_cast<uint2 *>(u);
+      }
     }
-    if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<float4 *>(dst)[i] = t;
-    } else {
-      __nv_bfloat162 u[2] = {__floats2bfloat162_rn(t.x, t.y), __floats2bfloat162_rn(t.z, t.w)};
-      reinterpret_cast<uint2 *>(dst)[i] = *reinterpret_cast<uint2 *>(u);
-    }
+  };
+  __shared__ int falls, last;  // the first bound behind which they fall, the last sequence with a token
+  if (threadIdx.x == 0) falls = n_seq, last = -1;
+  __syncthreads();
+  auto bound = [&](int s) { return min(max(__ldg(cu + s), 0), total); };
+  for (int s = threadIdx.x; s < n_seq; s += 256) {
+    const int a = bound(s), b = bound(s + 1);
+    if (b < a) atomicMin(&falls, s);
+    if (b > a) atomicMax(&last, s);
+  }
+  __syncthreads();
+  if (last < falls) {
+    sum(bound(0), bound(falls));
+  } else {
+    for (int s = 0; s <= last; ++s) sum(bound(s), max(bound(s), bound(s + 1)));
   }
 }
 
@@ -133,8 +152,9 @@ int launch_head_sums(const float *const src[2], void *const dst[2], int f32, con
                      int Hk, int share, int d, cudaStream_t stream) {
   const long long quads = (long long)total * Hk * (d / 4);
   if (quads == 0) return LA_OK;
-  const long long want = (quads + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(want < 16384 ? want : 16384), 2);
+  // as many CTAs as are resident: each looks through the bounds once
+  const long long want = (quads + 255) / 256, most = 5LL * (sm_count() > 0 ? sm_count() : 1);
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most), 2);
   if (f32)
     head_sum_kernel<<<grid, 256, 0, stream>>>(src[0], static_cast<float *>(dst[0]), src[1], static_cast<float *>(dst[1]),
                                               cu, n_seq, total, Hk, share, d);

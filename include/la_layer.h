@@ -42,8 +42,10 @@ extern "C" {
  *           sequence are not written
  *   cu_seqlens  int32 [n_seq + 1], device: sequence s is the tokens
  *           cu_seqlens[s] .. cu_seqlens[s+1] - 1; non-decreasing within
- *           [0, total] (values outside are clamped: memory-safe, not an
- *           error). Sequences may be empty.
+ *           [0, total] (values outside are clamped, and a bound below the one
+ *           before it ends an empty sequence: memory-safe, not an error).
+ *           Sequences may be empty; the unused end of a padded batch may
+ *           repeat the last bound or hold zeros.
  *   S0, S_final  float32 [n_slots][H][dk][dv] or NULL (zero / not written);
  *           S_final may be S0. An empty sequence's S_final is its S0.
  *   slots   int32 [n_seq], device: sequence s starts from S0[slots[s]] and

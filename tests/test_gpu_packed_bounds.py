@@ -1,0 +1,83 @@
+"""Packed retention on the GPU where a call's bounds are unusual: padded
+and decreasing cu_seqlens."""
+import pytest
+import torch
+
+import gated_delta_rule_linear_gb300 as la
+from layerlib import gammas, hold, packed_bound, retention, retention_bwd, starts, state_bound
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def cu(lens):
+    return torch.tensor(starts(lens), dtype=torch.int32).cuda()
+
+
+def up(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+def done():
+    assert la.la_stream_status(torch.cuda.current_stream().cuda_stream) == 0
+
+
+def draw(N, n, H, Hk, dk, dv, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen) * dk ** -0.5  # noqa: E731
+    q, k, v, dO = r(N, Hk, dk), r(N, Hk, dk), r(N, H, dv), r(N, H, dv)
+    return [t.to(dtype) for t in (q, k, v, dO)] + [r(n, H, dk, dv), r(n, H, dk, dv)]
+
+
+def raw_bwd(args, g, c, n, dtype):
+    """dq, dk, dv into buffers of fives."""
+    q, k, v, dO = args
+    (N, Hk, dk), (_, H, dv) = q.shape, v.shape
+    outs = [torch.full((N, h, d), 5.0, dtype=dtype, device="cuda") for h, d in ((Hk, dk), (Hk, dk), (H, dv))]
+    mode = la.MODE_IDS["retnet"] | (la.LA_F32 if dtype == F32 else 0)
+    assert la.la_packed_bwd(q, k, v, g, dO, None, None, *outs, None, c, n, N, 0, H, Hk, dk, dv, Hk * dk, Hk * dk, H * dv,
+                            mode, torch.cuda.current_stream().cuda_stream) == 0
+    done()
+    return outs
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (2, 1)])
+def test_gradients_of_a_padded_batch(H, Hk, dtype):
+    # a batch of fixed size with three sequences in use, the rest of cu_seqlens zero: empty sequences
+    lens, back = [60, 0, 140], 25
+    N = sum(lens) + back
+    q, k, v, dO, _, _ = draw(N, 1, H, Hk, 64, 64, dtype, 42)
+    c = torch.tensor([0, 60, 60, 200, 0, 0, 0], dtype=torch.int32).cuda()
+    g = gammas(H)
+    got = raw_bwd(up(q, k, v, dO), g.cuda(), c, 6, dtype)
+    part = [t[:200] for t in (q, k, v, dO)]
+    want, size = (retention_bwd(*part, g, lens, positive=p) for p in (False, True))
+    for name, a, b, e in zip(("dq", "dk", "dv"), got, want, size):
+        hold(a[:200], b, packed_bound(b, e, 140, dtype), name)
+        assert (a[200:] == 5.0).all(), name
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (2, 1)])
+def test_gradients_with_decreasing_bounds(H, Hk, dtype):
+    # clamped into [0, 700]: [0, 300), none, [100, 700), none. Rows of one sequence are that sequence's.
+    q, k, v, dO, _, _ = draw(700, 1, H, Hk, 64, 64, dtype, 43)
+    g = gammas(H)
+    got = raw_bwd(up(q, k, v, dO), g.cuda(), torch.tensor([-7, 300, 100, 2000, 650], dtype=torch.int32).cuda(), 4, dtype)
+    for a, b, rows in ((0, 300, slice(0, 100)), (100, 700, slice(300, 700))):
+        part = [t[a:b] for t in (q, k, v, dO)]
+        want, size = (retention_bwd(*part, g, [b - a], positive=p) for p in (False, True))
+        inner = slice(rows.start - a, rows.stop - a)
+        for name, t, w, e in zip(("dq", "dk", "dv"), got, want, size):
+            hold(t[rows], w[inner], packed_bound(w, e, 600, dtype)[inner], f"{name} of [{a}, {b})")
+    # [400, 500) and [50, 250): the rows between them are nobody's
+    got = raw_bwd(up(q, k, v, dO), g.cuda(), torch.tensor([400, 500, 50, 250], dtype=torch.int32).cuda(), 3, dtype)
+    for a, b in ((400, 500), (50, 250)):
+        part = [t[a:b] for t in (q, k, v, dO)]
+        want, size = (retention_bwd(*part, g, [b - a], positive=p) for p in (False, True))
+        for name, t, w, e in zip(("dq", "dk", "dv"), got, want, size):
+            hold(t[a:b], w, packed_bound(w, e, 200, dtype), f"{name} of [{a}, {b})")
+    for t in got:
+        assert (t[:50] == 5.0).all() and (t[250:400] == 5.0).all() and (t[500:] == 5.0).all()
