@@ -1,5 +1,5 @@
-"""Packed retention on the GPU where a call's bounds are unusual: padded
-and decreasing cu_seqlens."""
+"""Packed retention on the GPU where a call's bounds are unusual: batches of many short
+sequences, padded and decreasing cu_seqlens, values at the end of the range."""
 import pytest
 import torch
 
@@ -81,3 +81,30 @@ def test_gradients_with_decreasing_bounds(H, Hk, dtype):
             hold(t[a:b], w, packed_bound(w, e, 200, dtype), f"{name} of [{a}, {b})")
     for t in got:
         assert (t[:50] == 5.0).all() and (t[250:400] == 5.0).all() and (t[500:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_products_of_tokens_that_do_not_see_each_other(dtype):
+    # Tokens 10 and 20 hold values whose product is beyond float32, the others ones whose products with
+    # them are of order one. Neither sees the other (10 comes first), so that every result is finite.
+    n, H, d = 100, 2, 64
+    g = gammas(H)
+    for pair in ("qk", "vd"):  # q_10 . k_20, and dO_10 . v_20
+        q, k, v, dO, _, _ = draw(n, 1, H, H, d, d, F32, 44)
+        first, second = (q, k) if pair == "qk" else (dO, v)
+        for t, far in ((first, 10), (second, 20)):
+            scale = torch.full((n, 1, 1), 2.0 ** -70)
+            scale[far] = 2.0 ** 70
+            t *= scale
+        q, k, v, dO = (t.to(dtype) for t in (q, k, v, dO))
+        args = up(q, k, v, dO)
+        o, S = la.packed_fwd(*args[:3], cu([n]), "retnet", g=g.cuda())
+        got = la.packed_bwd(*args, cu([n]), "retnet", g=g.cuda())
+        done()
+        (want, Sw), (size, Ss) = (retention(q, k, v, g, [n], positive=p) for p in (False, True))
+        hold(o, want, packed_bound(want, size, n, dtype), f"o, {pair}")
+        hold(S, Sw, state_bound(Ss, n, dtype), f"S, {pair}")
+        want, size = (retention_bwd(q, k, v, dO, g, [n], positive=p) for p in (False, True))
+        for name, a, b, e in zip(("dq", "dk", "dv"), got, want, size):
+            hold(a, b, packed_bound(b, e, n, dtype), f"{name}, {pair}")
+        hold(got[3], want[3], state_bound(size[3], n, dtype), f"dS0, {pair}")
