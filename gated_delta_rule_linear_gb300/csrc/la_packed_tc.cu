@@ -16,8 +16,9 @@
 // work is a unit, a head and 64 value columns. One CTA a SM takes items from a
 // queue, the longest first, and the roles below go from one item's last chunk to
 // the next one's first without draining. Sequences longer than the segment first
-// go through the same kernel with STATE set, which only forms each segment's
-// own contribution to the state, and a scan over the segments. Unit u of
+// go through the same kernel with STATE set, which only forms each segment's own
+// contribution to the state (the last one's is not asked for), and a scan over
+// the segments. Unit u of
 // sequence s are the numbers from floor(cu[s]/seg) + s on: enough for its
 // segments, and increasing in s.
 //
@@ -86,11 +87,17 @@ struct Unit {
   int t0, t1, u, row;
 };
 
+// A sequence of more than one unit: tokens [a, b), its first unit's number, its state row or -1.
+struct Split {
+  int a, b, u, row;
+};
+
 struct Segments {
   int tokens;        // of a segment; 0: every sequence is one unit
-  int units;         // sequences, or the numbers units may have
-  const Unit *plan;  // units with something to do, the longest first, or null: unit u is sequence u, one item a CTA
-  const int *count;  // how many
+  int units;         // sequences, or the numbers units may have; STATE: the most segments with a state to form
+  const Unit *plan;  // units with something to do, the longest first (STATE: those segments, in any order), or null:
+                     // unit u is sequence u, one item a CTA
+  const int *count;  // how many of them
   unsigned *queue;   // next item for a CTA that is done, from zero
   const float *in;   // [unit][H][dk][dv] entering states of split sequences; the others': S_in by row
   float *out;        // STATE: the segments' own contributions
@@ -110,15 +117,20 @@ __device__ __forceinline__ int chunks_of(int tokens) { return (tokens + kN - 1) 
 
 // Where a long walk is left for the end the other SMs wait for it: the plan
 // lists the units from the longest down (a counting sort over their chunks; the
-// order of equal ones is arbitrary, and no result goes by it). One CTA a pass;
-// clears the queues on the way.
+// order of equal ones is arbitrary, and no result goes by it). Split sequences
+// and those of their segments whose state the others start from stand in lists
+// of their own, so that the passes over them do not go by the number of
+// sequences. One CTA a pass; clears the queues on the way.
 constexpr int kPlanThreads = 1024, kBuckets = 1024;
+// Words of `head`: queue and count of the state kernel, queue and count of the main one, split sequences.
+constexpr int kStateQueue = 0, kMainQueue = 1, kUnitCount = 2, kSegmentCount = 3, kSplitCount = 4;
 struct PlanJob {
   PackedPass p;
-  int seg, units;
+  int seg, units, most;  // most: segments with a state to form, no more than total / seg
   unsigned *head;
   int *owner;
-  Unit *plan;
+  Unit *plan, *segments;
+  Split *splits;
 };
 struct PlanJobs {
   PlanJob job[3];
@@ -128,11 +140,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs)
   const int seg = jobs.job[blockIdx.x].seg, units = jobs.job[blockIdx.x].units;
   unsigned *head = jobs.job[blockIdx.x].head;
   int *owner = jobs.job[blockIdx.x].owner;
-  Unit *plan = jobs.job[blockIdx.x].plan;
+  const int most = jobs.job[blockIdx.x].most;
+  Unit *plan = jobs.job[blockIdx.x].plan, *segments = jobs.job[blockIdx.x].segments;
+  Split *splits = jobs.job[blockIdx.x].splits;
   __shared__ int first[kBuckets];
   __shared__ int warp_sum[32];
+  __shared__ unsigned long long taken;  // segments given out
+  __shared__ int split, end;            // split sequences; where there was no more room for their segments
   const int tid = threadIdx.x;
   if (tid < 2) head[tid] = 0;
+  if (tid == 0) taken = split = 0, end = most;
   first[tid] = 0;
   const bool rows = p.S_in || p.S_out;
   if (rows && p.slots) {  // of sequences that name the same row the first one has it
@@ -159,16 +176,33 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs)
       }
       if (b == a && !(p.S_out && row >= 0)) continue;  // nothing to do
       if (u0 + n > units) continue;                    // only where cu_seqlens is not what it should be
+      bool room = true;                                // (none only where sequences overlap, as they should not)
+      int formed = 0;                                  // first of its segments whose state the others start from
+      if (pass && n > 1) {
+        const unsigned long long at = atomicAdd(&taken, n - 1ull);
+        room = at + (n - 1) <= most;
+        formed = static_cast<int>(min(at, static_cast<unsigned long long>(most)));
+        if (room) splits[atomicAdd(&split, 1)] = {a, b, u0, row};
+        else atomicMin(&end, formed);
+      }
       for (int k = 0; k < n; ++k) {
         const int t0 = a + k * seg, t1 = seg ? min(b, t0 + seg) : b;
         const int bucket = kBuckets - 1 - min(chunks_of(t1 - t0), kBuckets - 1);
         const int at = atomicAdd(first + bucket, 1);
-        // (more than `units` only where sequences overlap, as they should not)
-        if (pass && at < units) plan[at] = {t0, t1, u0 + k, 4 * row + 2 * (n == 1) + (p.reverse ? k == 0 : k == n - 1)};
+        const bool leaves = p.reverse ? k == 0 : k == n - 1;
+        if (!pass) continue;
+        if (!leaves && room) segments[formed++] = {t0, t1, u0 + k, 0};
+        if (static_cast<unsigned>(at) < static_cast<unsigned>(units)) {
+          if (room) plan[at] = {t0, t1, u0 + k, 4 * row + 2 * (n == 1) + leaves};
+          else plan[at] = {a, a, 0, -1};  // no tokens, no state
+        }
       }
     }
     __syncthreads();
-    if (pass) break;
+    if (pass) {
+      if (tid == 0) head[kSegmentCount] = min(taken, static_cast<unsigned long long>(end)), head[kSplitCount] = split;
+      break;
+    }
     // exclusive prefix sums of the buckets
     int v = first[tid], x = v;
     for (int o = 1; o < 32; o <<= 1) {
@@ -188,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs)
     __syncthreads();
     x += tid >= 32 ? warp_sum[(tid >> 5) - 1] : 0;
     first[tid] = x - v;
-    if (tid == kPlanThreads - 1) head[2] = min(x, units);
+    if (tid == kPlanThreads - 1) head[kUnitCount] = min(x, units);
     __syncthreads();
   }
 }
@@ -371,11 +405,6 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
         un.row = __shfl_sync(0xffffffffu, un.row, 0);
       };
       for (int k = 0; ok; ++k) {
-        // a sequence's last state is not needed from the state kernel: the main one forms it
-        while (STATE && w < items && (un.row & 1)) {
-          if (lane == 0) advance();
-          share();
-        }
         Item it;
         bool found = w < items;
         if (found) {
@@ -866,14 +895,12 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
 
 // The entering state of every segment from the segments' own contributions, in
 // place: a running sum per element, the loads of a few segments ahead in flight.
-__global__ void __launch_bounds__(256) segment_scan_kernel(const PackedPass p, int seg, int units, float *ws) {
-  const int s = blockIdx.x, h = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4;
-  int a, b;
-  packed_range(p.cu, s, p.total, &a, &b);
-  const int slot = packed_slot(p.slots, s, p.n_slots);
-  if (e >= p.sized) return;
-  const int n = max(1, (b - a + seg - 1) / seg), u0 = first_unit(p, seg, s);
-  if (n == 1 || u0 + n > units) return;  // whole sequences read S_in; the second only where cu_seqlens is not what it should be
+__global__ void __launch_bounds__(256) segment_scan_kernel(const PackedPass p, int seg, const Split *splits,
+                                                           const int *count, float *ws) {
+  const int h = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4;
+  if (static_cast<int>(blockIdx.x) >= *count || e >= p.sized) return;
+  const Split sp = splits[blockIdx.x];
+  const int a = sp.a, b = sp.b, slot = sp.row, n = (b - a + seg - 1) / seg, u0 = sp.u;
   const float g = p.g ? __ldg(p.g + h) : 0.f;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (p.S_in && slot >= 0) {
@@ -976,7 +1003,8 @@ int fail(const char *what, cudaError_t e) {
 struct Ready {
   Maps m;
   Segments sg;
-  size_t owners, plan, states;  // bytes of its workspace behind 256 of counters; plan 0: none
+  int most;                     // segments with a state to form
+  size_t owners, plan, lists, states;  // bytes of its workspace behind 256 of counters; plan 0: none
 };
 
 // Maps, split and workspace of a pass, of passes with `share` tokens for each SM
@@ -1013,10 +1041,12 @@ int make_ready(const PackedPass &p, int passes, long long share, Ready *r) {
     return LA_ERR_INVALID_ARG;
   }
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  r->owners = r->plan = r->states = 0;
+  r->most = r->sg.tokens ? p.total / r->sg.tokens : 0;
+  r->owners = r->plan = r->lists = r->states = 0;
   if (items > sms || r->sg.tokens) {
     r->owners = up(p.slots && (p.S_in || p.S_out) ? (size_t)p.n_slots * 4 : 0);
     r->plan = up((size_t)r->sg.units * sizeof(Unit));
+    r->lists = up((size_t)r->most * (sizeof(Unit) + sizeof(Split)));
     r->states = r->sg.tokens ? (size_t)r->sg.units * p.H * p.sized * 4 : 0;
   }
   return LA_OK;
@@ -1041,7 +1071,7 @@ int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream) {
   for (int i = 0; i < passes; ++i) {
     const int rc = make_ready(p[i], passes, share, &r[i]);
     if (rc != LA_OK) return rc;
-    if (r[i].plan) bytes += 256 + r[i].owners + r[i].plan + r[i].states;
+    if (r[i].plan) bytes += 256 + r[i].owners + r[i].plan + r[i].lists + r[i].states;
   }
   uint8_t *ws = nullptr;
   cudaError_t e = cudaSuccess;
@@ -1051,20 +1081,33 @@ int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream) {
     e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes, pool, stream);
     if (e != cudaSuccess) return fail("workspace allocation failed", e);
   }
-  // counters, owners of the state rows, plan, segments' states of each pass
+  // counters, owners of the state rows, plan, lists of split sequences and their segments, states of each pass
   uint8_t *at = ws;
   PlanJobs jobs = {};
+  Segments state[3];
+  const Split *splits[3] = {};
+  const int *split_count[3] = {};
   int planned = 0;
   for (int i = 0; i < passes; ++i) {
     if (!r[i].plan) continue;
     unsigned *head = reinterpret_cast<unsigned *>(at);
-    Unit *plan = reinterpret_cast<Unit *>(at + 256 + r[i].owners);
-    jobs.job[planned++] = {p[i], r[i].sg.tokens, r[i].sg.units, head, reinterpret_cast<int *>(at + 256), plan};
+    uint8_t *behind = at + 256 + r[i].owners;
+    Unit *plan = reinterpret_cast<Unit *>(behind), *segments = reinterpret_cast<Unit *>(behind + r[i].plan);
+    Split *split = reinterpret_cast<Split *>(segments + r[i].most);
+    const int *counts = reinterpret_cast<const int *>(head);
+    jobs.job[planned++] = {p[i], r[i].sg.tokens, r[i].sg.units, r[i].most, head, reinterpret_cast<int *>(at + 256),
+                           plan, segments, split};
+    if (r[i].sg.tokens) {
+      float *states = reinterpret_cast<float *>(behind + r[i].plan + r[i].lists);
+      state[i] = {r[i].sg.tokens, r[i].most, segments, counts + kSegmentCount, head + kStateQueue, nullptr, states};
+      r[i].sg.in = states;
+      splits[i] = split;
+      split_count[i] = counts + kSplitCount;
+    }
     r[i].sg.plan = plan;
-    r[i].sg.count = reinterpret_cast<const int *>(head + 2);
-    r[i].sg.queue = head;
-    if (r[i].sg.tokens) r[i].sg.out = reinterpret_cast<float *>(at + 256 + r[i].owners + r[i].plan);
-    at += 256 + r[i].owners + r[i].plan + r[i].states;
+    r[i].sg.count = counts + kUnitCount;
+    r[i].sg.queue = head + kMainQueue;
+    at += 256 + r[i].owners + r[i].plan + r[i].lists + r[i].states;
   }
   if (planned) {
     plan_kernel<<<planned, kPlanThreads, 0, stream>>>(jobs);
@@ -1073,17 +1116,14 @@ int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream) {
   bool beside = false;
   for (int i = 0; i < passes && e == cudaSuccess; ++i) {
     if (!r[i].sg.tokens) continue;
-    e = launch<true>(p[i], r[i].sg, r[i].m, beside, stream);
+    e = launch<true>(p[i], state[i], r[i].m, beside, stream);
     beside = true;
   }
   for (int i = 0; i < passes && e == cudaSuccess; ++i) {
-    if (r[i].sg.tokens) {
-      segment_scan_kernel<<<dim3(p[i].n_seq, p[i].H, (p[i].sized / 4 + 255) / 256), 256, 0, stream>>>(
-          p[i], r[i].sg.tokens, r[i].sg.units, r[i].sg.out);
-      e = cudaGetLastError();
-      r[i].sg.in = r[i].sg.out;
-    }
-    if (r[i].plan) ++r[i].sg.queue;  // the main kernel's own
+    if (!r[i].sg.tokens) continue;
+    segment_scan_kernel<<<dim3(r[i].most, p[i].H, (p[i].sized / 4 + 255) / 256), 256, 0, stream>>>(
+        p[i], r[i].sg.tokens, splits[i], split_count[i], state[i].out);
+    e = cudaGetLastError();
   }
   for (int i = 0; i < passes && e == cudaSuccess; ++i) e = launch<false>(p[i], r[i].sg, r[i].m, i > 0, stream);
   if (ws) {

@@ -30,6 +30,61 @@ def draw(N, n, H, Hk, dk, dv, dtype, seed):
     return [t.to(dtype) for t in (q, k, v, dO)] + [r(n, H, dk, dv), r(n, H, dk, dv)]
 
 
+def timed(fn):
+    for _ in range(3):
+        fn()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(5):
+        fn()
+    b.record()
+    b.synchronize()
+    return a.elapsed_time(b) / 5
+
+
+def test_unknown_lengths_cost_no_walk_over_all_sequences():
+    # 4096 prompts of 8 tokens on a pool of states: without max_len the call has to allow for long sequences, and
+    # finds none. That is a few launches more, not a second walk over the sequences.
+    n, H, d = 4096, 16, 128
+    q, k, v = (torch.zeros(8 * n, H, d, dtype=BF, device="cuda") for _ in range(3))
+    o = torch.empty_like(v)
+    g = torch.full((H,), -0.01, device="cuda")
+    c = torch.arange(0, 8 * n + 1, 8, dtype=torch.int32, device="cuda")
+    slots = torch.arange(n, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    pool = torch.zeros(n, H, d, d, device="cuda")
+    known, unknown = (timed(lambda m=m: la.packed_fwd(q, k, v, c, "retnet", g=g, S0=pool, S_final=pool, slots=slots,
+                                                      max_len=m, o=o)) for m in (8, 0))
+    done()
+    print(f"known {known:.3f} ms, unknown {unknown:.3f} ms")
+    assert unknown <= 1.1 * known + 0.05, (known, unknown)
+
+
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 1)])
+def test_few_split_sequences_among_many(H, Hk):
+    # split sequences between hundreds of short and empty ones, forward on a pool and backward
+    gen = torch.Generator().manual_seed(40)
+    lens = torch.randint(0, 5, (400,), generator=gen).tolist()
+    lens[3], lens[200], lens[399] = 2700, 5200, 3100
+    N, n, dk, dv = sum(lens), len(lens), 64, 64
+    q, k, v, dO, S0, dS = draw(N, n, H, Hk, dk, dv, BF, 41)
+    slots = torch.randperm(n + 5, generator=gen)[:n].to(torch.int32)
+    pool = torch.full((n + 5, H, dk, dv), 7.0)
+    pool[slots.long()] = S0
+    S, g = pool.cuda(), gammas(H)
+    o, _ = la.packed_fwd(*up(q, k, v), cu(lens), "retnet", g=g.cuda(), S0=S, S_final=S, slots=slots.cuda())
+    got = la.packed_bwd(*up(q, k, v, dO), cu(lens), "retnet", g=g.cuda(), S0=S0.cuda(), dS_final=dS.cuda())
+    done()
+    (want, Sw), (size, Ss) = (retention(q, k, v, g, lens, S0, positive=p) for p in (False, True))
+    hold(o, want, packed_bound(want, size, 5200, BF), "o")
+    hold(S.cpu()[slots.long()], Sw, state_bound(Ss, 5200, BF), "S")
+    free = [r for r in range(n + 5) if r not in slots.tolist()]
+    assert (S.cpu()[free] == 7.0).all()
+    want, size = (retention_bwd(q, k, v, dO, g, lens, S0, dS, positive=p) for p in (False, True))
+    for name, a, b, e in zip(("dq", "dk", "dv"), got, want, size):
+        hold(a, b, packed_bound(b, e, 5200, BF), name)
+    hold(got[3], want[3], state_bound(size[3], 5200, BF), "dS0")
+
+
 def raw_bwd(args, g, c, n, dtype):
     """dq, dk, dv into buffers of fives."""
     q, k, v, dO = args
