@@ -18,9 +18,10 @@
 // the next one's first without draining. Sequences longer than the segment first
 // go through the same kernel with STATE set, which only forms each segment's own
 // contribution to the state (the last one's is not asked for), and a scan over
-// the segments. Unit u of
-// sequence s are the numbers from floor(cu[s]/seg) + s on: enough for its
-// segments, and increasing in s.
+// the segments. Their states lie in a workspace, a row for each segment of a
+// split sequence: a sequence of n > 1 segments is longer than n - 1 of them, so
+// that there are at most total / seg segments but the last ones, and at most
+// twice as many in all, however many sequences the call has.
 //
 // The state stays in registers: every chunk's dS is formed in a TMEM tile of
 // its own and added by float32 FMAs, gamma^n - 1 carrying the decay. Adding in
@@ -81,25 +82,26 @@ constexpr uint32_t kSpin = 1u << 22;     // polls before a wait gives up (tens o
 constexpr int kRegsIssue = 56, kRegsState = 104, kRegsOut = 88, kRegsP = 72, kRegsZ = 56;
 static_assert(kRegsIssue + kRegsState + kRegsOut + 2 * kRegsP + 2 * kRegsZ <= 7 * 72, "register split");
 
-// A unit as the plan writes it: tokens [t0, t1), its number, and 4 * state row + 2 * (it is all of
-// its sequence) + (the state behind it is its sequence's last); state row -1: none.
+// A unit as the plan writes it: tokens [t0, t1), its row of the segments' states (of split
+// sequences only), and 4 * state row + 2 * (it is all of its sequence) + (the state behind it is its
+// sequence's last); state row -1: none.
 struct Unit {
   int t0, t1, u, row;
 };
 
-// A sequence of more than one unit: tokens [a, b), its first unit's number, its state row or -1.
+// A sequence of more than one unit: tokens [a, b), its first row of the segments' states, its state row or -1.
 struct Split {
   int a, b, u, row;
 };
 
 struct Segments {
   int tokens;        // of a segment; 0: every sequence is one unit
-  int units;         // sequences, or the numbers units may have; STATE: the most segments with a state to form
+  int units;         // at most this many; STATE: segments with a state to form
   const Unit *plan;  // units with something to do, the longest first (STATE: those segments, in any order), or null:
                      // unit u is sequence u, one item a CTA
   const int *count;  // how many of them
   unsigned *queue;   // next item for a CTA that is done, from zero
-  const float *in;   // [unit][H][dk][dv] entering states of split sequences; the others': S_in by row
+  const float *in;   // [row][H][dk][dv] entering states of split sequences' segments; the others': S_in by row
   float *out;        // STATE: the segments' own contributions
 };
 
@@ -107,11 +109,6 @@ struct Segments {
 struct Item {
   int t0, t1, chunks, h, v0, u, slot, leaves, whole;
 };
-
-// First unit number of sequence s.
-__device__ __forceinline__ int first_unit(const PackedPass &p, int seg, int s) {
-  return seg ? min(max(__ldg(p.cu + s), 0), p.total) / seg + s : s;
-}
 
 __device__ __forceinline__ int chunks_of(int tokens) { return (tokens + kN - 1) / kN; }
 
@@ -146,10 +143,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs)
   __shared__ int first[kBuckets];
   __shared__ int warp_sum[32];
   __shared__ unsigned long long taken;  // segments given out
-  __shared__ int split, end;            // split sequences; where there was no more room for their segments
+  __shared__ int split, given, end;     // split sequences, rows of theirs; where there was no more room
   const int tid = threadIdx.x;
   if (tid < 2) head[tid] = 0;
-  if (tid == 0) taken = split = 0, end = most;
+  if (tid == 0) taken = split = given = 0, end = most;
   first[tid] = 0;
   const bool rows = p.S_in || p.S_out;
   if (rows && p.slots) {  // of sequences that name the same row the first one has it
@@ -168,22 +165,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJobs jobs)
     for (int i = tid; i < p.n_seq; i += kPlanThreads) {
       int a, b;
       packed_range(p.cu, i, p.total, &a, &b);
-      const int n = seg ? max(1, (b - a + seg - 1) / seg) : 1, u0 = first_unit(p, seg, i);
+      const int n = seg ? max(1, (b - a + seg - 1) / seg) : 1;
       int row = -1;
       if (rows) {
         row = p.slots ? __ldg(p.slots + i) : i;
         if (row < 0 || row >= p.n_slots || (p.slots && *const_cast<volatile int *>(owner + row) != i)) row = -1;
       }
       if (b == a && !(p.S_out && row >= 0)) continue;  // nothing to do
-      if (u0 + n > units) continue;                    // only where cu_seqlens is not what it should be
       bool room = true;                                // (none only where sequences overlap, as they should not)
-      int formed = 0;                                  // first of its segments whose state the others start from
+      int formed = 0, u0 = 0;                          // first of its segments with a state to form, first row of all
       if (pass && n > 1) {
         const unsigned long long at = atomicAdd(&taken, n - 1ull);
         room = at + (n - 1) <= most;
         formed = static_cast<int>(min(at, static_cast<unsigned long long>(most)));
-        if (room) splits[atomicAdd(&split, 1)] = {a, b, u0, row};
-        else atomicMin(&end, formed);
+        if (room) {
+          u0 = atomicAdd(&given, n);
+          splits[atomicAdd(&split, 1)] = {a, b, u0, row};
+        } else {
+          atomicMin(&end, formed);
+        }
       }
       for (int k = 0; k < n; ++k) {
         const int t0 = a + k * seg, t1 = seg ? min(b, t0 + seg) : b;
@@ -1047,7 +1047,7 @@ int make_ready(const PackedPass &p, int passes, long long share, Ready *r) {
     r->owners = up(p.slots && (p.S_in || p.S_out) ? (size_t)p.n_slots * 4 : 0);
     r->plan = up((size_t)r->sg.units * sizeof(Unit));
     r->lists = up((size_t)r->most * (sizeof(Unit) + sizeof(Split)));
-    r->states = r->sg.tokens ? (size_t)r->sg.units * p.H * p.sized * 4 : 0;
+    r->states = (size_t)2 * r->most * p.H * p.sized * 4;
   }
   return LA_OK;
 }

@@ -62,8 +62,10 @@ extern "C" {
  *
  * bfloat16 runs chunkwise on the tensor cores, float32 token by token on the
  * CUDA cores. Workspace from the library's pool where the heads and sequences
- * are more than the SMs or a sequence is long: 16 bytes a sequence or segment,
- * 4*n_slots with slots, and for split sequences 4*H*dk*dv a segment.
+ * are more than the SMs or a sequence may be long (max_len unknown: as long as
+ * total): 16 bytes a sequence, 4*n_slots with slots, and for the segments of
+ * split sequences, however many sequences there are, up to 512*SMs*dk bytes
+ * (dv if that is more; about 10 MB).
  *
  * Inputs are finite: a NaN or infinity at a token may reach every token of the
  * same sequence; never another sequence, whatever the neighbours hold.

@@ -1,5 +1,9 @@
 """Packed retention on the GPU where a call's bounds are unusual: batches of many short
 sequences, padded and decreasing cu_seqlens, values at the end of the range."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -9,6 +13,7 @@ from layerlib import gammas, hold, packed_bound, retention, retention_bwd, start
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def cu(lens):
@@ -28,6 +33,47 @@ def draw(N, n, H, Hk, dk, dv, dtype, seed):
     r = lambda *s: torch.randn(*s, generator=gen) * dk ** -0.5  # noqa: E731
     q, k, v, dO = r(N, Hk, dk), r(N, Hk, dk), r(N, H, dv), r(N, H, dv)
     return [t.to(dtype) for t in (q, k, v, dO)] + [r(n, H, dk, dv), r(n, H, dk, dv)]
+
+
+# A process of its own: the library's pool keeps what earlier calls took.
+MEMORY = """
+import torch
+import gated_delta_rule_linear_gb300 as la
+
+def used(lens, max_len, backward, H=16, d=128):
+    N = sum(lens)
+    q, k, v, o = (torch.zeros(N, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    g = torch.full((H,), -0.01, device="cuda")
+    c = torch.tensor([0] + lens, dtype=torch.int64).cumsum(0).to(torch.int32).cuda()
+    spare = [torch.empty_like(q) for _ in range(3)]  # room for the results, kept by torch
+    del spare
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    if backward:
+        la.packed_bwd(q, k, v, o, c, "retnet", g=g, with_dS0=False, max_len=max_len)
+    else:
+        la.packed_fwd(q, k, v, c, "retnet", g=g, with_state=False, max_len=max_len, o=o)
+    torch.cuda.synchronize()
+    assert la.la_stream_status(torch.cuda.current_stream().cuda_stream) == 0
+    return before - torch.cuda.mem_get_info()[0]
+
+used([300], 0, False)
+used([300], 0, True)
+print(used(LENS, MAX_LEN, BACKWARD))
+"""
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("lens,max_len", [("[16] * 4096", 0), ("[60000] + [1] * 4095", 60000)])
+def test_many_sequences_take_little_workspace(lens, max_len, backward):
+    # No more states than the segments that a sequence was split into, however many sequences there are. 16 heads
+    # of 128 x 128: a state of all heads is 1 MiB. Split sequences hold at most two segments for each of total / seg,
+    # and seg is an SM's share of total * H * dv / 64 or more: 2 * 152 / 32 = 9.5 states a pass, three passes; plans
+    # and allocation granularity (32 MiB a pool block) on top.
+    code = MEMORY.replace("LENS", lens).replace("MAX_LEN", str(max_len)).replace("BACKWARD", str(backward))
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert int(r.stdout) <= 128 << 20, r.stdout
 
 
 def timed(fn):
