@@ -362,7 +362,8 @@ template <typename T> __device__ __forceinline__ void put_pair(uint4 &u, int j, 
 // (twice: for the sums, for the gradients): with the row's values in registers
 // as float32 the next row's loads did not fit beside them, and without those in
 // flight the kernel waited for memory (0.46 ms against 0.31 on 32768 x 2048).
-// GATE: 0 none, 1 silu, 2 sigmoid; NEXT: with the next norm's gradient; -1: as the arguments say.
+// GATE: 0 none, 1 silu, 2 sigmoid; NEXT: with the next norm's gradient; -1 (more than one load a thread): as the
+// arguments say.
 template <typename T, int V, int NV, int GATE, int NEXT>
 __global__ void __launch_bounds__(512, 1) epilogue_bwd_kernel(const EpilogueParams p, const XRows xr, int tpr,
                                                               float *part) {
@@ -624,11 +625,16 @@ cudaError_t launch(const EpilogueParams &p, const Shape &s, float *part, cudaStr
 #undef LA_BWD
       return cudaGetLastError();
     }
+  if constexpr (!BWD)
+    if (s.wide && s.nv == 1) {
+      LA_GO(V, 1);
+      return cudaGetLastError();
+    }
+  // up to 16384 channels: no bfloat16 row takes eight 16-byte loads a thread
   if (s.wide) {
-    if (!BWD && s.nv == 1) LA_GO(V, 1);
-    else if (s.nv == 2) LA_GO(V, 2);
-    else if (s.nv == 4) LA_GO(V, 4);
-    else LA_GO(V, 8);
+    if (s.nv == 2) LA_GO(V, 2);
+    else if (sizeof(T) == 2 || s.nv == 4) LA_GO(V, 4);
+    else if constexpr (sizeof(T) == 4) LA_GO(V, 8);
   } else {
     if (s.nv == 1) LA_GO(1, 1);
     else if (s.nv <= 8) LA_GO(1, 8);

@@ -52,7 +52,7 @@ struct PackedPass {
   const float *g;
   int reverse;
   int f32;                       // x, y, z are float32, else bfloat16
-  int out_f32;                   // out is float32
+  int out_f32;                   // out is float32 (always with f32)
   unsigned *status;
   int max_len;
 };
@@ -95,6 +95,7 @@ struct Decay {
   __device__ __forceinline__ float operator()(float S) const { return fmaf(S, m, near ? S : 0.f); }
 };
 
+// float32 passes, or passes without a token
 int launch_packed_walk(const PackedPass &p, cudaStream_t stream);
 // Up to three passes that do not depend on each other.
 int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream);

@@ -1,5 +1,6 @@
 // Packed retention, token by token on the CUDA cores in float32: the float32
-// path of la_packed_fwd and la_packed_bwd.
+// path of la_packed_fwd and la_packed_bwd, and either type's calls without a
+// token, which take states over and read nothing else.
 //
 // One CTA of 128 threads owns 32 value columns of one (sequence, head) and
 // walks its tokens, the state slice da x 32 in registers: thread (w, l) holds
@@ -17,11 +18,7 @@ namespace {
 
 constexpr int kTok = 16, kCols = 32;
 
-template <typename T> __device__ __forceinline__ float rd(const void *p, size_t i) {
-  return static_cast<float>(static_cast<const T *>(p)[i]);
-}
-
-template <typename T, int DA>
+template <int DA>
 __global__ void __launch_bounds__(128) packed_walk_kernel(const PackedPass p) {
   __shared__ __align__(16) float sx[kTok][DA], sy[kTok][DA];
   __shared__ float sz[kTok][kCols], part[kTok][4][kCols];
@@ -38,6 +35,8 @@ __global__ void __launch_bounds__(128) packed_walk_kernel(const PackedPass p) {
     const size_t at = p.in_t ? (size_t)col * DA + c0 + c : (size_t)(c0 + c) * p.db + col;
     S[c] = (p.S_in && slot >= 0) ? p.S_in[sbase + at] : 0.f;
   }
+  const float *px = static_cast<const float *>(p.x), *py = static_cast<const float *>(p.y),
+              *pz = static_cast<const float *>(p.z);
   const Decay decay(p.g ? __ldg(p.g + h) : 0.f, 1);
   const size_t xh = (size_t)(h / p.rx) * DA, yh = (size_t)(h / p.ry) * DA, zh = (size_t)(h / p.rz) * p.db;
 
@@ -47,11 +46,11 @@ __global__ void __launch_bounds__(128) packed_walk_kernel(const PackedPass p) {
     __syncthreads();
     for (int i = threadIdx.x; i < m * DA; i += 128) {
       const size_t t = token(i / DA);
-      sx[i / DA][i % DA] = rd<T>(p.x, t * p.ldx + xh + i % DA);
-      sy[i / DA][i % DA] = rd<T>(p.y, t * p.ldy + yh + i % DA);
+      sx[i / DA][i % DA] = px[t * p.ldx + xh + i % DA];
+      sy[i / DA][i % DA] = py[t * p.ldy + yh + i % DA];
     }
     for (int i = threadIdx.x; i < m * kCols; i += 128)
-      sz[i / kCols][i % kCols] = rd<T>(p.z, token(i / kCols) * p.ldz + zh + v0 + i % kCols);
+      sz[i / kCols][i % kCols] = pz[token(i / kCols) * p.ldz + zh + v0 + i % kCols];
     __syncthreads();
     for (int i = 0; i < m; ++i) {
       const float z = sz[i][l];
@@ -69,11 +68,7 @@ __global__ void __launch_bounds__(128) packed_walk_kernel(const PackedPass p) {
     for (int i = threadIdx.x; i < m * kCols; i += 128) {
       const int t = i / kCols, c = i % kCols;
       const float o = (part[t][0][c] + part[t][1][c]) + (part[t][2][c] + part[t][3][c]);
-      const size_t at = token(t) * p.ldo + (size_t)h * p.db + v0 + c;
-      if (p.out_f32)
-        static_cast<float *>(p.out)[at] = o;
-      else
-        static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(o);
+      static_cast<float *>(p.out)[token(t) * p.ldo + (size_t)h * p.db + v0 + c] = o;
     }
   }
   if (p.S_out && slot >= 0)
@@ -133,13 +128,8 @@ __global__ void __launch_bounds__(256) head_sum_kernel(const float *__restrict__
 
 int launch_packed_walk(const PackedPass &p, cudaStream_t stream) {
   const dim3 grid(p.n_seq, p.H, p.db / kCols);
-  if (p.f32) {
-    if (p.da == 64) packed_walk_kernel<float, 64><<<grid, 128, 0, stream>>>(p);
-    else packed_walk_kernel<float, 128><<<grid, 128, 0, stream>>>(p);
-  } else {
-    if (p.da == 64) packed_walk_kernel<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(p);
-    else packed_walk_kernel<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(p);
-  }
+  if (p.da == 64) packed_walk_kernel<64><<<grid, 128, 0, stream>>>(p);
+  else packed_walk_kernel<128><<<grid, 128, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("packed retention: launch failed: %s", cudaGetErrorString(e));
@@ -152,8 +142,8 @@ int launch_head_sums(const float *const src[2], void *const dst[2], int f32, con
                      int Hk, int share, int d, cudaStream_t stream) {
   const long long quads = (long long)total * Hk * (d / 4);
   if (quads == 0) return LA_OK;
-  // as many CTAs as are resident: each looks through the bounds once
-  const long long want = (quads + 255) / 256, most = 5LL * (sm_count() > 0 ? sm_count() : 1);
+  // as many CTAs as are resident, eight a SM: each looks through the bounds once
+  const long long want = (quads + 255) / 256, most = 4LL * (sm_count() > 0 ? sm_count() : 1);
   const dim3 grid(static_cast<unsigned>(want < most ? want : most), 2);
   if (f32)
     head_sum_kernel<<<grid, 256, 0, stream>>>(src[0], static_cast<float *>(dst[0]), src[1], static_cast<float *>(dst[1]),
