@@ -897,9 +897,10 @@ packed_tc_kernel(const PackedPass p, const Segments sg, const __grid_constant__ 
 // place: a running sum per element, the loads of a few segments ahead in flight.
 __global__ void __launch_bounds__(256) segment_scan_kernel(const PackedPass p, int seg, const Split *splits,
                                                            const int *count, float *ws) {
-  const int h = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4;
-  if (static_cast<int>(blockIdx.x) >= *count || e >= p.sized) return;
-  const Split sp = splits[blockIdx.x];
+  const int h = blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int split = *count;
+  const Split sp = splits[blockIdx.z];  // (the grid is within the list's room)
+  if (static_cast<int>(blockIdx.z) >= split || e >= p.sized) return;
   const int a = sp.a, b = sp.b, slot = sp.row, n = (b - a + seg - 1) / seg, u0 = sp.u;
   const float g = p.g ? __ldg(p.g + h) : 0.f;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1121,7 +1122,8 @@ int launch_packed_tc(const PackedPass *p, int passes, cudaStream_t stream) {
   }
   for (int i = 0; i < passes && e == cudaSuccess; ++i) {
     if (!r[i].sg.tokens) continue;
-    segment_scan_kernel<<<dim3(r[i].most, p[i].H, (p[i].sized / 4 + 255) / 256), 256, 0, stream>>>(
+    // (most is below 64 SMs / (H db): a segment is at least a SM's share of all items)
+    segment_scan_kernel<<<dim3((p[i].sized / 4 + 255) / 256, p[i].H, std::min(r[i].most, p[i].n_seq)), 256, 0, stream>>>(
         p[i], r[i].sg.tokens, splits[i], split_count[i], state[i].out);
     e = cudaGetLastError();
   }
