@@ -26,11 +26,22 @@ constexpr int kMaxDevices = 64;
 cudaMemPool_t g_pool[kMaxDevices] = {};
 std::mutex g_pool_mu;
 
+// What a first call sets up for good (the pool, a module's load) is no part of
+// the work that a capturing stream records: allowed under any capture mode.
+struct OutsideCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  OutsideCapture(const OutsideCapture &) = delete;
+  OutsideCapture &operator=(const OutsideCapture &) = delete;
+};
+
 cudaMemPool_t workspace_pool() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lock(g_pool_mu);
   if (!g_pool[dev]) {
+    OutsideCapture outside;
     cudaMemPoolProps props = {};
     props.allocType = cudaMemAllocationTypePinned;
     props.handleTypes = cudaMemHandleTypeNone;
@@ -65,6 +76,7 @@ void set_error(const char *fmt, ...) {
 // destroyed and created again.
 unsigned *status_word() {
   void *ptr = nullptr;
+  OutsideCapture outside;
   if (cudaGetSymbolAddress(&ptr, g_status_word) != cudaSuccess) return nullptr;
   return static_cast<unsigned *>(ptr);
 }
