@@ -7,7 +7,8 @@
 
 namespace la {
 
-// n / d and n % d of 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and
+// n / d and n % d of 0 <= n < 2^31 by a multiplication, the division by an invariant
+// of Granlund and Montgomery (1994): with s = ceil(log2 d) and
 // m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(m, n) + n) >> s (the sum
 // stays below 2^32 for n below 2^31).
 struct FastDiv {

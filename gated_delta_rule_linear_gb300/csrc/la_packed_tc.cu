@@ -47,12 +47,12 @@
 //   warps 8-11    output: gamma^(i+1) X S + P Z, to memory by TMA
 //   warps 12-19   Z' high and low
 //   warps 20-27   P, in TMEM over its scores
-// Measured on GB300, 16 heads of 128, bf16: forward of 4 x 16384 tokens 0.240 ms
-// (1.08 GB, 4.5 TB/s), one CTA for each of 128 heads and value tiles at about
-// 3350 cycles a chunk. What sets that period (clock64 traces, ncu): the way of a
-// chunk through the roles, about 6700 cycles with two chunks in flight (shared
+// Measured on GB300, 16 heads of 128, bf16: forward of 4 x 16384 tokens 0.247 ms
+// (1.08 GB, 4.4 TB/s), one CTA for each of 128 heads and value tiles at about
+// 3450 cycles a chunk. What sets that period (clock64 traces, ncu): the way of a
+// chunk through the roles, about 6900 cycles with two chunks in flight (shared
 // memory and TMEM hold no third): 8 tensor instructions of a product take 700 to
-// 1100 cycles to issue (the pipe itself is busy 1500 of 3350), P 1000, the output
+// 1100 cycles to issue (the pipe itself is busy 1500 of 3450), P 1100, the output
 // 600, loads 1400. A change of item costs about 2 periods more, most of it cold
 // code: the steady state already fills the instruction cache.
 // Every wait is bounded; on expiry the CTA raises the status word, all roles

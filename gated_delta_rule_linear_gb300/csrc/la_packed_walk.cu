@@ -8,7 +8,8 @@
 // memory; every warp's partial of out_t over its rows goes to shared memory and
 // is added up once per block of tokens. The walk is bound by its own serial
 // chain, about da/2 FMAs a token and warp, not by memory (4 x 16384 tokens of 16
-// heads of 128: 7.9 ms, 0.48 us a token).
+// heads of 128: 6.9 ms, 0.42 us a token; the backward's three walks over 8 x 4096
+// tokens: 6.9 ms).
 #include <cuda_bf16.h>
 
 #include "la_layer_internal.h"
