@@ -2,32 +2,13 @@
 // the workspaces of the layer operators.
 #include <climits>
 #include <cmath>
-#include <initializer_list>
 
+#include "la_check.h"
 #include "la_layer_internal.h"
 
 using namespace la;
 
 namespace {
-
-bool at(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// An output that is one of the inputs, or another output. (Tensors that overlap in part are not looked for.)
-bool same(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
-  for (auto o = outs.begin(); o != outs.end(); ++o) {
-    if (!*o) continue;
-    for (const void *i : ins)
-      if (*o == i) return true;
-    for (auto u = outs.begin(); u != o; ++u)
-      if (*o == *u) return true;
-  }
-  return false;
-}
-
-int bad(const char *fn, const char *what) {
-  set_error("%s: %s", fn, what);
-  return LA_ERR_INVALID_ARG;
-}
 
 // LA_LINEAR or LA_RETNET, with or without LA_F32; heads and widths.
 int check_packed(const char *fn, int mode, const float *g, int H, int Hk, int dk, int dv, long long ldq,

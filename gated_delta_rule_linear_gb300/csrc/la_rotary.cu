@@ -6,16 +6,9 @@
 // their way from HBM passes under the sines (0.219 -> 0.189 ms, 5.7 TB/s, on
 // 65536 tokens of 16 + 16 heads of 128, bf16).
 //
-// Angles. pos * freq reaches millions of radians, where a float32 product has
-// lost the angle and a float64 one is slow here. A frequency is held instead as
-// its turns per position modulo one in 64-bit fixed point, F = frac(freq / 2 pi)
-// 2^64; the integer product pos * F wraps at whole turns by itself, and its top
-// 32 bits, signed, are the angle in [-1/2, 1/2) turns to 2^-32. freq / 2 pi is
-// one float64 product: off by 2^-53 of itself, 2^-22 turns at a position of
-// 2^31 and a frequency of one radian, far less at any real position.
-#include <cuda_bf16.h>
-
+// Angles: see rotary_turn.
 #include "la_layer_internal.h"
+#include "la_rotary.cuh"
 #include "la_sm100.cuh"
 
 namespace la {
@@ -33,39 +26,6 @@ __device__ __forceinline__ size_t row_at(int n, int h, int heads, int d, int T, 
 
 struct RotaryDiv {
   FastDiv items, heads, T_in, T_out, P;
-};
-
-template <typename T, int V> struct Vec {
-  static __device__ __forceinline__ void load(const T *p, float *f) {
-    if constexpr (V == 1) {
-      f[0] = static_cast<float>(*p);
-    } else {
-      const uint4 u = *reinterpret_cast<const uint4 *>(p);
-      if constexpr (sizeof(T) == 4) {
-        f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-        f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-      } else {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[2 * i] = __uint_as_float(w[i] << 16);
-          f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-      }
-    }
-  }
-  static __device__ __forceinline__ void store(T *p, const float *f) {
-    if constexpr (V == 1) {
-      *p = T(f[0]);
-    } else if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    } else {
-      __nv_bfloat162 h[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(h);
-    }
-  }
 };
 
 // V channels at a time (16 bytes), or 1 where sizes or addresses do not allow it.
@@ -88,13 +48,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p, 
     uint32_t n, c;
     by.P.split(i, n, c);
     const int axis = (int)c < p.s0 ? 0 : (int)c < p.s0 + p.s1 ? 1 : 2;
-    const double f = __ldg(p.freq + c) * 0.15915494309189535;  // 1 / (2 pi)
-    const unsigned long long F = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0);
-    const long long pos = __ldg(p.pos + (size_t)(n0 + n) * p.n_axes + axis);
-    const int t = static_cast<int>((static_cast<unsigned long long>(pos) * F) >> 32);
-    float s, co;
-    sincospif(static_cast<float>(t) * 4.656612873077393e-10f, &s, &co);  // 2^-31: half turns
-    turn[i] = make_float2(co, p.inverse ? -s : s);
+    turn[i] = rotary_turn(__ldg(p.freq + c), __ldg(p.pos + (size_t)(n0 + n) * p.n_axes + axis), p.inverse);
   }
   __syncthreads();
   constexpr int W = V == 1 && IL ? 2 : V;             // channels of one load
