@@ -1,82 +1,702 @@
 // Attention of one new token of each sequence over a paged cache:
-// o_h = sum_p softmax_p(scale q_h . k_p) v_p.
+// o_h = sum_p softmax_p(scale q_h . k_p) v_p, in one pass over the places with a
+// running maximum and sum (Milakov and Gimelshein, 2018).
 //
-// One CTA takes a (sequence, query head); each warp walks every fourth place
-// with a running maximum and sum, a lane holding d / 32 channels.
+// Bound by reading keys and values once. The heads that share a key/value head
+// are the rows of one block of 8 or 16 (a `part`, of a sequence), so that a place
+// is read once for all of them.
+//
+// Work. The places of a part are cut into units of four warps' blocks; the units
+// of all parts, one after the other, are dealt to the CTAs in equal runs, however
+// long the sequences are (each CTA adds up the lengths for itself: nothing is
+// known on the host). A CTA's run begins and ends inside a part: what it has of
+// that goes to a workspace, and join_kernel adds the pieces up. Every other part
+// is finished where it was begun.
+//
+// A warp streams its blocks through a ring of stages in shared memory by 16-byte
+// asynchronous copies, across the ends of parts, with no barrier but its own; the
+// CTA's warps meet at the end of a part only.
+//
+// bfloat16: S = Q K^T and O = P V by 16 x 8 x 16 matrix instructions of a warp.
+// With 8 or 16 rows the tensor cores have an eighth of a tile's work, and the
+// operands come straight from the 16-byte rows as they are stored: channels are
+// taken in the order in which a thread holds them, for keys and queries alike. P
+// keeps 16 bits as a high and a low bfloat16 part; with up to 8 heads the low part
+// is in the tile's other 8 rows and costs nothing.
+//
+// float32: CUDA cores, a lane a key for S and a lane four channels for O.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+#include <atomic>
+
+#include "la_f32x2.cuh"
 #include "la_serve_internal.h"
+#include "la_sm100.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kJoinThreads = 512;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const FastDiv by_page) {
-  constexpr int C = D / 32;
-  __shared__ float so[kWarps][D], sm[kWarps], sl[kWarps];
-  const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int len = min((long long)max(__ldg(p.at.lens + s), 0), (long long)p.at.max_pages * p.at.page_size);
-  const int first = p.window > 0 ? max(len - p.window, 0) : 0;
-  const T *q = static_cast<const T *>(p.q) + s * p.ldq + h * D;
-  float qf[C], o[C], m = -INFINITY, l = 0.f;
-  for (int c = 0; c < C; ++c) {
-    qf[c] = static_cast<float>(q[lane + 32 * c]);
-    o[c] = 0.f;
-  }
-  for (int i = first + warp; i < len; i += kWarps) {
-    uint32_t pg, r;
-    by_page.split(i, pg, r);
-    const int g = __ldg(p.at.table + s * p.at.ld_table + pg);
-    if (g < 0 || g >= p.at.n_pages) continue;
-    const long long at = g * p.at.ld_page + ((long long)r * p.Hk + hk) * D + lane;
-    const T *k = static_cast<const T *>(p.k_cache) + at, *v = static_cast<const T *>(p.v_cache) + at;
-    float x = 0.f;
-    for (int c = 0; c < C; ++c) x = fmaf(qf[c], static_cast<float>(k[32 * c]), x);
-    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(~0u, x, d);
-    x *= p.scale;
-    const float next = fmaxf(m, x), keep = expf(m - next), e = expf(x - next);
-    l = l * keep + e;
-    for (int c = 0; c < C; ++c) o[c] = o[c] * keep + e * static_cast<float>(v[32 * c]);
-    m = next;
-  }
-  for (int c = 0; c < C; ++c) so[warp][lane + 32 * c] = o[c];
-  if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  if (top == -INFINITY) top = 0.f;
-  for (int w = 0; w < kWarps; ++w) sum += sl[w] * expf(sm[w] - top);
-  for (int c = threadIdx.x; c < D; c += kThreads) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += so[w][c] * expf(sm[w] - top);
-    static_cast<T *>(p.o)[((size_t)s * p.H + h) * D + c] = T(sum > 0.f ? x / sum : 0.f);
-  }
-  if (p.lse && threadIdx.x == 0) p.lse[(size_t)s * p.H + h] = sum > 0.f ? top + logf(sum) : -INFINITY;
+// Sizes of a kernel with d = D and HB rows.
+template <typename T, int D, int HB> struct Shape {
+  static constexpr bool kF32 = sizeof(T) == 4;
+  static constexpr int kKeys = kF32 && D == 256 ? 8 : 16;       // places of a warp's block
+  static constexpr int kUnit = kKeys * kWarps;
+  static constexpr int kChunks = D * static_cast<int>(sizeof(T)) / 16;  // 16-byte chunks of a row
+  static constexpr int kTile = kKeys * kChunks * 16;            // bytes of a block's keys
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kJoin = kWarps * HB * D * 4;             // the warps' sums, where they meet
+  // two CTAs on a SM where three stages allow it, else one with what fits
+  static constexpr bool kTwo = 3 * kStage * kWarps + kJoin <= 112 * 1024;
+  static constexpr int kStages = std::min(((kTwo ? 112 : 224) * 1024 - kJoin) / (kStage * kWarps), 6);
+  static constexpr int kBytes = kStages * kStage * kWarps + kJoin;
+};
+
+// What the CTAs of a call share: rows of a part, pieces of parts in the workspace.
+struct Split {
+  int blocks;      // blocks of HB heads of a key/value head
+  int parts;       // parts of a sequence: Hk * blocks
+  int whole;       // a CTA takes one whole part: no pieces, no workspace
+  int least;       // least units of a run
+  float *sums;     // [2 * CTAs][HB][D]
+  float2 *ml;      // [2 * CTAs][HB]: maximum (of log2) and sum
+  int4 *joins;     // [CTAs]: sequence, part, last CTA with a piece of it; sequence -1: none
+};
+
+constexpr int kMostPlaces = 0x7fff0000;  // a unit behind the last place is still an int
+
+struct Range {
+  int first, len;  // places of a sequence: first .. len - 1
+};
+__device__ __forceinline__ Range places_of(const PagedAttn &p, int s) {
+  const long long most = min((long long)p.at.max_pages * p.at.page_size, (long long)kMostPlaces);
+  const int len = static_cast<int>(min((long long)max(__ldg(p.at.lens + s), 0), most));
+  return {p.window > 0 ? max(len - p.window, 0) : 0, len};
 }
 
+// A place in a CTA's run of units.
+template <int UNIT> struct Cursor {
+  int s, part, unit, units, first, len;
+  long long left;  // units of the run from here on
+
+  __device__ __forceinline__ void enter(const PagedAttn &p) {  // the next sequence with a place
+    for (; s < p.n; ++s) {
+      const Range r = places_of(p, s);
+      first = r.first;
+      len = r.len;
+      units = (len - first + UNIT - 1) / UNIT;
+      if (units > 0) return;
+    }
+  }
+  __device__ __forceinline__ void next(const PagedAttn &p, int parts) {
+    --left;
+    if (++unit < units) return;
+    unit = 0;
+    if (++part < parts) return;
+    part = 0;
+    ++s;
+    if (left > 0) enter(p);
+  }
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void wait_all_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The 16-byte chunk that chunk c of row r is stored at, so that the reads below hit all banks.
+template <bool F32, bool VALUES> __device__ __forceinline__ int stored(int r, int c) {
+  if (F32) return c ^ (r & 7);
+  return VALUES ? c ^ ((r >> 1 & 3) << 1) : c ^ ((r & 1) << 2);
+}
+
+// A warp's part of the softmax of up to HB heads, bfloat16. Thread (g, t) = (lane / 4, lane % 4) holds rows g and
+// g + 8. Channels: the k-th pair of matrix instructions of S takes chunk 4 k + t of every row, thread t's 8 channels of
+// it two instructions' fragments; O's tile 8 b + j has channel 64 b + 8 g + j in column g.
+template <int D, int HB> struct Bf16Warp {
+  static constexpr int R = HB / 8;  // rows of a thread
+  uint32_t q[R][D / 32][4];
+  float o[D / 8][4], m[R], l[R];
+  float scale;
+
+  __device__ __forceinline__ void begin(const PagedAttn &p, int s, int h0, int heads, int lane, float *) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const __nv_bfloat16 *row = static_cast<const __nv_bfloat16 *>(p.q) + s * p.ldq + (long long)(h0 + g + 8 * r) * D;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (g + 8 * r < heads) u = __ldg(reinterpret_cast<const uint4 *>(row) + 4 * k + t);
+        q[r][k][0] = u.x; q[r][k][1] = u.y; q[r][k][2] = u.z; q[r][k][3] = u.w;
+      }
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    scale = p.scale * 1.44269504f;  // exponents of two
+  }
+
+  __device__ __forceinline__ void block(uint32_t keys, uint32_t values, uint32_t there, int lane, float *) {
+    constexpr int kRow = D * 2;
+    const int g = lane >> 2, t = lane & 3;
+    float x[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float c[2][4] = {};  // the k steps alternate between two accumulators
+      const int row = 8 * i + g;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const uint4 u = lds(keys + row * kRow + stored<false, false>(row, 4 * k + t) * 16);
+        mma(c[0], q[0][k][0], q[R - 1][k][0], q[0][k][1], q[R - 1][k][1], u.x, u.y);
+        mma(c[1], q[0][k][2], q[R - 1][k][2], q[0][k][3], q[R - 1][k][3], u.z, u.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[i][j] = there >> (8 * i + 2 * t + (j & 1)) & 1 ? (c[0][j] + c[1][j]) * scale : -INFINITY;
+    }
+    uint32_t hi[R][2], lo[R][2];
+    float keep[R];
+    bool moved = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float top = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      const float now = fmaxf(m[r], top), base = now == -INFINITY ? 0.f : now;
+      keep[r] = sm100::ex2(m[r] - base);
+      moved |= now > m[r];
+      m[r] = now;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = sm100::ex2(x[i][2 * r] - base), b = sm100::ex2(x[i][2 * r + 1] - base);
+        l[r] = i == 0 ? fmaf(l[r], keep[r], a + b) : l[r] + (a + b);
+        hi[r][i] = pack(a, b);
+        lo[r][i] = pack(a - __uint_as_float(hi[r][i] << 16), b - __uint_as_float(hi[r][i] & 0xffff0000u));
+      }
+    }
+    if (__any_sync(~0u, moved)) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= keep[0]; o[i][1] *= keep[0];
+        o[i][2] *= keep[R - 1]; o[i][3] *= keep[R - 1];
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+      uint4 u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+        u[i] = lds(values + row * kRow + stored<false, true>(row, 8 * b + g) * 16);
+      }
+      const uint32_t v[4][4] = {{u[0].x, u[0].y, u[0].z, u[0].w}, {u[1].x, u[1].y, u[1].z, u[1].w},
+                                {u[2].x, u[2].y, u[2].z, u[2].w}, {u[3].x, u[3].y, u[3].z, u[3].w}};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b0 = __byte_perm(v[0][j / 2], v[1][j / 2], j & 1 ? 0x7632 : 0x5410);
+        const uint32_t b1 = __byte_perm(v[2][j / 2], v[3][j / 2], j & 1 ? 0x7632 : 0x5410);
+        float(&c)[4] = o[8 * b + j];
+        if constexpr (R == 1) {
+          mma(c, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+        } else {
+          mma(c, hi[0][0], hi[1][0], hi[0][1], hi[1][1], b0, b1);
+          mma(c, lo[0][0], lo[1][0], lo[0][1], lo[1][1], b0, b1);
+        }
+      }
+    }
+  }
+
+  // The warp's sums into [HB][D] and [HB] of shared memory.
+  __device__ __forceinline__ void end(float *sums, float2 *ml, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      if (t == 0) ml[g + 8 * r] = make_float2(m[r], l[r]);
+      float4 *row = reinterpret_cast<float4 *>(sums + (g + 8 * r) * D);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // 16 channels from 64 b + 16 t on: column 2t's 8, then 2t + 1's
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float(&a)[4] = o[8 * b + 4 * (c & 1) + e];
+            f[e] = R == 1 ? a[c >> 1] + a[2 + (c >> 1)] : a[2 * r + (c >> 1)];
+          }
+          row[16 * b + ((4 * t + c) ^ g)] = make_float4(f[0], f[1], f[2], f[3]);
+        }
+    }
+  }
+  // Where quad c of row g is in there.
+  static __device__ __forceinline__ int quad(int g, int c) { return (c & ~15) + ((c & 15) ^ (g & 7)); }
+};
+
+// The same in float32: lane (key, part of the channels) for S, lane (four channels, part of the keys) for O.
+template <int D, int HB> struct F32Warp {
+  static constexpr int kKeys = Shape<float, D, HB>::kKeys, kLanes = 32 / kKeys;  // lanes of a key
+  static constexpr int kQuads = D / 4, kPer = kQuads >= 32 ? kQuads / 32 : 1, kSplit = kQuads >= 32 ? 1 : 32 / kQuads;
+  static_assert(HB == 8, "");
+  float o[HB][kPer][4], m[HB], l[HB];
+  float scale;
+  const float *q;  // [HB][D] in shared memory
+
+  __device__ __forceinline__ void begin(const PagedAttn &p, int s, int h0, int heads, int lane, float *sq) {
+    const int tid = threadIdx.x;
+    const float *src = static_cast<const float *>(p.q) + s * p.ldq + (long long)h0 * D;
+    for (int i = tid; i < HB * D; i += kThreads) sq[i] = i < heads * D ? __ldg(src + i) : 0.f;
+    __syncthreads();
+    q = sq;
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[h][i][0] = o[h][i][1] = o[h][i][2] = o[h][i][3] = 0.f;
+    }
+    scale = p.scale * 1.44269504f;
+  }
+
+  __device__ __forceinline__ void block(uint32_t keys, uint32_t values, uint32_t there, int lane, float *weights) {
+    constexpr int kRow = D * 4;
+    const int key = lane % kKeys, piece = lane / kKeys;
+    uint64_t x2[HB] = {};
+#pragma unroll 4
+    for (int i = 0; i < kQuads / kLanes; ++i) {
+      const int c = i * kLanes + piece;
+      const uint4 k = lds(keys + key * kRow + stored<true, false>(key, c) * 16);
+      const uint64_t k0 = f32x2::pair(__uint_as_float(k.x), __uint_as_float(k.y));
+      const uint64_t k1 = f32x2::pair(__uint_as_float(k.z), __uint_as_float(k.w));
+#pragma unroll
+      for (int h = 0; h < HB; ++h) {
+        const float4 a = *reinterpret_cast<const float4 *>(q + h * D + 4 * c);
+        x2[h] = f32x2::fma(k0, f32x2::pair(a.x, a.y), x2[h]);
+        x2[h] = f32x2::fma(k1, f32x2::pair(a.z, a.w), x2[h]);
+      }
+    }
+    const bool on = there >> key & 1;
+    float keep[HB];
+    bool moved = false;
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      float pair[2];
+      f32x2::split(x2[h], pair);
+      float x = pair[0] + pair[1];
+#pragma unroll
+      for (int d = kKeys; d < 32; d *= 2) x += __shfl_xor_sync(~0u, x, d);
+      x = on ? x * scale : -INFINITY;
+      float top = x;
+#pragma unroll
+      for (int d = 1; d < kKeys; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      const float now = fmaxf(m[h], top), base = now == -INFINITY ? 0.f : now;
+      keep[h] = sm100::ex2(m[h] - base);
+      moved |= now > m[h];
+      m[h] = now;
+      const float w = sm100::ex2(x - base);
+      l[h] = fmaf(l[h], keep[h], w);
+      if (piece == 0) weights[key * HB + h] = w;
+    }
+    __syncwarp();
+    if (moved)
+#pragma unroll
+      for (int h = 0; h < HB; ++h)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][i][e] *= keep[h];
+    const int quad = lane % (kQuads >= 32 ? 32 : kQuads), half = kQuads >= 32 ? 0 : lane / kQuads;
+#pragma unroll 4
+    for (int i = 0; i < kKeys / kSplit; ++i) {
+      const int row = i * kSplit + half;
+      const float4 w0 = *reinterpret_cast<const float4 *>(weights + row * HB);
+      const float4 w1 = *reinterpret_cast<const float4 *>(weights + row * HB + 4);
+      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const uint4 u = lds(values + row * kRow + stored<true, true>(row, quad + 32 * j) * 16);
+        const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+#pragma unroll
+        for (int h = 0; h < HB; ++h) f32x2::vfma(o[h][j], v, w[h], o[h][j]);
+      }
+    }
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void end(float *sums, float2 *ml, int lane) {
+    const int quad = lane % (kQuads >= 32 ? 32 : kQuads);
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+#pragma unroll
+      for (int d = 1; d < kKeys; d *= 2) l[h] += __shfl_xor_sync(~0u, l[h], d);
+      if (lane == 0) ml[h] = make_float2(m[h], l[h]);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+#pragma unroll
+        for (int d = kQuads; d < 32; d *= 2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][j][e] += __shfl_xor_sync(~0u, o[h][j][e], d);
+        if (lane < kQuads)
+          reinterpret_cast<float4 *>(sums + h * D)[quad + 32 * j] = make_float4(o[h][j][0], o[h][j][1], o[h][j][2], o[h][j][3]);
+      }
+    }
+  }
+  static __device__ __forceinline__ int quad(int, int c) { return c; }
+};
+
+template <typename T> __device__ __forceinline__ void store4(T *dst, float4 v) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(dst) = v;
+  else *reinterpret_cast<uint2 *>(dst) = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
+}
+
+// A row's result from its sums: maximum m (of log2) and sum l.
 template <typename T>
-void launch(const PagedAttn &p, cudaStream_t stream) {
+__device__ __forceinline__ void finish(const PagedAttn &p, int s, int h, int D, int quad, float m, float l, float4 v) {
+  const float f = l > 0.f ? 1.f / l : 0.f;
+  const size_t row = (size_t)s * p.H + h;
+  store4(static_cast<T *>(p.o) + row * D + 4 * quad, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+  if (quad == 0 && p.lse) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+}
+
+template <typename T, int D, int HB>
+__global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const Split sp, const FastDiv by_page) {
+  using S = Shape<T, D, HB>;
+  constexpr int kUnit = S::kUnit, kKeys = S::kKeys, kChunks = S::kChunks, kStages = S::kStages;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 ml[kWarps][HB];
+  __shared__ uint32_t masks[kWarps][kStages];
+  __shared__ long long scan[kWarps];
+  __shared__ long long start_units;
+  __shared__ int start_seq;
+  float *sums = reinterpret_cast<float *>(smem + kStages * S::kStage * kWarps);  // [kWarps][HB][D]
+  float *aside = nullptr;  // float32: the queries where the sums will be, the weights behind them
+  if constexpr (S::kF32) aside = sums + HB * D + (threadIdx.x >> 5) * kKeys * HB;
+  static_assert(!S::kF32 || kWarps * HB * D >= HB * D + kWarps * kKeys * HB, "");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // the CTA's run of units [t0, t1)
+  Cursor<kUnit> at = {};
+  long long t0, t1, base, share = 0;
+  if (sp.whole) {
+    at.s = blockIdx.x / sp.parts;
+    at.part = blockIdx.x % sp.parts;
+    const Range r = places_of(p, at.s);
+    at.first = r.first;
+    at.len = r.len;
+    at.units = (r.len - r.first + kUnit - 1) / kUnit;
+    at.left = at.units;
+    t0 = base = 0;
+    t1 = at.units;
+  } else {
+    const int per = (p.n + kThreads - 1) / kThreads, a = min(tid * per, p.n), b = min(a + per, p.n);
+    long long mine = 0;
+    for (int s = a; s < b; ++s) {
+      const Range r = places_of(p, s);
+      mine += (r.len - r.first + kUnit - 1) / kUnit;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long o = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) scan[warp] = upto;
+    if (tid == 0) sp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) upto += scan[w];
+      total += scan[w];
+    }
+    total *= sp.parts;
+    share = max((total + gridDim.x - 1) / gridDim.x, (long long)sp.least);
+    t0 = blockIdx.x * share;
+    t1 = min(t0 + share, total);
+    // sequences without a place, by whoever comes to them first
+    if (t0 >= t1) {
+      at.left = 0;
+    } else {
+      long long before = (upto - mine) * sp.parts;
+      if (before <= t0 && t0 < upto * sp.parts) {
+        for (int s = a; s < b; ++s) {
+          const Range r = places_of(p, s);
+          const long long u = (long long)((r.len - r.first + kUnit - 1) / kUnit) * sp.parts;
+          if (t0 < before + u) {
+            start_seq = s;
+            start_units = before;
+            break;
+          }
+          before += u;
+        }
+      }
+      __syncthreads();
+      at.s = start_seq;
+      at.enter(p);
+      base = start_units;
+      at.part = static_cast<int>((t0 - base) / at.units);
+      at.unit = static_cast<int>((t0 - base) % at.units);
+      at.left = t1 - t0;
+    }
+    // rows of sequences without a place
+    for (int s = blockIdx.x; s < p.n; s += gridDim.x) {
+      const Range r = places_of(p, s);
+      if (r.len > r.first) continue;
+      for (int i = tid; i < p.H * (D / 4); i += kThreads)
+        finish<T>(p, s, i / (D / 4), D, i % (D / 4), 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    if (at.left == 0) return;
+  }
+
+  // the ring
+  const uint32_t ring = sm100::smem_u32(smem) + warp * kStages * S::kStage;
+  Cursor<kUnit> to = at;  // where the copies are
+  auto load = [&](int stage) {
+    const int i = to.first + to.unit * kUnit + warp * kKeys + lane % kKeys;
+    long long off = -1;
+    if (i < to.len) {
+      uint32_t pg, r;
+      by_page.split(i, pg, r);
+      const int page = __ldg(p.at.table + to.s * p.at.ld_table + pg);
+      if (page >= 0 && page < p.at.n_pages) off = page * p.at.ld_page + ((long long)r * p.Hk + to.part / sp.blocks) * D;
+    }
+    const uint32_t there = __ballot_sync(~0u, off >= 0) & ((1u << kKeys) - 1);
+    if (lane == 0) masks[warp][stage] = there;
+    if (there) {
+      const uint32_t keys = ring + stage * S::kStage, values = keys + S::kTile;
+#pragma unroll
+      for (int j = 0; j < kKeys * kChunks / 32; ++j) {
+        const int c = j * 32 + lane, row = c / kChunks, chunk = c % kChunks;
+        const long long o = __shfl_sync(~0u, off, row);
+        const long long e = (o < 0 ? 0 : o) + chunk * (16 / (int)sizeof(T));
+        copy16(keys + (row * kChunks + stored<S::kF32, false>(row, chunk)) * 16, static_cast<const T *>(p.k_cache) + e, o >= 0);
+        copy16(values + (row * kChunks + stored<S::kF32, true>(row, chunk)) * 16, static_cast<const T *>(p.v_cache) + e, o >= 0);
+      }
+    }
+    to.next(p, sp.parts);
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (to.left > 0) load(i);
+    commit();
+  }
+
+  using Warp = std::conditional_t<S::kF32, F32Warp<D, HB>, Bf16Warp<D, HB>>;
+  Warp w;
+  const int share_heads = p.H / p.Hk;
+  int stage = 0;
+  bool fresh = true;
+  long long t = t0;  // units in front of this one
+  long long part_begin = sp.whole ? 0 : base + (long long)at.part * at.units;
+  if (at.left == 0) w.begin(p, at.s, 0, 0, lane, sums);  // a whole part without a place
+  while (true) {
+    const int h0 = at.part / sp.blocks * share_heads + at.part % sp.blocks * HB;
+    const int heads = min(HB, share_heads - at.part % sp.blocks * HB);
+    bool last = true;
+    if (at.left > 0) {
+      if (fresh) w.begin(p, at.s, h0, heads, lane, sums);
+      wait_all_but<kStages - 2>();
+      __syncwarp();
+      const int free = stage == 0 ? kStages - 1 : stage - 1;
+      const uint32_t there = masks[warp][stage];
+      if (to.left > 0) load(free);
+      commit();
+      if (there) {
+        const uint32_t keys = ring + stage * S::kStage;
+        w.block(keys, keys + S::kTile, there, lane, aside);
+      }
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      ++t;
+      last = at.unit + 1 == at.units || at.left == 1;
+    }
+    fresh = last;
+    if (last) {
+      if (S::kF32) __syncthreads();  // the queries are where the sums go
+      w.end(sums + warp * HB * D, ml[warp], lane);
+      __syncthreads();
+      const long long part_end = part_begin + at.units;
+      const bool begun = part_begin >= t0, done = part_end <= t1;
+      for (int i = tid; i < HB * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), c = i % (D / 4);
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) m = fmaxf(m, ml[k][h].x);
+        const float zero = m == -INFINITY ? 0.f : m;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float f = sm100::ex2(ml[k][h].x - zero);
+          const float4 a = reinterpret_cast<const float4 *>(sums + (k * HB + h) * D)[Warp::quad(h, c)];
+          l = fmaf(f, ml[k][h].y, l);
+          v.x = fmaf(f, a.x, v.x); v.y = fmaf(f, a.y, v.y); v.z = fmaf(f, a.z, v.z); v.w = fmaf(f, a.w, v.w);
+        }
+        if (begun && done) {
+          if (h < heads) finish<T>(p, at.s, h0 + h, D, c, m, l, v);
+        } else {
+          const size_t piece = 2 * (size_t)blockIdx.x + begun;
+          reinterpret_cast<float4 *>(sp.sums + (piece * HB + h) * D)[c] = v;
+          if (c == 0) sp.ml[piece * HB + h] = make_float2(m, l);
+        }
+      }
+      if (begun && !done && tid == 0) sp.joins[blockIdx.x] = make_int4(at.s, at.part, static_cast<int>((part_end - 1) / share), 0);
+      if (at.left <= 1) return;
+      part_begin = part_end;
+      __syncthreads();
+    }
+    at.next(p, sp.parts);
+  }
+}
+
+// The pieces of a part, of the CTAs first .. last, added up: block (first, some of the heads).
+template <typename T, int D, int HB>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn p, const Split sp) {
+  constexpr int kQuads = D / 4;
+  __shared__ float4 sums[kJoinThreads];
+  __shared__ float2 ml[kJoinThreads];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 join = sp.joins[blockIdx.x];
+  if (join.x < 0) return;
+  const int each = HB / gridDim.y, share_heads = p.H / p.Hk, block = join.y % sp.blocks;
+  const int heads = min(HB, share_heads - block * HB), h0 = join.y / sp.blocks * share_heads + block * HB;
+  const int items = each * kQuads, groups = max(kJoinThreads / items, 1);
+  const int pieces = join.z - blockIdx.x + 1;
+  for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
+    const int i = i0 + threadIdx.x % min(items, kJoinThreads), group = threadIdx.x / min(items, kJoinThreads);
+    const int h = blockIdx.y * each + i / kQuads, c = i % kQuads;
+    float m = -INFINITY, l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (h < heads) {
+#pragma unroll 4
+      for (int k = group; k < pieces; k += groups) {
+        const size_t piece = 2 * (size_t)(blockIdx.x + k) + (k == 0);
+        const float2 b = sp.ml[piece * HB + h];
+        const float4 a = reinterpret_cast<const float4 *>(sp.sums + (piece * HB + h) * D)[c];
+        const float now = fmaxf(m, b.x), zero = now == -INFINITY ? 0.f : now;
+        const float f = sm100::ex2(m - zero), e = sm100::ex2(b.x - zero);
+        l = l * f + b.y * e;
+        v = make_float4(v.x * f + a.x * e, v.y * f + a.y * e, v.z * f + a.z * e, v.w * f + a.w * e);
+        m = now;
+      }
+    }
+    if (groups > 1) {
+      sums[threadIdx.x] = v;
+      ml[threadIdx.x] = make_float2(m, l);
+      __syncthreads();
+      if (group == 0) {
+        for (int g = 1; g < groups; ++g) {
+          const float2 b = ml[g * items + threadIdx.x];
+          const float4 a = sums[g * items + threadIdx.x];
+          const float now = fmaxf(m, b.x), zero = now == -INFINITY ? 0.f : now;
+          const float f = sm100::ex2(m - zero), e = sm100::ex2(b.x - zero);
+          l = l * f + b.y * e;
+          v = make_float4(v.x * f + a.x * e, v.y * f + a.y * e, v.z * f + a.z * e, v.w * f + a.w * e);
+          m = now;
+        }
+      }
+    }
+    if (group == 0 && h < heads) finish<T>(p, join.x, h0 + h, D, c, m, l, v);
+  }
+}
+
+int fail(const char *what, cudaError_t e) {
+  set_error("la_paged_attn: %s: %s", what, cudaGetErrorString(e));
+  return LA_ERR_CUDA;
+}
+
+// Units below which a part is not split.
+constexpr int kLeast = 2;
+
+template <typename T, int D, int HB>
+int launch(const PagedAttn &p, cudaStream_t stream) {
+  using S = Shape<T, D, HB>;
+  auto kernel = attn_kernel<T, D, HB>;
+  static std::atomic<bool> ready[64];  // once for each device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail("no device", e);
+  if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    if (e != cudaSuccess) return fail("shared memory", e);
+    if (dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  Split sp = {};
+  sp.blocks = (p.H / p.Hk + HB - 1) / HB;
+  sp.parts = p.Hk * sp.blocks;
+  sp.least = kLeast;
+  const long long most = (long long)p.at.max_pages * p.at.page_size;
+  long long longest = p.max_len > 0 ? std::min<long long>(p.max_len, most) : most;
+  if (p.window > 0) longest = std::min<long long>(longest, p.window);
+  const long long parts = (long long)p.n * sp.parts, slots = (S::kTwo ? 2 : 1) * std::max(sm_count(), 1);
+  sp.whole = longest <= (long long)kLeast * S::kUnit;
   const FastDiv by(p.at.page_size);
-  const unsigned grid = static_cast<unsigned>(p.n) * p.H;
-  if (p.d == 64) attn_kernel<T, 64><<<grid, kThreads, 0, stream>>>(p, by);
-  else if (p.d == 128) attn_kernel<T, 128><<<grid, kThreads, 0, stream>>>(p, by);
-  else attn_kernel<T, 256><<<grid, kThreads, 0, stream>>>(p, by);
+  if (sp.whole) {
+    kernel<<<static_cast<unsigned>(parts), kThreads, S::kBytes, stream>>>(p, sp, by);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? LA_OK : fail("launch failed", e);
+  }
+  const long long units = (longest + S::kUnit - 1) / S::kUnit * parts;
+  const int ctas = static_cast<int>(std::min(slots, (units + kLeast - 1) / kLeast));
+  const size_t sums = (size_t)2 * ctas * HB * D * 4, ml = (size_t)2 * ctas * HB * sizeof(float2);
+  cudaMemPool_t pool = library_pool();
+  if (!pool) return fail("could not create the workspace pool", cudaGetLastError());
+  uint8_t *ws = nullptr;
+  e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), sums + ml + (size_t)ctas * sizeof(int4), pool, stream);
+  if (e != cudaSuccess) return fail("workspace allocation failed", e);
+  sp.sums = reinterpret_cast<float *>(ws);
+  sp.ml = reinterpret_cast<float2 *>(ws + sums);
+  sp.joins = reinterpret_cast<int4 *>(ws + sums + ml);
+  kernel<<<ctas, kThreads, S::kBytes, stream>>>(p, sp, by);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, parts <= 64 ? HB : 1);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, join_kernel<T, D, HB>, p, sp);
+  }
+  const cudaError_t f = cudaFreeAsync(ws, stream);
+  if (e == cudaSuccess) e = f;
+  return e == cudaSuccess ? LA_OK : fail("launch failed", e);
+}
+
+template <int D> int launch_d(const PagedAttn &p, cudaStream_t stream) {
+  if (p.f32) return launch<float, D, 8>(p, stream);
+  return p.H / p.Hk <= 8 ? launch<__nv_bfloat16, D, 8>(p, stream) : launch<__nv_bfloat16, D, 16>(p, stream);
 }
 
 }  // namespace
 
 int launch_paged_attn(const PagedAttn &p, cudaStream_t stream) {
-  if (p.f32) launch<float>(p, stream);
-  else launch<__nv_bfloat16>(p, stream);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) {
-    set_error("la_paged_attn: launch failed: %s", cudaGetErrorString(e));
-    return LA_ERR_CUDA;
-  }
-  return LA_OK;
+  return p.d == 64 ? launch_d<64>(p, stream) : p.d == 128 ? launch_d<128>(p, stream) : launch_d<256>(p, stream);
 }
 
 }  // namespace la

@@ -55,7 +55,7 @@ int la_cache_append(const void *q, const void *k, const void *v, void *q_out, vo
     return bad(fn, "token strides must cover a token's heads");
   if (total == 0 || n_seq == 0) return LA_OK;
   if (!k || !v || !lens) return bad(fn, "k, v and lens are required");
-  if (max_pages > 0 && n_pages > 0 && (!table || !k_cache || !v_cache)) return bad(fn, "table and caches are required");
+  if (max_pages > 0 && (!table || (n_pages > 0 && (!k_cache || !v_cache)))) return bad(fn, "table and caches are required");
   const size_t el = (flags & LA_F32) ? 4 : 2;
   const void *all[] = {q, k, v, q_out, k_cache, v_cache};
   for (const void *t : all)
@@ -90,7 +90,7 @@ int la_paged_attn(const void *q, const void *k_cache, const void *v_cache, void 
   if ((long long)n * H > INT_MAX / 2) return bad(fn, "n*H too large");
   if (n == 0) return LA_OK;
   if (!q || !o || !lens) return bad(fn, "q, o and lens are required");
-  if (max_pages > 0 && n_pages > 0 && (!table || !k_cache || !v_cache)) return bad(fn, "table and caches are required");
+  if (max_pages > 0 && (!table || (n_pages > 0 && (!k_cache || !v_cache)))) return bad(fn, "table and caches are required");
   if (!at(q, 16) || !at(o, 16) || !at(k_cache, 16) || !at(v_cache, 16) || !at(lse, 4))
     return bad(fn, "tensors must be 16-byte aligned, lse 4-byte aligned");
   if (same({o, lse}, {q, k_cache, v_cache})) return bad(fn, "outputs must not be inputs, nor one another");

@@ -70,7 +70,7 @@ int la_cache_append(const void *q, const void *k, const void *v, void *q_out, vo
  *     o_h = sum_p softmax_p(scale q_h . k_p) v_p
  *
  * over the places p of max(0, L - window) .. L - 1, L = lens[s] (at most
- * max_pages*page_size; window = 0: all of them), without those that have no
+ * max_pages*page_size, and 2^31 - 2^16; window = 0: all of them), without those that have no
  * page. A sequence with no place (L <= 0) gives o = 0, and lse = -infinity.
  *
  *   q       [n][H][d], token stride ldq
