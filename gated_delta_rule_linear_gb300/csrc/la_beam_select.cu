@@ -6,21 +6,23 @@
 // and the segment's part of the sum. The second takes a request: the log of each
 // beam's sum, the segments' candidates' scores in 64 bits, and their K best.
 //
-// K best of a segment. A thread holds 16 elements; each warp sorts its lanes'
-// largest, and no element below a warp's K-th largest lane can be among the K
-// best: the highest of these bounds leaves little more than K elements, which
-// are collected and sorted. Keys are value and index together, so that equal
-// logits (bfloat16 has many) neither break the order nor the bound on how many
-// are collected.
+// K best of a segment. A thread holds 8, 16 or 32 elements; each warp sorts its
+// lanes' largest, and no element below a warp's K-th largest lane can be among
+// the K best: the highest of these bounds leaves little more than K elements, of
+// a few threads, which are collected and sorted as (value, index). Rows with so
+// many equal logits that the list runs over go round by round instead.
 //
-// The sum. exp(x - max) with 24 bits (a polynomial: the special-function unit's
-// 22 bits would blur the comparison of two beams), summed in pairs inside a
-// thread and in 64-bit fixed point across threads: the sum does not depend on
-// the order, two beams with the same logits get the same one.
+// The sum. exp2((x - max) log2 e), in pairs inside a thread, in 64-bit fixed point
+// across threads and segments: what is added does not depend on where a row lies
+// or which threads had it, so that two beams with the same logits get the same
+// sum. Rows that do not start at 16 bytes are therefore shifted into place.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <algorithm>
+
 #include "la_serve_internal.h"
+#include "la_sm100.cuh"
 
 namespace la {
 namespace {
@@ -28,9 +30,9 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPer = 16;                       // elements of a thread
-constexpr int kSegment = kThreads * kPer;
-constexpr double kFixed = 17592186044416.0;    // 2^44: a segment's sum of at most 4096 stays below 2^57
+constexpr int kList = 512;                    // elements that a segment's bound may leave
+constexpr float kLog2e = 1.44269504f;
+constexpr float kFixed = 17592186044416.f;    // 2^44: a segment's sum of at most 8192 stays below 2^58
 
 // What the first kernel leaves of a segment; its K keys are in an array of their own.
 struct Segment {
@@ -49,30 +51,10 @@ __device__ __forceinline__ float unordered(unsigned u) {
   return __int_as_float(b ^ (b >> 31 & 0x7fffffff));
 }
 
-constexpr unsigned kPlusInf = 0xff800000u;  // ordered(+infinity); NaNs are above (x + 0 has made them positive)
-
-// exp(x), x <= 0, to about 2^-24: x = (n + f) ln 2 with the product's rounding carried along, then the
-// series of 2^f = exp(f ln 2) for |f| <= 1/2 to its seventh power (2^-27 off).
-__device__ __forceinline__ float exp_of(float x) {
-  x = fmaxf(x, -87.f);  // below: 1e-38 each
-  const float t = x * 1.44269504f;
-  const float lo = fmaf(x, 1.44269504f, -t) + x * 1.925963033e-8f;
-  const float n = rintf(t);
-  const float f = ((t - n) + lo) * 0.693147181f;
-  float y = 1.f / 5040;
-  y = fmaf(y, f, 1.f / 720);
-  y = fmaf(y, f, 1.f / 120);
-  y = fmaf(y, f, 1.f / 24);
-  y = fmaf(y, f, 1.f / 6);
-  y = fmaf(y, f, 0.5f);
-  y = fmaf(y, f, 1.f);
-  y = fmaf(y, f, 1.f);
-  return y * __int_as_float((static_cast<int>(n) + 127) << 23);
-}
-
 // Bitonic exchange with the lane j away; `top` keeps the larger key.
-__device__ __forceinline__ u64 exchange(u64 k, int j, bool top) {
-  const u64 o = __shfl_xor_sync(~0u, k, j);
+template <typename Word>
+__device__ __forceinline__ Word exchange(Word k, int j, bool top) {
+  const Word o = __shfl_xor_sync(~0u, k, j);
   return (o > k) == top ? o : k;
 }
 struct Key128 {  // a candidate: score (ordered), then the order of w * V + v; 0, 0: none
@@ -111,102 +93,161 @@ __device__ __forceinline__ Key merged(Key a, const Key &b, int lane) {
   return a;
 }
 
-template <typename T, bool WIDE>
+// max(a, b), NaN if one of them is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 16 bytes of a row of logits at element v of it: E elements, -infinity behind the row's end. SHIFT: the row may start
+// anywhere, `off` bytes behind a multiple of 16; the granules of 16 bytes are read whole, but never outside [lo, hi).
+template <typename T, bool SHIFT, int E>
+__device__ __forceinline__ void load_row(const T *x, int v, int V, int off, const char *lo, const char *hi, float (&f)[E]) {
+  static_assert(E * sizeof(T) == 16, "");
+  unsigned w[4];
+  const char *at = reinterpret_cast<const char *>(x + v) - off;
+  const bool whole = v + E <= V;
+  if (whole && (!SHIFT || (at >= lo && at + (off ? 32 : 16) <= hi))) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(at));
+    if constexpr (SHIFT) {
+      uint4 b = a;
+      if (off) b = __ldcs(reinterpret_cast<const uint4 *>(at) + 1);  // the next thread's, from L1
+      const unsigned in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      const unsigned bits = off % 4 * 8;
+      switch (off / 4) {
+#define LA_SHIFTED(Q)                                                                                \
+  case Q:                                                                                            \
+    _Pragma("unroll") for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(in[Q + i], in[Q + i + (Q + i < 7)], bits); \
+    break;
+        LA_SHIFTED(0) LA_SHIFTED(1) LA_SHIFTED(2) LA_SHIFTED(3)
+#undef LA_SHIFTED
+      }
+    } else {
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if constexpr (sizeof(T) == 4) f[e] = __uint_as_float(w[e]);
+      else f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = v + e < V ? static_cast<float>(x[v + e]) : -INFINITY;
+  }
+}
+
+// A segment: kThreads * PER elements of a row.
+template <typename T, int PER, bool SHIFT>
 __global__ void __launch_bounds__(kThreads) segment_kernel(const BeamSelect p, int segments, Segment *seg, u64 *keys) {
-  __shared__ u64 list[kSegment];
-  __shared__ u64 bound[kWarps], sums[kWarps];
-  __shared__ unsigned most[kWarps];
+  constexpr int E = 16 / sizeof(T), N = PER / E, kSegment = kThreads * PER;
+  __shared__ u64 list[kList];
+  __shared__ u64 sums[kWarps];
+  __shared__ float bounds[kWarps], tops[kWarps];
   __shared__ int count;
   const int row = blockIdx.x / segments, j = blockIdx.x % segments, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (p.done && p.done[row]) return;
   const T *x = static_cast<const T *>(p.logits) + row * p.ld;
-  const int v0 = j * kSegment;
-  constexpr int E = WIDE ? 16 / sizeof(T) : 1;
-  // element e of the thread's i-th vector is v0 + (i * kThreads + tid) * E + e
-  float f[kPer];
+  const int v0 = j * kSegment + tid * E;  // element e of the thread's i-th vector is v0 + i * kThreads * E + e
+  const char *lo = static_cast<const char *>(p.logits);
+  const char *hi = reinterpret_cast<const char *>(static_cast<const T *>(p.logits) + ((size_t)p.B * p.W - 1) * p.ld + p.V);
+  const int off = SHIFT ? static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15) : 0;
+  float f[N][E];
 #pragma unroll
-  for (int i = 0; i < kPer / E; ++i) {
-    const int v = v0 + (i * kThreads + tid) * E;
-    if constexpr (E == 1) {
-      f[i] = v < p.V ? static_cast<float>(x[v]) : -INFINITY;
-    } else {
-      if (v + E <= p.V) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(x + v));
-        const unsigned a[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if constexpr (sizeof(T) == 4) f[i * E + e] = __uint_as_float(a[e]);
-          else f[i * E + e] = __uint_as_float(e & 1 ? a[e / 2] & 0xffff0000u : a[e / 2] << 16);
-        }
-      } else {  // the row ends inside, or before
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[i * E + e] = v + e < p.V ? static_cast<float>(x[v + e]) : -INFINITY;
-      }
-    }
-  }
+  for (int i = 0; i < N; ++i) load_row<T, SHIFT, E>(x, v0 + i * kThreads * E, p.V, off, lo, hi, f[i]);
   if (tid == 0) count = 0;
-  // the largest of the thread, with the lowest index: key 0 for places behind the row's end
-  u64 top = 0;
-  auto key = [&](int i) {
-    const int v = v0 + (i / E * kThreads + tid) * E + i % E;
-    return v < p.V ? (u64)ordered(f[i]) << 32 | ~static_cast<unsigned>(v) : 0ull;
-  };
+  float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    f[i] += 0.f;  // one zero, and one NaN
-    const u64 k = key(i);
-    if (k > top) top = k;
-  }
-  const u64 order = sorted(top, lane);
-  const u64 kth = __shfl_sync(~0u, order, p.K - 1);
-  if (lane == 0) {
-    bound[warp] = kth;
-    most[warp] = static_cast<unsigned>(order >> 32);
-  }
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) top = max_nan(top, f[i][e]);
+  const bool nan = isnan(top);
+  if (nan) top = INFINITY;
+  // the warp's K-th largest lane, as ordered integers (+0 and -0 alike)
+  const unsigned order = sorted(ordered(top + 0.f), lane);
+  if (lane == 0) tops[warp] = unordered(order);
+  if (lane == p.K - 1) bounds[warp] = unordered(order);
   __syncthreads();
-  u64 low = 0;
-  unsigned high = 0;
+  float low = bounds[0], m = tops[0];
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    low = bound[i] > low ? bound[i] : low;
-    high = max(high, most[i]);
+  for (int i = 1; i < kWarps; ++i) {
+    low = fmaxf(low, bounds[i]);
+    m = fmaxf(m, tops[i]);
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const u64 k = key(i);
-    if (k && k >= low) list[atomicAdd(&count, 1)] = k;
-  }
-  const bool bad = high >= kPlusInf;
-  const float m = unordered(high);
+  const bool bad = m == INFINITY;
   // the sum, where there is one
   u64 sum = 0;
   if (!bad && m > -INFINITY) {
-    float e[kPer];
+    float t[N];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) e[i] = key(i) ? exp_of(f[i] - m) : 0.f;
+    for (int i = 0; i < N; ++i) {
+      float g[E];
 #pragma unroll
-    for (int n = kPer / 2; n > 0; n /= 2)
+      for (int e = 0; e < E; ++e) g[e] = sm100::ex2((f[i][e] - m) * kLog2e);
 #pragma unroll
-      for (int i = 0; i < n; ++i) e[i] += e[i + n];
-    sum = static_cast<u64>(static_cast<double>(e[0]) * kFixed);
+      for (int n = E / 2; n > 0; n /= 2)
+#pragma unroll
+        for (int e = 0; e < n; ++e) g[e] += g[e + n];
+      t[i] = g[0];
+    }
+#pragma unroll
+    for (int n = N / 2; n > 0; n /= 2)
+#pragma unroll
+      for (int i = 0; i < n; ++i) t[i] += t[i + n];
+    sum = static_cast<u64>(t[0] * kFixed);
   }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
   if (lane == 0) sums[warp] = sum;
+  auto key = [&](int i, int e) {
+    const int v = v0 + i * kThreads * E + e;
+    return v < p.V ? (u64)ordered(f[i][e] + 0.f) << 32 | ~static_cast<unsigned>(v) : 0ull;
+  };
+  // (a bad row's candidates are not looked at)
+  if (!bad && top >= low)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (f[i][e] >= low && v0 + i * kThreads * E + e < p.V) {
+          const int at = atomicAdd(&count, 1);
+          if (at < kList) list[at] = key(i, e);
+        }
   __syncthreads();
-  // the list's K best: every warp sorts what it takes of it, the first one joins them
   const int n = count;
   u64 best = 0;
-  for (int i = warp * 32; i < n; i += kThreads) {
-    const u64 k = sorted(i + lane < n ? list[i + lane] : 0, lane);
-    best = merged(best, k, lane);
-  }
-  if (n > 32) {
-    __syncthreads();
-    list[tid] = best;
-    __syncthreads();
-    if (warp == 0)
-      for (int i = 1; i < min(kWarps, (n + 31) / 32); ++i) best = merged(best, list[i * 32 + lane], lane);
+  if (n > kList) {
+    // the next one below the last, K times
+    u64 last = ~0ull;
+    for (int k = 0; k < p.K; ++k) {
+      u64 mine = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const u64 c = key(i, e);
+          if (c < last && c > mine) mine = c;
+        }
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) mine = max(mine, __shfl_xor_sync(~0u, mine, d));
+      if (lane == 0) list[(k & 1) * kWarps + warp] = mine;
+      __syncthreads();
+      last = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) last = max(last, list[(k & 1) * kWarps + i]);
+      if (lane == k) best = last;
+    }
+  } else {
+    // every warp sorts what it takes of the list, the first one joins them
+    for (int i = warp * 32; i < n; i += kThreads) best = merged(best, sorted(i + lane < n ? list[i + lane] : 0, lane), lane);
+    if (n > 32) {
+      __syncthreads();
+      list[tid] = best;
+      __syncthreads();
+      if (warp == 0)
+        for (int i = 1; i < min(kWarps, (n + 31) / 32); ++i) best = merged(best, list[i * 32 + lane], lane);
+    }
   }
   if (warp == 0) {
     if (lane < p.K) keys[(size_t)blockIdx.x * p.K + lane] = best;
@@ -228,72 +269,113 @@ __device__ __forceinline__ double unordered(u64 u) {
   return __longlong_as_double(b ^ (b >> 63 & 0x7fffffffffffffffll));
 }
 
-__global__ void __launch_bounds__(kThreads) select_kernel(const BeamSelect p, int segments, const Segment *seg, const u64 *keys) {
+// exp(x) for x <= 0, to about 2^-24, as a factor of 2^32.
+__device__ __forceinline__ unsigned weight(float x) {
+  return x == 0.f ? ~0u : __float2uint_rz(expf(x) * 4294967296.f);
+}
+
+constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect p, int segments, const Segment *seg,
+                                                                const u64 *keys) {
   __shared__ double lse[kMaxBeams];   // of each beam; NaN: its candidates have no value
-  __shared__ Key128 lists[kThreads];
+  __shared__ u64 total[kMaxBeams];
+  __shared__ float tops[kMaxBeams];
+  __shared__ u64 bounds[kSelectWarps];
+  __shared__ Key128 list[kList];
+  __shared__ int count;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int w = warp; w < p.W; w += kWarps) {
-    const int row = b * p.W + w;
-    double value = CUDART_NAN;
-    const float score = p.scores[row];
-    const bool ends = p.done && p.done[row];
-    if (!ends && isfinite(score)) {
-      const Segment *s = seg + (size_t)row * segments;
-      float m = -INFINITY;
-      int bad = 0;
-      for (int i = lane; i < segments; i += 32) {
-        m = fmaxf(m, s[i].max);
-        bad |= s[i].bad;
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-      if (!__any_sync(~0u, bad) && m > -INFINITY) {
-        double sum = 0;
-        for (int i = lane; i < segments; i += 32)
-          if (s[i].sum) sum += static_cast<double>(s[i].sum) * (1.0 / kFixed) * exp(static_cast<double>(s[i].max) - m);
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
-        value = m + log(sum);
-      }
+  const float *scores = p.scores + b * p.W;
+  const unsigned char *done = p.done ? p.done + b * p.W : nullptr;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0) count = 0;
+  for (int w = warp; w < p.W; w += kSelectWarps) {
+    if (done && done[w]) continue;
+    const Segment *s = seg + (size_t)(b * p.W + w) * segments;
+    float m = -INFINITY;
+    bool bad = false;
+    for (int i = lane; i < segments; i += 32) {
+      m = fmaxf(m, s[i].max);
+      bad |= s[i].bad != 0;
     }
-    if (lane == 0) lse[w] = value;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    if (__any_sync(~0u, bad) || m == -INFINITY) {
+      if (lane == 0) total[w] = 0;
+      continue;
+    }
+    u64 sum = 0;
+    for (int i = lane; i < segments; i += 32) {
+      const unsigned f = s[i].sum ? weight(s[i].max - m) : 0;
+      sum += f == ~0u ? s[i].sum : __umul64hi(s[i].sum, (u64)f << 32);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
+    if (lane == 0) {
+      total[w] = sum;
+      tops[w] = m;
+    }
+  }
+  __syncthreads();
+  if (tid < p.W) {  // all logs of a request in one warp: 64-bit instructions are few on this chip
+    double value = CUDART_NAN;
+    if (!(done && done[tid]) && total[tid] && isfinite(scores[tid])) value = tops[tid] + log((double)total[tid] * (1.0 / kFixed));
+    lse[tid] = value;
   }
   __syncthreads();
   const u64 none = ordered(-(double)INFINITY);
+  const int each = segments * p.K, lists = p.W * segments;
+  // the r-th candidate of segment j of beam w; each segment's come in descending order
+  auto candidate = [&](int w, int j, int r) -> Key128 {
+    const int at = j * p.K + r;
+    if (done && done[w]) {
+      // eos, and the first tokens besides it without a value
+      if (at == 0) return {isfinite(scores[w]) ? ordered((double)scores[w]) : none, ~static_cast<unsigned>(w * p.V + p.eos)};
+      if (at < p.K && at < p.V) return {none, ~static_cast<unsigned>(w * p.V + at - (at <= p.eos))};
+      return {0, 0};
+    }
+    if (isnan(lse[w])) return at < p.K && at < p.V ? Key128{none, ~static_cast<unsigned>(w * p.V + at)} : Key128{0, 0};
+    const u64 c = keys[(size_t)(b * p.W + w) * each + at];
+    if (!c) return {0, 0};
+    const double x = (double)scores[w] + ((double)unordered(static_cast<unsigned>(c >> 32)) - lse[w]);
+    return {ordered(x), ~(static_cast<unsigned>(w * p.V) + ~static_cast<unsigned>(c))};
+  };
+  // as in a segment: the K-th of the lists' first candidates bounds what can be among the K best
+  u64 head = 0;
+  for (int i = tid; i < lists; i += kSelectThreads) head = max(head, candidate(i / segments, i % segments, 0).score);
+  const u64 order = sorted(head, lane);
+  if (lane == p.K - 1) bounds[warp] = order;
+  __syncthreads();
+  u64 low = 1;
+#pragma unroll
+  for (int i = 0; i < kSelectWarps; ++i) low = max(low, bounds[i]);
+  for (int i = tid; i < lists; i += kSelectThreads)
+    for (int r = 0; r < p.K; ++r) {
+      const Key128 k = candidate(i / segments, i % segments, r);
+      if (k.score < low) break;
+      const int at = atomicAdd(&count, 1);
+      if (at < kList) list[at] = k;
+    }
+  __syncthreads();
+  const int n = count;
   Key128 best = {0, 0};
-  const int each = segments * p.K;
-  for (int i0 = warp * 32; i0 < p.W * each; i0 += kThreads) {
-    const int i = i0 + lane;
-    Key128 k = {0, 0};
-    if (i < p.W * each) {
-      const int w = i / each, at = i % each, row = b * p.W + w;
-      const float score = p.scores[row];
-      if (p.done && p.done[row]) {
-        // eos, and the first tokens besides it without a value
-        if (at == 0) {
-          k = {isfinite(score) ? ordered((double)score) : none, ~static_cast<unsigned>(w * p.V + p.eos)};
-        } else if (at < p.K && at < p.V) {
-          k = {none, ~static_cast<unsigned>(w * p.V + at - (at <= p.eos))};
-        }
-      } else if (isnan(lse[w])) {
-        if (at < p.K && at < p.V) k = {none, ~static_cast<unsigned>(w * p.V + at)};
-      } else {
-        const u64 c = keys[(size_t)row * each + at];
-        if (c) {
-          const double x = (double)score + ((double)unordered(static_cast<unsigned>(c >> 32)) - lse[w]);
-          k = {ordered(x), ~(static_cast<unsigned>(w * p.V) + ~static_cast<unsigned>(c))};
-        }
-      }
+  if (n > kList) {  // all of them
+    for (int i0 = warp * 32; i0 < p.W * each; i0 += kSelectThreads) {
+      const int i = i0 + lane;
+      Key128 k = {0, 0};
+      if (i < p.W * each) k = candidate(i / each, i % each / p.K, i % p.K);
+      best = merged(best, sorted(k, lane), lane);
     }
-    best = merged(best, sorted(k, lane), lane);
+  } else {
+    const int i = warp * 32 + lane;
+    if (warp * 32 < n) best = sorted(i < n ? list[i] : Key128{0, 0}, lane);
   }
-  lists[tid] = best;
-  for (int half = kWarps / 2; half > 0; half /= 2) {
+  for (int half = kSelectWarps / 2; half > 0; half /= 2) {
+    if (n <= half * 32) continue;  // (nothing in those warps)
     __syncthreads();
-    if (warp < half) {
-      best = merged(best, lists[tid + half * 32], lane);
-      lists[tid] = best;
-    }
+    if (warp >= half && warp < 2 * half) list[tid - half * 32] = best;
+    __syncthreads();
+    if (warp < half) best = merged(best, list[tid], lane);
   }
   if (tid < p.K) {
     const unsigned at = ~best.rank;
@@ -304,12 +386,26 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BeamSelect p, in
   }
 }
 
-template <typename T>
-void launch(const BeamSelect &p, int segments, Segment *seg, u64 *keys, cudaStream_t stream) {
+// Elements of a thread: few where the grid would leave SMs idle (four beams of 32000 float32 logits, both kernels:
+// 8 a thread TODO us, 32 TODO us), many where the sorting of the lanes counts (32 x 8 rows of 50257: TODO).
+int per_thread(const BeamSelect &p) {
+  const long long all = (long long)p.B * p.W * p.V, room = 2ll * kThreads * std::max(sm_count(), 1);
+  return all <= 8 * room ? 8 : all <= 16 * room ? 16 : 32;
+}
+
+template <typename T, int PER>
+void launch_per(const BeamSelect &p, int segments, Segment *seg, u64 *keys, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p.B) * p.W * segments;
   const bool wide = (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0 && p.ld * sizeof(T) % 16 == 0;
-  if (wide) segment_kernel<T, true><<<grid, kThreads, 0, stream>>>(p, segments, seg, keys);
-  else segment_kernel<T, false><<<grid, kThreads, 0, stream>>>(p, segments, seg, keys);
+  if (wide) segment_kernel<T, PER, false><<<grid, kThreads, 0, stream>>>(p, segments, seg, keys);
+  else segment_kernel<T, PER, true><<<grid, kThreads, 0, stream>>>(p, segments, seg, keys);
+}
+
+template <typename T>
+void launch(const BeamSelect &p, int per, int segments, Segment *seg, u64 *keys, cudaStream_t stream) {
+  if (per == 8) launch_per<T, 8>(p, segments, seg, keys, stream);
+  else if (per == 16) launch_per<T, 16>(p, segments, seg, keys, stream);
+  else launch_per<T, 32>(p, segments, seg, keys, stream);
 }
 
 int fail(const char *what, cudaError_t e) {
@@ -320,7 +416,7 @@ int fail(const char *what, cudaError_t e) {
 }  // namespace
 
 int launch_beam_select(const BeamSelect &p, cudaStream_t stream) {
-  const int segments = (p.V - 1) / kSegment + 1;
+  const int per = per_thread(p), segments = (p.V - 1) / (kThreads * per) + 1;
   const size_t parts = (size_t)p.B * p.W * segments;
   uint8_t *ws = nullptr;
   cudaMemPool_t pool = library_pool();
@@ -330,12 +426,20 @@ int launch_beam_select(const BeamSelect &p, cudaStream_t stream) {
   if (e != cudaSuccess) return fail("workspace allocation failed", e);
   Segment *seg = reinterpret_cast<Segment *>(ws);
   u64 *keys = reinterpret_cast<u64 *>(seg + parts);
-  if (p.f32) launch<float>(p, segments, seg, keys, stream);
-  else launch<__nv_bfloat16>(p, segments, seg, keys, stream);
+  if (p.f32) launch<float>(p, per, segments, seg, keys, stream);
+  else launch<__nv_bfloat16>(p, per, segments, seg, keys, stream);
   e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    select_kernel<<<p.B, kThreads, 0, stream>>>(p, segments, seg, keys);
-    e = cudaGetLastError();
+  if (e == cudaSuccess) {  // launched while the first one runs, and waits for its end
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.B);
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, select_kernel, p, segments, static_cast<const Segment *>(seg), static_cast<const u64 *>(keys));
   }
   const cudaError_t f = cudaFreeAsync(ws, stream);
   if (e == cudaSuccess) e = f;

@@ -24,7 +24,7 @@
 // keeps 16 bits as a high and a low bfloat16 part; with up to 8 heads the low part
 // is in the tile's other 8 rows and costs nothing.
 //
-// float32: CUDA cores, a lane a key for S and a lane four channels for O.
+// float32: CUDA cores, see F32Warp.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -55,6 +55,9 @@ template <typename T, int D, int HB> struct Shape {
   static constexpr int kBytes = kStages * kStage * kWarps + kJoin;
 };
 
+// What a part costs besides its units, in units: its queries, and the meeting of the warps at its end.
+constexpr int kPartCost = 1;
+
 // What the CTAs of a call share: rows of a part, pieces of parts in the workspace.
 struct Split {
   int blocks;      // blocks of HB heads of a key/value head
@@ -77,10 +80,10 @@ __device__ __forceinline__ Range places_of(const PagedAttn &p, int s) {
   return {p.window > 0 ? max(len - p.window, 0) : 0, len};
 }
 
-// A place in a CTA's run of units.
+// A unit in a CTA's run. All parts' units are numbered through, with kPartCost numbers left out in front of each part.
 template <int UNIT> struct Cursor {
   int s, part, unit, units, first, len;
-  long long left;  // units of the run from here on
+  long long number;
 
   __device__ __forceinline__ void enter(const PagedAttn &p) {  // the next sequence with a place
     for (; s < p.n; ++s) {
@@ -91,14 +94,15 @@ template <int UNIT> struct Cursor {
       if (units > 0) return;
     }
   }
-  __device__ __forceinline__ void next(const PagedAttn &p, int parts) {
-    --left;
+  __device__ __forceinline__ void next(const PagedAttn &p, int parts, long long end) {
+    ++number;
     if (++unit < units) return;
     unit = 0;
+    number += kPartCost;
     if (++part < parts) return;
     part = 0;
     ++s;
-    if (left > 0) enter(p);
+    if (number < end) enter(p);
   }
 };
 
@@ -127,7 +131,7 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 
 // The 16-byte chunk that chunk c of row r is stored at, so that the reads below hit all banks.
 template <bool F32, bool VALUES> __device__ __forceinline__ int stored(int r, int c) {
-  if (F32) return c ^ (r & 7);
+  if (F32) return c;
   return VALUES ? c ^ ((r >> 1 & 3) << 1) : c ^ ((r & 1) << 2);
 }
 
@@ -140,7 +144,7 @@ template <int D, int HB> struct Bf16Warp {
   float o[D / 8][4], m[R], l[R];
   float scale;
 
-  __device__ __forceinline__ void begin(const PagedAttn &p, int s, int h0, int heads, int lane, float *) {
+  __device__ __forceinline__ void begin(const PagedAttn &p, int s, int h0, int heads, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -256,113 +260,132 @@ template <int D, int HB> struct Bf16Warp {
   static __device__ __forceinline__ int quad(int g, int c) { return (c & ~15) + ((c & 15) ^ (g & 7)); }
 };
 
-// The same in float32: lane (key, part of the channels) for S, lane (four channels, part of the keys) for O.
+// The same in float32 on the CUDA cores. A lane holds 4 (8) channels of all HB queries; a row of keys is spread over
+// 32 lanes (two rows over 16 each), so that a lane has one partial product for each of 32 (16) pairs of key and
+// head, and a butterfly that halves the pairs at each step leaves one whole score to each lane: lane % HB is its head.
 template <int D, int HB> struct F32Warp {
-  static constexpr int kKeys = Shape<float, D, HB>::kKeys, kLanes = 32 / kKeys;  // lanes of a key
-  static constexpr int kQuads = D / 4, kPer = kQuads >= 32 ? kQuads / 32 : 1, kSplit = kQuads >= 32 ? 1 : 32 / kQuads;
-  static_assert(HB == 8, "");
-  float o[HB][kPer][4], m[HB], l[HB];
-  float scale;
-  const float *q;  // [HB][D] in shared memory
+  static constexpr int kKeys = Shape<float, D, HB>::kKeys;
+  static constexpr int kLanes = D / 4 < 32 ? D / 4 : 32, kRows = 32 / kLanes;  // lanes of a row, rows at a time
+  static constexpr int kPer = D / 4 / kLanes;                                  // quads of a lane
+  static constexpr int kSteps = kLanes / HB, kGroup = kSteps * kRows;          // rows of a butterfly: one after another, all
+  static constexpr int kGroups = kKeys / kGroup;
+  static_assert(kGroups >= 1 && kGroups * kGroup == kKeys, "");
+  float q[HB][kPer][4], o[HB][kPer][4], m, l, scale;
 
-  __device__ __forceinline__ void begin(const PagedAttn &p, int s, int h0, int heads, int lane, float *sq) {
-    const int tid = threadIdx.x;
+  __device__ __forceinline__ void begin(const PagedAttn &p, int s, int h0, int heads, int lane) {
     const float *src = static_cast<const float *>(p.q) + s * p.ldq + (long long)h0 * D;
-    for (int i = tid; i < HB * D; i += kThreads) sq[i] = i < heads * D ? __ldg(src + i) : 0.f;
-    __syncthreads();
-    q = sq;
 #pragma unroll
-    for (int h = 0; h < HB; ++h) {
-      m[h] = -INFINITY;
-      l[h] = 0.f;
+    for (int h = 0; h < HB; ++h)
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) o[h][i][0] = o[h][i][1] = o[h][i][2] = o[h][i][3] = 0.f;
+      for (int j = 0; j < kPer; ++j) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (h < heads) a = __ldg(reinterpret_cast<const float4 *>(src + h * D) + lane % kLanes + 32 * j);
+        q[h][j][0] = a.x; q[h][j][1] = a.y; q[h][j][2] = a.z; q[h][j][3] = a.w;
+        o[h][j][0] = o[h][j][1] = o[h][j][2] = o[h][j][3] = 0.f;
+      }
+    m = -INFINITY;
+    l = 0.f;
+    scale = p.scale * 1.44269504f;  // exponents of two
+  }
+
+  static __device__ __forceinline__ void row(uint32_t tile, int r, int lane, float (&v)[kPer][4]) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint4 u = lds(tile + (r * (D / 4) + lane % kLanes + 32 * j) * 16);
+      v[j][0] = __uint_as_float(u.x); v[j][1] = __uint_as_float(u.y);
+      v[j][2] = __uint_as_float(u.z); v[j][3] = __uint_as_float(u.w);
     }
-    scale = p.scale * 1.44269504f;
   }
 
   __device__ __forceinline__ void block(uint32_t keys, uint32_t values, uint32_t there, int lane, float *weights) {
-    constexpr int kRow = D * 4;
-    const int key = lane % kKeys, piece = lane / kKeys;
-    uint64_t x2[HB] = {};
-#pragma unroll 4
-    for (int i = 0; i < kQuads / kLanes; ++i) {
-      const int c = i * kLanes + piece;
-      const uint4 k = lds(keys + key * kRow + stored<true, false>(key, c) * 16);
-      const uint64_t k0 = f32x2::pair(__uint_as_float(k.x), __uint_as_float(k.y));
-      const uint64_t k1 = f32x2::pair(__uint_as_float(k.z), __uint_as_float(k.w));
+    const int half = lane / kLanes, step = lane % kLanes / HB, head = lane % HB;
+    float x[kGroups], top = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      float part[kLanes];
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        float v[kPer][4];
+        row(keys, g * kGroup + k * kRows + half, lane, v);
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          uint64_t t = f32x2::mul(f32x2::at(v[0]), f32x2::at(q[h][0]));
+          t = f32x2::fma(f32x2::at(v[0] + 2), f32x2::at(q[h][0] + 2), t);
+#pragma unroll
+          for (int j = 1; j < kPer; ++j) {
+            t = f32x2::fma(f32x2::at(v[j]), f32x2::at(q[h][j]), t);
+            t = f32x2::fma(f32x2::at(v[j] + 2), f32x2::at(q[h][j] + 2), t);
+          }
+          float two[2];
+          f32x2::split(t, two);
+          part[k * HB + h] = two[0] + two[1];
+        }
+      }
+#pragma unroll
+      for (int d = kLanes / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < d; ++i) {
+          const bool high = lane & d;
+          const float keep = high ? part[i + d] : part[i], give = high ? part[i] : part[i + d];
+          part[i] = keep + __shfl_xor_sync(~0u, give, d);
+        }
+      x[g] = there >> (g * kGroup + step * kRows + half) & 1 ? part[0] * scale : -INFINITY;
+      top = fmaxf(top, x[g]);
+    }
+#pragma unroll
+    for (int d = HB; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    const float now = fmaxf(m, top), base = now == -INFINITY ? 0.f : now;
+    const float keep = sm100::ex2(m - base);
+    if (__any_sync(~0u, now > m)) {
 #pragma unroll
       for (int h = 0; h < HB; ++h) {
-        const float4 a = *reinterpret_cast<const float4 *>(q + h * D + 4 * c);
-        x2[h] = f32x2::fma(k0, f32x2::pair(a.x, a.y), x2[h]);
-        x2[h] = f32x2::fma(k1, f32x2::pair(a.z, a.w), x2[h]);
+        const float f = __shfl_sync(~0u, keep, h);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) f32x2::vmul(o[h][j], o[h][j], f);
       }
     }
-    const bool on = there >> key & 1;
-    float keep[HB];
-    bool moved = false;
+    m = now;
+    l *= keep;
 #pragma unroll
-    for (int h = 0; h < HB; ++h) {
-      float pair[2];
-      f32x2::split(x2[h], pair);
-      float x = pair[0] + pair[1];
-#pragma unroll
-      for (int d = kKeys; d < 32; d *= 2) x += __shfl_xor_sync(~0u, x, d);
-      x = on ? x * scale : -INFINITY;
-      float top = x;
-#pragma unroll
-      for (int d = 1; d < kKeys; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      const float now = fmaxf(m[h], top), base = now == -INFINITY ? 0.f : now;
-      keep[h] = sm100::ex2(m[h] - base);
-      moved |= now > m[h];
-      m[h] = now;
-      const float w = sm100::ex2(x - base);
-      l[h] = fmaf(l[h], keep[h], w);
-      if (piece == 0) weights[key * HB + h] = w;
+    for (int g = 0; g < kGroups; ++g) {
+      const float w = sm100::ex2(x[g] - base);
+      l += w;
+      weights[(g * kGroup + step * kRows + half) * HB + head] = w;
     }
     __syncwarp();
-    if (moved)
+#pragma unroll 4
+    for (int k = 0; k < kKeys / kRows; ++k) {
+      const int r = k * kRows + half;
+      float w[HB], v[kPer][4];
+#pragma unroll
+      for (int h = 0; h < HB; h += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(weights + r * HB + h);
+        w[h] = a.x; w[h + 1] = a.y; w[h + 2] = a.z; w[h + 3] = a.w;
+      }
+      row(values, r, lane, v);
 #pragma unroll
       for (int h = 0; h < HB; ++h)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[h][i][e] *= keep[h];
-    const int quad = lane % (kQuads >= 32 ? 32 : kQuads), half = kQuads >= 32 ? 0 : lane / kQuads;
-#pragma unroll 4
-    for (int i = 0; i < kKeys / kSplit; ++i) {
-      const int row = i * kSplit + half;
-      const float4 w0 = *reinterpret_cast<const float4 *>(weights + row * HB);
-      const float4 w1 = *reinterpret_cast<const float4 *>(weights + row * HB + 4);
-      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const uint4 u = lds(values + row * kRow + stored<true, true>(row, quad + 32 * j) * 16);
-        const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-#pragma unroll
-        for (int h = 0; h < HB; ++h) f32x2::vfma(o[h][j], v, w[h], o[h][j]);
-      }
+        for (int j = 0; j < kPer; ++j) f32x2::vfma(o[h][j], v[j], w[h], o[h][j]);
     }
     __syncwarp();
   }
 
   __device__ __forceinline__ void end(float *sums, float2 *ml, int lane) {
-    const int quad = lane % (kQuads >= 32 ? 32 : kQuads);
 #pragma unroll
-    for (int h = 0; h < HB; ++h) {
+    for (int d = HB; d < 32; d *= 2) l += __shfl_xor_sync(~0u, l, d);
+    if (lane < HB) ml[lane] = make_float2(m, l);
 #pragma unroll
-      for (int d = 1; d < kKeys; d *= 2) l[h] += __shfl_xor_sync(~0u, l[h], d);
-      if (lane == 0) ml[h] = make_float2(m[h], l[h]);
+    for (int h = 0; h < HB; ++h)
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
+        if constexpr (kRows == 2) {
 #pragma unroll
-        for (int d = kQuads; d < 32; d *= 2)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[h][j][e] += __shfl_xor_sync(~0u, o[h][j][e], d);
-        if (lane < kQuads)
-          reinterpret_cast<float4 *>(sums + h * D)[quad + 32 * j] = make_float4(o[h][j][0], o[h][j][1], o[h][j][2], o[h][j][3]);
+          for (int e = 0; e < 4; ++e) o[h][j][e] += __shfl_xor_sync(~0u, o[h][j][e], 16);
+        }
+        if (lane < kLanes)
+          reinterpret_cast<float4 *>(sums + h * D)[lane + 32 * j] = make_float4(o[h][j][0], o[h][j][1], o[h][j][2], o[h][j][3]);
       }
-    }
   }
   static __device__ __forceinline__ int quad(int, int c) { return c; }
 };
@@ -389,18 +412,17 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
   __shared__ float2 ml[kWarps][HB];
   __shared__ uint32_t masks[kWarps][kStages];
   __shared__ long long scan[kWarps];
-  __shared__ long long start_units;
+  __shared__ long long start_number;
   __shared__ int start_seq;
   float *sums = reinterpret_cast<float *>(smem + kStages * S::kStage * kWarps);  // [kWarps][HB][D]
-  float *aside = nullptr;  // float32: the queries where the sums will be, the weights behind them
-  if constexpr (S::kF32) aside = sums + HB * D + (threadIdx.x >> 5) * kKeys * HB;
-  static_assert(!S::kF32 || kWarps * HB * D >= HB * D + kWarps * kKeys * HB, "");
+  __shared__ __align__(16) float weights[S::kF32 ? kWarps : 1][S::kF32 ? kKeys * HB : 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched before the kernel in front of it is done)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // the CTA's run of units [t0, t1)
+  // the CTA's run: the units with numbers in [t0, t1)
   Cursor<kUnit> at = {};
-  long long t0, t1, base, share = 0;
+  long long t0, t1, part_begin, share = 0;
   if (sp.whole) {
     at.s = blockIdx.x / sp.parts;
     at.part = blockIdx.x % sp.parts;
@@ -408,16 +430,17 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
     at.first = r.first;
     at.len = r.len;
     at.units = (r.len - r.first + kUnit - 1) / kUnit;
-    at.left = at.units;
-    t0 = base = 0;
+    t0 = part_begin = 0;
     t1 = at.units;
   } else {
     const int per = (p.n + kThreads - 1) / kThreads, a = min(tid * per, p.n), b = min(a + per, p.n);
-    long long mine = 0;
-    for (int s = a; s < b; ++s) {
+    auto numbers = [&](int s) {
       const Range r = places_of(p, s);
-      mine += (r.len - r.first + kUnit - 1) / kUnit;
-    }
+      const int units = (r.len - r.first + kUnit - 1) / kUnit;
+      return units > 0 ? (long long)(units + kPartCost) * sp.parts : 0ll;
+    };
+    long long mine = 0;
+    for (int s = a; s < b; ++s) mine += numbers(s);
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -433,22 +456,17 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
       if (w < warp) upto += scan[w];
       total += scan[w];
     }
-    total *= sp.parts;
     share = max((total + gridDim.x - 1) / gridDim.x, (long long)sp.least);
     t0 = blockIdx.x * share;
     t1 = min(t0 + share, total);
-    // sequences without a place, by whoever comes to them first
-    if (t0 >= t1) {
-      at.left = 0;
-    } else {
-      long long before = (upto - mine) * sp.parts;
-      if (before <= t0 && t0 < upto * sp.parts) {
+    if (t0 < t1) {
+      long long before = upto - mine;
+      if (before <= t0 && t0 < upto) {
         for (int s = a; s < b; ++s) {
-          const Range r = places_of(p, s);
-          const long long u = (long long)((r.len - r.first + kUnit - 1) / kUnit) * sp.parts;
+          const long long u = numbers(s);
           if (t0 < before + u) {
             start_seq = s;
-            start_units = before;
+            start_number = before;
             break;
           }
           before += u;
@@ -457,10 +475,12 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
       __syncthreads();
       at.s = start_seq;
       at.enter(p);
-      base = start_units;
-      at.part = static_cast<int>((t0 - base) / at.units);
-      at.unit = static_cast<int>((t0 - base) % at.units);
-      at.left = t1 - t0;
+      const int each = at.units + kPartCost;
+      const long long in = t0 - start_number;
+      at.part = static_cast<int>(in / each);
+      at.unit = max(static_cast<int>(in % each) - kPartCost, 0);
+      part_begin = start_number + (long long)at.part * each + kPartCost;
+      at.number = part_begin + at.unit;
     }
     // rows of sequences without a place
     for (int s = blockIdx.x; s < p.n; s += gridDim.x) {
@@ -469,9 +489,10 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
       for (int i = tid; i < p.H * (D / 4); i += kThreads)
         finish<T>(p, s, i / (D / 4), D, i % (D / 4), 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
     }
-    if (at.left == 0) return;
+    if (t0 >= t1 || at.number >= t1) return;
   }
 
+  const int share_heads = p.H / p.Hk;
   // the ring
   const uint32_t ring = sm100::smem_u32(smem) + warp * kStages * S::kStage;
   Cursor<kUnit> to = at;  // where the copies are
@@ -497,45 +518,47 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
         copy16(values + (row * kChunks + stored<S::kF32, true>(row, chunk)) * 16, static_cast<const T *>(p.v_cache) + e, o >= 0);
       }
     }
-    to.next(p, sp.parts);
+    // the queries of a part into L1 while its first keys are on their way
+    if (warp == 0 && (to.unit == 0 || to.number == at.number)) {
+      const int h0 = to.part / sp.blocks * share_heads + to.part % sp.blocks * HB;
+      const char *q = reinterpret_cast<const char *>(static_cast<const T *>(p.q) + to.s * p.ldq + (long long)h0 * D);
+      for (int i = lane * 128; i < min(HB, share_heads - to.part % sp.blocks * HB) * D * (int)sizeof(T); i += 32 * 128)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+    }
+    to.next(p, sp.parts, t1);
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    if (to.left > 0) load(i);
+    if (to.number < t1) load(i);
     commit();
   }
 
   using Warp = std::conditional_t<S::kF32, F32Warp<D, HB>, Bf16Warp<D, HB>>;
   Warp w;
-  const int share_heads = p.H / p.Hk;
   int stage = 0;
   bool fresh = true;
-  long long t = t0;  // units in front of this one
-  long long part_begin = sp.whole ? 0 : base + (long long)at.part * at.units;
-  if (at.left == 0) w.begin(p, at.s, 0, 0, lane, sums);  // a whole part without a place
+  if (at.units == 0) w.begin(p, at.s, 0, 0, lane);  // a whole part without a place
   while (true) {
     const int h0 = at.part / sp.blocks * share_heads + at.part % sp.blocks * HB;
     const int heads = min(HB, share_heads - at.part % sp.blocks * HB);
     bool last = true;
-    if (at.left > 0) {
-      if (fresh) w.begin(p, at.s, h0, heads, lane, sums);
+    if (at.units > 0) {
+      if (fresh) w.begin(p, at.s, h0, heads, lane);
       wait_all_but<kStages - 2>();
       __syncwarp();
       const int free = stage == 0 ? kStages - 1 : stage - 1;
       const uint32_t there = masks[warp][stage];
-      if (to.left > 0) load(free);
+      if (to.number < t1) load(free);
       commit();
       if (there) {
         const uint32_t keys = ring + stage * S::kStage;
-        w.block(keys, keys + S::kTile, there, lane, aside);
+        w.block(keys, keys + S::kTile, there, lane, weights[S::kF32 ? warp : 0]);
       }
       stage = stage == kStages - 1 ? 0 : stage + 1;
-      ++t;
-      last = at.unit + 1 == at.units || at.left == 1;
+      last = at.unit + 1 == at.units || at.number + 1 == t1;
     }
     fresh = last;
     if (last) {
-      if (S::kF32) __syncthreads();  // the queries are where the sums go
       w.end(sums + warp * HB * D, ml[warp], lane);
       __syncthreads();
       const long long part_end = part_begin + at.units;
@@ -563,11 +586,12 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
         }
       }
       if (begun && !done && tid == 0) sp.joins[blockIdx.x] = make_int4(at.s, at.part, static_cast<int>((part_end - 1) / share), 0);
-      if (at.left <= 1) return;
-      part_begin = part_end;
-      __syncthreads();
+      part_begin = part_end + kPartCost;
     }
-    at.next(p, sp.parts);
+    if (at.units == 0) return;
+    at.next(p, sp.parts, t1);
+    if (at.number >= t1) return;
+    if (last) __syncthreads();
   }
 }
 
@@ -630,6 +654,22 @@ int fail(const char *what, cudaError_t e) {
 // Units below which a part is not split.
 constexpr int kLeast = 2;
 
+// Launched programmatically: what stands in front of it in the stream may still be running.
+template <typename... Args>
+cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, const Args &...args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename T, int D, int HB>
 int launch(const PagedAttn &p, cudaStream_t stream) {
   using S = Shape<T, D, HB>;
@@ -654,11 +694,10 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
   sp.whole = longest <= (long long)kLeast * S::kUnit;
   const FastDiv by(p.at.page_size);
   if (sp.whole) {
-    kernel<<<static_cast<unsigned>(parts), kThreads, S::kBytes, stream>>>(p, sp, by);
-    e = cudaGetLastError();
+    e = launch_early(kernel, dim3(static_cast<unsigned>(parts)), kThreads, S::kBytes, stream, p, sp, by);
     return e == cudaSuccess ? LA_OK : fail("launch failed", e);
   }
-  const long long units = (longest + S::kUnit - 1) / S::kUnit * parts;
+  const long long units = ((longest + S::kUnit - 1) / S::kUnit + kPartCost) * parts;
   const int ctas = static_cast<int>(std::min(slots, (units + kLeast - 1) / kLeast));
   const size_t sums = (size_t)2 * ctas * HB * D * 4, ml = (size_t)2 * ctas * HB * sizeof(float2);
   cudaMemPool_t pool = library_pool();
@@ -669,27 +708,16 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
   sp.sums = reinterpret_cast<float *>(ws);
   sp.ml = reinterpret_cast<float2 *>(ws + sums);
   sp.joins = reinterpret_cast<int4 *>(ws + sums + ml);
-  kernel<<<ctas, kThreads, S::kBytes, stream>>>(p, sp, by);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, parts <= 64 ? HB : 1);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join_kernel<T, D, HB>, p, sp);
-  }
+  e = launch_early(kernel, dim3(ctas), kThreads, S::kBytes, stream, p, sp, by);
+  if (e == cudaSuccess)
+    e = launch_early(join_kernel<T, D, HB>, dim3(ctas, parts <= 64 ? HB : 1), kJoinThreads, 0, stream, p, sp);
   const cudaError_t f = cudaFreeAsync(ws, stream);
   if (e == cudaSuccess) e = f;
   return e == cudaSuccess ? LA_OK : fail("launch failed", e);
 }
 
 template <int D> int launch_d(const PagedAttn &p, cudaStream_t stream) {
-  if (p.f32) return launch<float, D, 8>(p, stream);
+  if (p.f32) return p.H / p.Hk <= 4 ? launch<float, D, 4>(p, stream) : launch<float, D, 8>(p, stream);
   return p.H / p.Hk <= 8 ? launch<__nv_bfloat16, D, 8>(p, stream) : launch<__nv_bfloat16, D, 16>(p, stream);
 }
 
