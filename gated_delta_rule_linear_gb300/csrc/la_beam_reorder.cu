@@ -3,11 +3,9 @@
 //
 // Bound by HBM traffic: a row is read once if it is the parent of another one,
 // and written if its parent is another one; rows that stay are not touched.
-// A thread takes a column of all W rows: it reads the parents' values into
-// registers before it writes any, so no row needs a second place. Registers are
-// indexed by the parent, an unrolled loop, and a parent's value goes to its
-// children's rows one after the other (a bit mask), so that nothing is indexed
-// by what is only known at run time.
+// A thread takes a column of all W rows: it reads what each row becomes into
+// registers before it writes any, so no row needs a second place. A parent of
+// several is asked for several times, and comes from memory once.
 #include <algorithm>
 
 #include "la_serve_internal.h"
@@ -17,123 +15,124 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// What a request's rows do: kids[p] are the rows that become row p, source the rows with such kids.
+// Which rows of a request move, where they start and where their parents do.
 struct Moves {
-  unsigned kids[kMaxBeams];
-  char *row[kMaxBeams];
-  unsigned source;
+  longlong2 at[kMaxBeams];  // byte of the parent's row, byte of the row
+  unsigned rows;
 };
 
-// Filled by the block's first warp; row: this lane's row, or null if it has none.
-__device__ __forceinline__ void read_moves(Moves &m, const int *parent, int W, char *row) {
+// Filled by the block's first warp: lane w's parent is `from`, its row starts at byte `at` (-1: it has none).
+__device__ __forceinline__ void set_moves(Moves &m, int W, int from, long long at) {
   const int w = threadIdx.x;
   if (w < 32) {
-    const int from = w < W && row ? __ldg(parent + w) : -1;
-    const unsigned there = __ballot_sync(~0u, row != nullptr);
-    const bool moves = from >= 0 && from < W && from != w && ((there >> from) & 1);
-    unsigned source = 0;
-    for (int p = 0; p < W; ++p) {
-      const unsigned kids = __ballot_sync(~0u, moves && from == p);
-      if (w == p) m.kids[p] = kids;
-      if (kids) source |= 1u << p;
-    }
-    m.row[w] = row;
-    if (w == 0) m.source = source;
+    const unsigned there = __ballot_sync(~0u, w < W && at >= 0);
+    const bool moves = (there >> w & 1) && from >= 0 && from < W && from != w && (there >> from & 1);
+    const long long theirs = __shfl_sync(~0u, at, from & 31);
+    m.at[w] = make_longlong2(theirs, at);
+    const unsigned rows = __ballot_sync(~0u, moves);
+    if (w == 0) m.rows = rows;
   }
   __syncthreads();
 }
 
-// Columns first, first + stride, .. below n of type U.
-template <typename U, int WMAX>
-__device__ __forceinline__ void move_columns(const Moves &m, long long first, long long n, long long stride) {
-  const unsigned source = m.source;
-  if (!source) return;
-  for (long long c = first; c < n; c += stride) {
+// The rows of `pools` pools, pool(l) their bases, each of n columns of type U; this thread is number `thread` of
+// `threads`.
+template <typename U, int WMAX, typename Pool>
+__device__ __forceinline__ void move_columns(const Moves &m, Pool pool, unsigned pools, unsigned n, unsigned thread,
+                                             unsigned threads) {
+  const unsigned rows = m.rows;
+  unsigned l = 0;
+  for (unsigned long long c = thread;; c += threads) {
+    while (c >= n) {
+      c -= n;
+      if (++l >= pools) return;
+    }
+    asm volatile("" ::: "memory");  // the rows' places stay in shared memory: held, they would take the registers
+    char *at = pool(l) + c * sizeof(U);
     U val[WMAX];
 #pragma unroll
-    for (int p = 0; p < WMAX; ++p)
-      if (source >> p & 1) val[p] = reinterpret_cast<const U *>(m.row[p])[c];
+    for (int i = 0; i < WMAX; ++i)
+      if (rows >> i & 1) val[i] = *reinterpret_cast<const U *>(at + m.at[i].x);
 #pragma unroll
-    for (int p = 0; p < WMAX; ++p)
-      if (source >> p & 1)
-        for (unsigned k = m.kids[p]; k; k &= k - 1) reinterpret_cast<U *>(m.row[__ffs(k) - 1])[c] = val[p];
+    for (int i = 0; i < WMAX; ++i)
+      if (rows >> i & 1) *reinterpret_cast<U *>(at + m.at[i].y) = val[i];
   }
 }
 
+// Block (request, chunk of the columns): all layers.
 template <typename U, int WMAX>
 __global__ void __launch_bounds__(kThreads) states_kernel(const BeamStates p, int chunks) {
   __shared__ Moves m;
-  const unsigned i = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int l = i % p.layers, b = i / p.layers, w = threadIdx.x;
-  char *row = nullptr;
+  const int chunk = blockIdx.x % chunks, b = blockIdx.x / chunks, w = threadIdx.x;
+  wait_for_stream();
+  int from = -1;
+  long long at = -1;
   if (w < p.W) {
-    const int at = b * p.W + w, slot = p.slots ? __ldg(p.slots + at) : at;
-    if (slot >= 0 && slot < p.n_slots) row = static_cast<char *>(p.pool) + l * p.ld_layer + slot * p.ld_row;
+    const int i = b * p.W + w, slot = p.slots ? p.slots[i] : i;
+    from = p.parent[i];
+    if (slot >= 0 && slot < p.n_slots) at = slot * p.ld_row;
   }
-  read_moves(m, p.parent + (size_t)b * p.W, p.W, row);
-  move_columns<U, WMAX>(m, (long long)chunk * kThreads + threadIdx.x, p.row_bytes / (long long)sizeof(U),
-                        (long long)chunks * kThreads);
+  set_moves(m, p.W, from, at);
+  if (!m.rows) return;
+  move_columns<U, WMAX>(m, [&](unsigned l) { return static_cast<char *>(p.pool) + l * p.ld_layer; }, p.layers,
+                        static_cast<unsigned>(p.row_bytes / sizeof(U)), chunk * kThreads + w, chunks * kThreads);
 }
 
+// Block (request, chunk): chunk 0 the table, the others the open pages of all layers' keys and values.
 template <typename U, int WMAX>
 __global__ void __launch_bounds__(kThreads) cache_kernel(const BeamCache p, const FastDiv by_page, int chunks) {
   __shared__ Moves m;
-  const unsigned jobs = 2 * p.layers * chunks + 1, b = blockIdx.x / jobs, w = threadIdx.x;
-  unsigned job = blockIdx.x % jobs;
-  const int len = min((long long)max(__ldg(p.lens + (size_t)b * p.W), 0), (long long)p.max_pages * p.page_size);
+  const int b = blockIdx.x / (chunks + 1), chunk = static_cast<int>(blockIdx.x % (chunks + 1)) - 1, w = threadIdx.x;
+  wait_for_stream();
+  int from = -1;
+  if (w < p.W) from = p.parent[b * p.W + w];
+  const int len = min((long long)max(p.lens[(size_t)b * p.W], 0), (long long)p.max_pages * p.page_size);
   uint32_t open, fill;
   by_page.split(len, open, fill);
-  int *entries = p.table + ((size_t)b * p.W + w) * p.ld_table;
-  const int *parent = p.parent + (size_t)b * p.W;
-  if (job == 0) {  // the table
-    read_moves(m, parent, p.W, (int)w < p.W ? reinterpret_cast<char *>(entries) : nullptr);
-    move_columns<int, WMAX>(m, threadIdx.x, open, kThreads);
+  int *table = p.table + (long long)b * p.W * p.ld_table;
+  if (chunk < 0) {
+    set_moves(m, p.W, from, w < p.W ? w * p.ld_table * 4 : -1);
+    if (m.rows && open) move_columns<int, WMAX>(m, [&](unsigned) { return reinterpret_cast<char *>(table); }, 1, open, w, kThreads);
     return;
   }
   if (fill == 0) return;  // (open < max_pages otherwise)
-  --job;
-  const int chunk = job % chunks, l = job / chunks % p.layers, which = job / chunks / p.layers;
-  char *row = nullptr;
-  if ((int)w < p.W) {
-    const int page = __ldg(entries + open);  // behind the entries that are moved
-    if (page >= 0 && page < p.n_pages) row = static_cast<char *>(which ? p.v_cache : p.k_cache) + l * p.ld_layer + page * p.ld_page;
+  long long at = -1;
+  if (w < p.W) {
+    const int page = table[w * p.ld_table + open];  // behind the entries that chunk 0 moves
+    if (page >= 0 && page < p.n_pages) at = page * p.ld_page;
   }
-  read_moves(m, parent, p.W, row);
-  move_columns<U, WMAX>(m, (long long)chunk * kThreads + threadIdx.x, fill * p.token_bytes / (long long)sizeof(U),
-                        (long long)chunks * kThreads);
+  set_moves(m, p.W, from, at);
+  if (!m.rows) return;
+  move_columns<U, WMAX>(m, [&](unsigned l) {
+    return static_cast<char *>(l & 1 ? p.v_cache : p.k_cache) + (l >> 1) * p.ld_layer;
+  }, 2 * p.layers, static_cast<unsigned>(fill * p.token_bytes / sizeof(U)), chunk * kThreads + w, chunks * kThreads);
 }
 
-// Blocks of a row's columns: one column a thread, up to `most` blocks in all.
-int chunks_of(long long columns, long long rows, long long most) {
-  const long long c = (columns + kThreads - 1) / kThreads;
-  return static_cast<int>(std::max(1ll, std::min(c, most / std::max(rows, 1ll))));
+// Blocks of a request: a column a thread, up to those that are on the SMs together.
+int chunks_of(long long columns, int requests) {
+  const long long c = (columns + kThreads - 1) / kThreads, most = 8ll * std::max(sm_count(), 1) / requests;
+  return static_cast<int>(std::max(1ll, std::min(c, most)));
 }
-
-long long most_blocks() { return 64ll * std::max(sm_count(), 1); }
 
 template <typename U>
 cudaError_t states(const BeamStates &p, cudaStream_t stream) {
-  const long long rows = (long long)p.B * p.layers;
-  const int chunks = chunks_of(p.row_bytes / (long long)sizeof(U), rows, most_blocks());
-  const unsigned grid = static_cast<unsigned>(rows * chunks);  // the caller keeps B * layers below 2^27
-  if (p.W <= 4) states_kernel<U, 4><<<grid, kThreads, 0, stream>>>(p, chunks);
-  else if (p.W <= 8) states_kernel<U, 8><<<grid, kThreads, 0, stream>>>(p, chunks);
-  else if (p.W <= 16) states_kernel<U, 16><<<grid, kThreads, 0, stream>>>(p, chunks);
-  else states_kernel<U, 32><<<grid, kThreads, 0, stream>>>(p, chunks);
-  return cudaGetLastError();
+  const int chunks = chunks_of(p.layers * (p.row_bytes / (long long)sizeof(U)), p.B);
+  const unsigned grid = static_cast<unsigned>(p.B) * chunks;  // (B of one chunk, or a few for each SM)
+  if (p.W <= 4) return launch_early(states_kernel<U, 4>, dim3(grid), kThreads, 0, stream, p, chunks);
+  if (p.W <= 8) return launch_early(states_kernel<U, 8>, dim3(grid), kThreads, 0, stream, p, chunks);
+  if (p.W <= 16) return launch_early(states_kernel<U, 16>, dim3(grid), kThreads, 0, stream, p, chunks);
+  return launch_early(states_kernel<U, 32>, dim3(grid), kThreads, 0, stream, p, chunks);
 }
 
 template <typename U>
 cudaError_t cache(const BeamCache &p, cudaStream_t stream) {
-  const long long rows = 2ll * p.B * p.layers;
-  const int chunks = chunks_of(p.page_size * p.token_bytes / (long long)sizeof(U), rows, most_blocks());
-  const unsigned grid = static_cast<unsigned>(rows * chunks + p.B);
+  const int chunks = chunks_of(2 * p.layers * (p.page_size * p.token_bytes / (long long)sizeof(U)), p.B);
+  const unsigned grid = static_cast<unsigned>(p.B) * (chunks + 1);
   const FastDiv by(p.page_size);
-  if (p.W <= 4) cache_kernel<U, 4><<<grid, kThreads, 0, stream>>>(p, by, chunks);
-  else if (p.W <= 8) cache_kernel<U, 8><<<grid, kThreads, 0, stream>>>(p, by, chunks);
-  else if (p.W <= 16) cache_kernel<U, 16><<<grid, kThreads, 0, stream>>>(p, by, chunks);
-  else cache_kernel<U, 32><<<grid, kThreads, 0, stream>>>(p, by, chunks);
-  return cudaGetLastError();
+  if (p.W <= 4) return launch_early(cache_kernel<U, 4>, dim3(grid), kThreads, 0, stream, p, by, chunks);
+  if (p.W <= 8) return launch_early(cache_kernel<U, 8>, dim3(grid), kThreads, 0, stream, p, by, chunks);
+  if (p.W <= 16) return launch_early(cache_kernel<U, 16>, dim3(grid), kThreads, 0, stream, p, by, chunks);
+  return launch_early(cache_kernel<U, 32>, dim3(grid), kThreads, 0, stream, p, by, chunks);
 }
 
 // Whether an address and its strides allow 16 bytes at a time.

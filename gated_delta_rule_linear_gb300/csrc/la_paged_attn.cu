@@ -76,7 +76,7 @@ struct Range {
 };
 __device__ __forceinline__ Range places_of(const PagedAttn &p, int s) {
   const long long most = min((long long)p.at.max_pages * p.at.page_size, (long long)kMostPlaces);
-  const int len = static_cast<int>(min((long long)max(__ldg(p.at.lens + s), 0), most));
+  const int len = static_cast<int>(min((long long)max(p.at.lens[s], 0), most));
   return {p.window > 0 ? max(len - p.window, 0) : 0, len};
 }
 
@@ -152,7 +152,7 @@ template <int D, int HB> struct Bf16Warp {
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (g + 8 * r < heads) u = __ldg(reinterpret_cast<const uint4 *>(row) + 4 * k + t);
+        if (g + 8 * r < heads) u = reinterpret_cast<const uint4 *>(row)[4 * k + t];
         q[r][k][0] = u.x; q[r][k][1] = u.y; q[r][k][2] = u.z; q[r][k][3] = u.w;
       }
       m[r] = -INFINITY;
@@ -279,7 +279,7 @@ template <int D, int HB> struct F32Warp {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h < heads) a = __ldg(reinterpret_cast<const float4 *>(src + h * D) + lane % kLanes + 32 * j);
+        if (h < heads) a = reinterpret_cast<const float4 *>(src + h * D)[lane % kLanes + 32 * j];
         q[h][j][0] = a.x; q[h][j][1] = a.y; q[h][j][2] = a.z; q[h][j][3] = a.w;
         o[h][j][0] = o[h][j][1] = o[h][j][2] = o[h][j][3] = 0.f;
       }
@@ -417,8 +417,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
   float *sums = reinterpret_cast<float *>(smem + kStages * S::kStage * kWarps);  // [kWarps][HB][D]
   __shared__ __align__(16) float weights[S::kF32 ? kWarps : 1][S::kF32 ? kKeys * HB : 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched before the kernel in front of it is done)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_stream();
 
   // the CTA's run: the units with numbers in [t0, t1)
   Cursor<kUnit> at = {};
@@ -502,7 +501,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
     if (i < to.len) {
       uint32_t pg, r;
       by_page.split(i, pg, r);
-      const int page = __ldg(p.at.table + to.s * p.at.ld_table + pg);
+      const int page = p.at.table[to.s * p.at.ld_table + pg];
       if (page >= 0 && page < p.at.n_pages) off = page * p.at.ld_page + ((long long)r * p.Hk + to.part / sp.blocks) * D;
     }
     const uint32_t there = __ballot_sync(~0u, off >= 0) & ((1u << kKeys) - 1);
@@ -601,7 +600,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn p, c
   constexpr int kQuads = D / 4;
   __shared__ float4 sums[kJoinThreads];
   __shared__ float2 ml[kJoinThreads];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   const int4 join = sp.joins[blockIdx.x];
   if (join.x < 0) return;
   const int each = HB / gridDim.y, share_heads = p.H / p.Hk, block = join.y % sp.blocks;
@@ -653,22 +652,6 @@ int fail(const char *what, cudaError_t e) {
 
 // Units below which a part is not split.
 constexpr int kLeast = 2;
-
-// Launched programmatically: what stands in front of it in the stream may still be running.
-template <typename... Args>
-cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, const Args &...args) {
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 template <typename T, int D, int HB>
 int launch(const PagedAttn &p, cudaStream_t stream) {

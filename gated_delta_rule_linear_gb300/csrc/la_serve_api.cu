@@ -108,7 +108,7 @@ int la_beam_select(const void *logits, const float *scores, const unsigned char 
   if (W < 1 || W > kMaxBeams) return unsupported(fn, "W must be 1..32", W);
   if (K < 1 || K > kMaxBeams) return unsupported(fn, "K must be 1..32", K);
   if ((long long)W * V > INT_MAX || K > W * V) return bad(fn, "K must be <= W*V, W*V below 2^31");
-  if (((long long)V / 2048 + 1) * W * B > INT_MAX / 2) return bad(fn, "B*W*V too large");
+  if (((long long)V / 128 + 1) * W * B > INT_MAX / 2) return bad(fn, "B*W*V too large");
   if (ld < V) return bad(fn, "ld must be >= V");
   if (done && (eos < 0 || eos >= V)) return bad(fn, "eos must be in 0..V-1");
   if (B == 0) return LA_OK;
@@ -133,6 +133,7 @@ int la_beam_states(void *pool, const int *slots, const int *parent, int B, int W
   if ((long long)B * layers > (1 << 27) || (long long)B * W > INT_MAX) return bad(fn, "B*layers too large");
   if ((row_bytes | ld_row | ld_layer) & 3) return bad(fn, "row_bytes, ld_row and ld_layer must be multiples of 4");
   if (ld_row < row_bytes || ld_layer < 0) return bad(fn, "ld_row must cover a row");
+  if (row_bytes >> 34) return bad(fn, "row_bytes must be below 2^34");
   if (B == 0 || layers == 0 || row_bytes == 0 || n_slots == 0) return LA_OK;
   if (!pool || !parent) return bad(fn, "pool and parent are required");
   if (!at(pool, 4) || !at(parent, 4) || !at(slots, 4)) return bad(fn, "pointers must be 4-byte aligned");
@@ -155,6 +156,7 @@ int la_beam_cache(void *k_cache, void *v_cache, int *table, const int *lens, con
   if ((long long)B * (layers + 1) > (1 << 26) || (long long)B * W > INT_MAX) return bad(fn, "B*layers too large");
   if ((token_bytes | ld_page | ld_layer) & 3) return bad(fn, "token_bytes, ld_page and ld_layer must be multiples of 4");
   if (ld_layer < 0) return bad(fn, "ld_layer must be >= 0");
+  if (page_size * token_bytes >> 34) return bad(fn, "a page must be below 2^34 bytes");
   if (B == 0 || max_pages == 0) return LA_OK;
   if (!table || !lens || !parent) return bad(fn, "table, lens and parent are required");
   if (layers > 0 && n_pages > 0 && (!k_cache || !v_cache)) return bad(fn, "k_cache and v_cache are required");

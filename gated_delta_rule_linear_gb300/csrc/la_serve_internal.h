@@ -7,6 +7,31 @@
 
 namespace la {
 
+// The kernels of a decoding step are short and follow one another: each is launched
+// programmatically, so that it may be set up while what stands in front of it in
+// the stream still runs, and waits for that (wait_for_stream) before it touches
+// memory, by loads that are not of the read-only kind (a kernel in front may be
+// writing in this one's lifetime). Kernels behind it are let through at the same point.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const Args &...args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+__device__ __forceinline__ void wait_for_stream() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Where the tokens of a paged cache are.
 struct PagedCache {
   const int *table, *lens;

@@ -350,6 +350,48 @@ def test_select_rising_and_falling_rows():
         check_select(logits, torch.tensor([[-1.0, -2.1, -3.2, -4.3]]), 32, gap=1e-6)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_select_masks_of_the_lowest_value(dtype):
+    """Tokens masked by the type's lowest value instead of -infinity; rows of nothing else; the highest value."""
+    logits, scores = select_case(4, 2, 3000, 6, dtype, 5)
+    low = torch.finfo(dtype).min
+    logits[0, :, 10:2900] = low
+    logits[1, 0] = low
+    logits[2] = low
+    logits[2, 1, 7] = 0.0
+    logits[3, 1, 100:103] = torch.finfo(dtype).max
+    check_select(logits, scores, 6)
+
+
+def test_select_rows_at_every_alignment():
+    """Vocabularies and strides that put rows at any offset from 16 bytes; rows that are alike tie."""
+    for dtype in (BF, F32):
+        for V, ld in ((4099, 4099), (9001, 9003), (257, 259), (8, 9), (70005, 70005)):
+            gen = torch.Generator().manual_seed(ld)
+            store = (3 * torch.randn(6, ld, generator=gen)).to(dtype)
+            store[3, :V] = store[1, :V]
+            for first in (0, 1, 3):
+                flat = torch.cat([torch.zeros(first, dtype=dtype), store.flatten()]).cuda()
+                view = flat[first:].view(6, ld)[:, :V].unflatten(0, (2, 3))
+                scores = torch.tensor([[0.0, -1.0, -2.0], [-1.0, -2.5, -1.0]])
+                scores[1, 0] = scores[0, 1]
+                K = min(8, V)
+                best, parent, token = la.beam_select(view, scores.cuda(), K)
+                c = ref.candidates(store[:, :V].unflatten(0, (2, 3)), scores)
+                assert ref.nearest(c, K) > 1e-5
+                want = ref.selection(c, K)
+                assert torch.equal(parent.cpu(), want[1]) and torch.equal(token.cpu(), want[2])
+                hold(best, want[0], ref.select_bound(want[0]), "scores")
+        # a row and its copy at another alignment, in one request
+        gen = torch.Generator().manual_seed(1)
+        for V in (5001, 33333):
+            row = (3 * torch.randn(V, generator=gen)).to(dtype)
+            best, parent, token = la.beam_select(row.expand(1, 7, V).contiguous().cuda(), torch.zeros(1, 7).cuda(), 21)
+            order = torch.sort(-row.double(), stable=True)[1][:4]
+            assert token.cpu()[0].tolist() == [int(order[i // 7]) for i in range(21)]
+            assert parent.cpu()[0].tolist() == [i % 7 for i in range(21)]
+
+
 def test_select_strides_streams_and_graphs():
     gen = torch.Generator().manual_seed(4)
     padded = (3 * torch.randn(2, 4, 5008, generator=gen)).to(BF).cuda()

@@ -180,6 +180,7 @@ BAD = {
         (dict(ld_layer=642), INVALID, "multiples of 4"),
         (dict(ld_row=60), INVALID, "ld_row must cover"),
         (dict(ld_layer=-640), INVALID, "ld_row must cover"),
+        (dict(row_bytes=2 ** 34, ld_row=2 ** 34), INVALID, "below 2^34"),
         (dict(pool=None), INVALID, "are required"),
         (dict(parent=None), INVALID, "are required"),
         (dict(pool=A + 2), INVALID, "4-byte aligned"),
@@ -201,6 +202,7 @@ BAD = {
         (dict(ld_page=4098), INVALID, "multiples of 4"),
         (dict(ld_layer=40962), INVALID, "multiples of 4"),
         (dict(ld_layer=-4), INVALID, "ld_layer must be"),
+        (dict(token_bytes=2 ** 32, ld_page=2 ** 40), INVALID, "below 2^34"),
         (dict(table=None), INVALID, "are required"),
         (dict(lens=None), INVALID, "are required"),
         (dict(parent=None), INVALID, "are required"),
