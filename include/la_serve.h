@@ -114,8 +114,7 @@ int la_paged_attn(const void *q, const void *k_cache, const void *v_cache, void 
  * are taken, in that order, where there are fewer than K others. The log of the
  * sum is good to about 1e-7, candidates are compared in 64 bits: two
  * beams' candidates closer than that may change places.
- * Workspace from the library's pool: 8*K + 16 bytes for each 128 logits at most,
- * and some 20 parts of a SM where the rows are long.
+ * Workspace from the library's pool: 8*K + 16 bytes for each 256 logits at most.
  */
 int la_beam_select(const void *logits, const float *scores, const unsigned char *done, float *scores_out, int *parent,
                    int *token, int B, int W, int V, int K, long long ld, int eos, int flags, la_stream_t stream);
