@@ -28,7 +28,9 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <climits>
 #include <atomic>
+#include <type_traits>
 
 #include "la_f32x2.cuh"
 #include "la_serve_internal.h"
@@ -43,15 +45,18 @@ constexpr int kJoinThreads = 512;
 // Sizes of a kernel with d = D and HB rows.
 template <typename T, int D, int HB> struct Shape {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kKeys = kF32 && D == 256 ? 8 : 16;       // places of a warp's block
-  static constexpr int kUnit = kKeys * kWarps;
-  static constexpr int kChunks = D * static_cast<int>(sizeof(T)) / 16;  // 16-byte chunks of a row
-  static constexpr int kTile = kKeys * kChunks * 16;            // bytes of a block's keys
+  static constexpr int kKeys = !kF32 || D == 64 ? 16 : D == 256 && HB == 8 ? 4 : 8;  // places of a warp's block
+  static constexpr int kChunks = D * static_cast<int>(sizeof(T)) / 16;    // 16-byte chunks of a row
+  static constexpr int kTile = kKeys * kChunks * 16;                      // bytes of a block's keys
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kJoin = kWarps * HB * D * 4;             // the warps' sums, where they meet
-  // two CTAs on a SM where three stages allow it, else one with what fits
-  static constexpr bool kTwo = 3 * kStage * kWarps + kJoin <= 112 * 1024;
-  static constexpr int kStages = std::min(((kTwo ? 112 : 224) * 1024 - kJoin) / (kStage * kWarps), 6);
+  // CTAs on a SM, of two stages each: 64 KB on their way are what the memory's latency asks for, and more of these copies
+  // stand in the way of the warps' own reads of shared memory. (32 x 16384 places, 16/8 heads of 128: 2 CTAs of two
+  // stages 314 us, 6.8 TB/s; of three stages 365, 3 CTAs of two 395. 64 x 8192, 16/8 heads of 64: 4 CTAs of two stages
+  // 170 us, 3 181; 2 of three 242.)
+  static constexpr int kCtas = D == 64 ? kF32 ? 3 : 4 : D == 128 || (kF32 && HB == 8) ? 2 : 1;  // on a SM
+  static constexpr int kStages = 2;
+  static constexpr int kUnit = kKeys * kWarps;
+  static constexpr int kJoin = kWarps / 2 * HB * D * 4;         // half of the warps' sums, where they meet
   static constexpr int kBytes = kStages * kStage * kWarps + kJoin;
 };
 
@@ -62,17 +67,22 @@ constexpr int kPartCost = 1;
 struct Split {
   int blocks;      // blocks of HB heads of a key/value head
   int parts;       // parts of a sequence: Hk * blocks
+  int lines;       // 128-byte lines of a table row that are asked for ahead
   int whole;       // a CTA takes one whole part: no pieces, no workspace
   int least;       // least units of a run
   float *sums;     // [2 * CTAs][HB][D]
   float2 *ml;      // [2 * CTAs][HB]: maximum (of log2) and sum
-  int4 *joins;     // [CTAs]: sequence, part, last CTA with a piece of it; sequence -1: none
+  int4 *joins;     // sequence, part, first and last CTA with a piece of it; sequence -1: none
+  int by_part;     // joins has an entry for each part of each sequence, else for the first CTA of each
 };
 
 constexpr int kMostPlaces = 0x7fff0000;  // a unit behind the last place is still an int
 
 struct Range {
   int first, len;  // places of a sequence: first .. len - 1
+  __device__ __forceinline__ int units(int keys, int unit) const {  // from the block of `keys` that holds the first
+    return len > first ? (len - first / keys * keys + unit - 1) / unit : 0;
+  }
 };
 __device__ __forceinline__ Range places_of(const PagedAttn &p, int s) {
   const long long most = min((long long)p.at.max_pages * p.at.page_size, (long long)kMostPlaces);
@@ -81,20 +91,22 @@ __device__ __forceinline__ Range places_of(const PagedAttn &p, int s) {
 }
 
 // A unit in a CTA's run. All parts' units are numbered through, with kPartCost numbers left out in front of each part.
-template <int UNIT> struct Cursor {
-  int s, part, unit, units, first, len;
-  long long number;
+template <int KEYS, int UNIT> struct Cursor {
+  int s, part, unit, units;
+  Range at;
+  int number;
 
+  __device__ __forceinline__ void set(const PagedAttn &p) {
+    at = places_of(p, s);
+    units = at.units(KEYS, UNIT);
+  }
   __device__ __forceinline__ void enter(const PagedAttn &p) {  // the next sequence with a place
     for (; s < p.n; ++s) {
-      const Range r = places_of(p, s);
-      first = r.first;
-      len = r.len;
-      units = (len - first + UNIT - 1) / UNIT;
+      set(p);
       if (units > 0) return;
     }
   }
-  __device__ __forceinline__ void next(const PagedAttn &p, int parts, long long end) {
+  __device__ __forceinline__ void next(const PagedAttn &p, int parts, int end) {
     ++number;
     if (++unit < units) return;
     unit = 0;
@@ -105,6 +117,16 @@ template <int UNIT> struct Cursor {
     if (number < end) enter(p);
   }
 };
+
+// Maximum (of log2) and sum of two pieces, and what each is multiplied by.
+__device__ __forceinline__ void meet(float &m, float &l, float m2, float l2, float &f, float &f2) {
+  const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
+  f = sm100::ex2(m - base);
+  f2 = sm100::ex2(m2 - base);
+  l = l * f + l2 * f2;
+  m = top;
+}
+constexpr float kSlack = 8.f;  // log2 that a weight may exceed 1 by before sums are rescaled to a new maximum
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -182,30 +204,39 @@ template <int D, int HB> struct Bf16Warp {
         x[i][j] = there >> (8 * i + 2 * t + (j & 1)) & 1 ? (c[0][j] + c[1][j]) * scale : -INFINITY;
     }
     uint32_t hi[R][2], lo[R][2];
-    float keep[R];
+    float top[R];
     bool moved = false;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float top = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      const float now = fmaxf(m[r], top), base = now == -INFINITY ? 0.f : now;
-      keep[r] = sm100::ex2(m[r] - base);
-      moved |= now > m[r];
-      m[r] = now;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float a = sm100::ex2(x[i][2 * r] - base), b = sm100::ex2(x[i][2 * r + 1] - base);
-        l[r] = i == 0 ? fmaf(l[r], keep[r], a + b) : l[r] + (a + b);
-        hi[r][i] = pack(a, b);
-        lo[r][i] = pack(a - __uint_as_float(hi[r][i] << 16), b - __uint_as_float(hi[r][i] & 0xffff0000u));
-      }
+      top[r] = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+      moved |= top[r] > m[r] + kSlack;
     }
     if (__any_sync(~0u, moved)) {
+      float keep[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float now = fmaxf(m[r], top[r]);
+        keep[r] = now == -INFINITY ? 1.f : sm100::ex2(m[r] - now);
+        l[r] *= keep[r];
+        m[r] = now;
+      }
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         o[i][0] *= keep[0]; o[i][1] *= keep[0];
         o[i][2] *= keep[R - 1]; o[i][3] *= keep[R - 1];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = sm100::ex2(x[i][2 * r] - base), b = sm100::ex2(x[i][2 * r + 1] - base);
+        l[r] += a + b;
+        hi[r][i] = pack(a, b);
+        lo[r][i] = pack(a - __uint_as_float(hi[r][i] << 16), b - __uint_as_float(hi[r][i] & 0xffff0000u));
       }
     }
 #pragma unroll
@@ -233,6 +264,37 @@ template <int D, int HB> struct Bf16Warp {
     }
   }
 
+  // The warp's sums to another warp, as they are held.
+  static constexpr int kGiven = R;  // maxima and sums of a lane
+  __device__ __forceinline__ void give(float *sums, float2 (*ml)[32], int lane) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) ml[r][lane] = make_float2(m[r], l[r]);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      if constexpr (R == 1) reinterpret_cast<float2 *>(sums)[i * 32 + lane] = make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
+      else reinterpret_cast<float4 *>(sums)[i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+    }
+  }
+  __device__ __forceinline__ void take(const float *sums, const float2 (*ml)[32], int lane) {
+    float f[R], f2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) meet(m[r], l[r], ml[r][lane].x, ml[r][lane].y, f[r], f2[r]);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      if constexpr (R == 1) {
+        const float2 a = reinterpret_cast<const float2 *>(sums)[i * 32 + lane];
+        o[i][0] = fmaf(o[i][0] + o[i][2], f[0], a.x * f2[0]);
+        o[i][1] = fmaf(o[i][1] + o[i][3], f[0], a.y * f2[0]);
+        o[i][2] = o[i][3] = 0.f;
+      } else {
+        const float4 a = reinterpret_cast<const float4 *>(sums)[i * 32 + lane];
+        o[i][0] = fmaf(o[i][0], f[0], a.x * f2[0]);
+        o[i][1] = fmaf(o[i][1], f[0], a.y * f2[0]);
+        o[i][2] = fmaf(o[i][2], f[R - 1], a.z * f2[R - 1]);
+        o[i][3] = fmaf(o[i][3], f[R - 1], a.w * f2[R - 1]);
+      }
+    }
+  }
   // The warp's sums into [HB][D] and [HB] of shared memory.
   __device__ __forceinline__ void end(float *sums, float2 *ml, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -334,18 +396,18 @@ template <int D, int HB> struct F32Warp {
     }
 #pragma unroll
     for (int d = HB; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    const float now = fmaxf(m, top), base = now == -INFINITY ? 0.f : now;
-    const float keep = sm100::ex2(m - base);
-    if (__any_sync(~0u, now > m)) {
+    if (__any_sync(~0u, top > m + kSlack)) {
+      const float now = fmaxf(m, top), keep = now == -INFINITY ? 1.f : sm100::ex2(m - now);
 #pragma unroll
       for (int h = 0; h < HB; ++h) {
         const float f = __shfl_sync(~0u, keep, h);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) f32x2::vmul(o[h][j], o[h][j], f);
       }
+      m = now;
+      l *= keep;
     }
-    m = now;
-    l *= keep;
+    const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float w = sm100::ex2(x[g] - base);
@@ -371,21 +433,54 @@ template <int D, int HB> struct F32Warp {
     __syncwarp();
   }
 
+  static constexpr int kGiven = 1;
+  __device__ __forceinline__ void halves() {  // the two rows' sums
+    if constexpr (kRows == 2)
+#pragma unroll
+      for (int h = 0; h < HB; ++h)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][j][e] += __shfl_xor_sync(~0u, o[h][j][e], 16);
+  }
+  __device__ __forceinline__ void give(float *sums, float2 (*ml)[32], int lane) {
+    halves();
+    ml[0][lane] = make_float2(m, l);
+    if (lane < kLanes)
+#pragma unroll
+      for (int h = 0; h < HB; ++h)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          reinterpret_cast<float4 *>(sums)[(h * kPer + j) * kLanes + lane] = make_float4(o[h][j][0], o[h][j][1], o[h][j][2], o[h][j][3]);
+  }
+  __device__ __forceinline__ void take(const float *sums, const float2 (*ml)[32], int lane) {
+    halves();
+    float mine, theirs;
+    meet(m, l, ml[0][lane].x, ml[0][lane].y, mine, theirs);
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      const float f = __shfl_sync(~0u, mine, h), f2 = __shfl_sync(~0u, theirs, h);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const float4 a = reinterpret_cast<const float4 *>(sums)[(h * kPer + j) * kLanes + lane % kLanes];
+        o[h][j][0] = fmaf(o[h][j][0], f, a.x * f2);
+        o[h][j][1] = fmaf(o[h][j][1], f, a.y * f2);
+        o[h][j][2] = fmaf(o[h][j][2], f, a.z * f2);
+        o[h][j][3] = fmaf(o[h][j][3], f, a.w * f2);
+      }
+    }
+  }
+  // (behind take: the rows' halves are together)
   __device__ __forceinline__ void end(float *sums, float2 *ml, int lane) {
 #pragma unroll
     for (int d = HB; d < 32; d *= 2) l += __shfl_xor_sync(~0u, l, d);
     if (lane < HB) ml[lane] = make_float2(m, l);
+    if (lane < kLanes)
 #pragma unroll
-    for (int h = 0; h < HB; ++h)
+      for (int h = 0; h < HB; ++h)
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if constexpr (kRows == 2) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[h][j][e] += __shfl_xor_sync(~0u, o[h][j][e], 16);
-        }
-        if (lane < kLanes)
+        for (int j = 0; j < kPer; ++j)
           reinterpret_cast<float4 *>(sums + h * D)[lane + 32 * j] = make_float4(o[h][j][0], o[h][j][1], o[h][j][2], o[h][j][3]);
-      }
   }
   static __device__ __forceinline__ int quad(int, int c) { return c; }
 };
@@ -405,64 +500,68 @@ __device__ __forceinline__ void finish(const PagedAttn &p, int s, int h, int D, 
 }
 
 template <typename T, int D, int HB>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const Split sp, const FastDiv by_page) {
+__global__ void __launch_bounds__(kThreads, Shape<T, D, HB>::kCtas)
+attn_kernel(const PagedAttn p, const Split sp, const FastDiv by_page) {
   using S = Shape<T, D, HB>;
+  using Warp = std::conditional_t<S::kF32, F32Warp<D, HB>, Bf16Warp<D, HB>>;
   constexpr int kUnit = S::kUnit, kKeys = S::kKeys, kChunks = S::kChunks, kStages = S::kStages;
+  constexpr int kHalf = kWarps / 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 ml[kWarps][HB];
+  __shared__ float2 given[kHalf][Warp::kGiven][32];
+  __shared__ float2 ml[kHalf][HB];
   __shared__ uint32_t masks[kWarps][kStages];
-  __shared__ long long scan[kWarps];
-  __shared__ long long start_number;
-  __shared__ int start_seq;
-  float *sums = reinterpret_cast<float *>(smem + kStages * S::kStage * kWarps);  // [kWarps][HB][D]
+  __shared__ int scan[kWarps], start_seq, start_number;
+  float *sums = reinterpret_cast<float *>(smem + kStages * S::kStage * kWarps);  // [kHalf][HB][D]
   __shared__ __align__(16) float weights[S::kF32 ? kWarps : 1][S::kF32 ? kKeys * HB : 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!sp.whole) {  // what the run is found from into L2 while the kernel in front ends
+    const int line = blockIdx.x * kThreads + tid;
+    if (line * 32ll < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.at.lens + line * 32ll));
+    if (line < p.n * sp.lines)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.at.table + line / sp.lines * p.at.ld_table + line % sp.lines * 32));
+  }
   wait_for_stream();
 
   // the CTA's run: the units with numbers in [t0, t1)
-  Cursor<kUnit> at = {};
-  long long t0, t1, part_begin, share = 0;
+  Cursor<kKeys, kUnit> at = {};
+  int t0, t1, part_begin, share = 0;
   if (sp.whole) {
     at.s = blockIdx.x / sp.parts;
     at.part = blockIdx.x % sp.parts;
-    const Range r = places_of(p, at.s);
-    at.first = r.first;
-    at.len = r.len;
-    at.units = (r.len - r.first + kUnit - 1) / kUnit;
+    at.set(p);
     t0 = part_begin = 0;
     t1 = at.units;
   } else {
     const int per = (p.n + kThreads - 1) / kThreads, a = min(tid * per, p.n), b = min(a + per, p.n);
     auto numbers = [&](int s) {
-      const Range r = places_of(p, s);
-      const int units = (r.len - r.first + kUnit - 1) / kUnit;
-      return units > 0 ? (long long)(units + kPartCost) * sp.parts : 0ll;
+      const int units = places_of(p, s).units(kKeys, kUnit);
+      return units > 0 ? (units + kPartCost) * sp.parts : 0;
     };
-    long long mine = 0;
+    int mine = 0;
     for (int s = a; s < b; ++s) mine += numbers(s);
-    long long upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-      const long long o = __shfl_up_sync(~0u, upto, d);
+      const int o = __shfl_up_sync(~0u, upto, d);
       if (lane >= d) upto += o;
     }
     if (lane == 31) scan[warp] = upto;
-    if (tid == 0) sp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !sp.by_part) sp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     __syncthreads();
-    long long total = 0;
+    int total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) upto += scan[w];
       total += scan[w];
     }
-    share = max((total + gridDim.x - 1) / gridDim.x, (long long)sp.least);
-    t0 = blockIdx.x * share;
+    share = max((total + gridDim.x - 1) / gridDim.x, (unsigned)sp.least);
+    t0 = min((long long)blockIdx.x * share, (long long)total);
     t1 = min(t0 + share, total);
     if (t0 < t1) {
-      long long before = upto - mine;
+      int before = upto - mine;
       if (before <= t0 && t0 < upto) {
         for (int s = a; s < b; ++s) {
-          const long long u = numbers(s);
+          const int u = numbers(s);
           if (t0 < before + u) {
             start_seq = s;
             start_number = before;
@@ -473,66 +572,103 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
       }
       __syncthreads();
       at.s = start_seq;
-      at.enter(p);
-      const int each = at.units + kPartCost;
-      const long long in = t0 - start_number;
-      at.part = static_cast<int>(in / each);
-      at.unit = max(static_cast<int>(in % each) - kPartCost, 0);
-      part_begin = start_number + (long long)at.part * each + kPartCost;
+      at.set(p);
+      const unsigned each = at.units + kPartCost, in = t0 - start_number;
+      at.part = in / each;
+      at.unit = max((int)(in - at.part * each) - kPartCost, 0);
+      part_begin = start_number + at.part * each + kPartCost;
       at.number = part_begin + at.unit;
+    } else {
+      at.number = t1;
     }
-    // rows of sequences without a place
-    for (int s = blockIdx.x; s < p.n; s += gridDim.x) {
-      const Range r = places_of(p, s);
-      if (r.len > r.first) continue;
-      for (int i = tid; i < p.H * (D / 4); i += kThreads)
-        finish<T>(p, s, i / (D / 4), D, i % (D / 4), 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
-    }
-    if (t0 >= t1 || at.number >= t1) return;
   }
 
   const int share_heads = p.H / p.Hk;
   // the ring
   const uint32_t ring = sm100::smem_u32(smem) + warp * kStages * S::kStage;
-  Cursor<kUnit> to = at;  // where the copies are
+  const size_t row_step = (size_t)p.Hk * D;
+  Cursor<kKeys, kUnit> to = at;  // where the copies are
   auto load = [&](int stage) {
-    const int i = to.first + to.unit * kUnit + warp * kKeys + lane % kKeys;
-    long long off = -1;
-    if (i < to.len) {
-      uint32_t pg, r;
-      by_page.split(i, pg, r);
-      const int page = p.at.table[to.s * p.at.ld_table + pg];
-      if (page >= 0 && page < p.at.n_pages) off = page * p.at.ld_page + ((long long)r * p.Hk + to.part / sp.blocks) * D;
-    }
-    const uint32_t there = __ballot_sync(~0u, off >= 0) & ((1u << kKeys) - 1);
-    if (lane == 0) masks[warp][stage] = there;
+    // places i0 .. i0 + kKeys - 1; i0 is a multiple of kKeys
+    const int i0 = to.at.first / kKeys * kKeys + to.unit * kUnit + warp * kKeys;
+    const uint32_t all = (1u << kKeys) - 1;
+    uint32_t there = to.at.first > i0 ? all << (to.at.first - i0) & all : all;  // (first is in the first block)
+    if (to.at.len - i0 < kKeys) there = to.at.len > i0 ? there & ((1u << (to.at.len - i0)) - 1) : 0;
+    const uint32_t keys = ring + stage * S::kStage, values = keys + S::kTile;
+    const int head = to.part / sp.blocks;
+    const int *table = p.at.table + to.s * p.at.ld_table;
     if (there) {
-      const uint32_t keys = ring + stage * S::kStage, values = keys + S::kTile;
+      uint32_t pg, r0;
+      by_page.split(i0, pg, r0);
+      if (r0 + kKeys <= (uint32_t)p.at.page_size) {  // all in one page
+        const int page = table[pg];
+        if (page < 0 || page >= p.at.n_pages) there = 0;
+        const size_t e = page * p.at.ld_page + (size_t)r0 * row_step + head * D + lane / kChunks * row_step +
+                         lane % kChunks * (16 / (int)sizeof(T));
+        const T *k = static_cast<const T *>(p.k_cache) + e, *v = static_cast<const T *>(p.v_cache) + e;
+        if (there)
 #pragma unroll
-      for (int j = 0; j < kKeys * kChunks / 32; ++j) {
-        const int c = j * 32 + lane, row = c / kChunks, chunk = c % kChunks;
-        const long long o = __shfl_sync(~0u, off, row);
-        const long long e = (o < 0 ? 0 : o) + chunk * (16 / (int)sizeof(T));
-        copy16(keys + (row * kChunks + stored<S::kF32, false>(row, chunk)) * 16, static_cast<const T *>(p.k_cache) + e, o >= 0);
-        copy16(values + (row * kChunks + stored<S::kF32, true>(row, chunk)) * 16, static_cast<const T *>(p.v_cache) + e, o >= 0);
+          for (int j = 0; j < kKeys * kChunks / 32; ++j) {
+            const int c = j * 32 + lane, row = c / kChunks, chunk = c % kChunks;
+            const bool on = there >> row & 1;
+            copy16(keys + (row * kChunks + stored<S::kF32, false>(row, chunk)) * 16, k, on);
+            copy16(values + (row * kChunks + stored<S::kF32, true>(row, chunk)) * 16, v, on);
+            // the next one of this lane: 32 / kChunks rows on, or in the same row
+            const size_t step = kChunks <= 32 ? 32 / kChunks * row_step
+                                : (j + 1) % (kChunks / 32) ? 32 * (16 / sizeof(T))
+                                                           : row_step - (kChunks - 32) * (16 / sizeof(T));
+            k += step;
+            v += step;
+          }
+      } else {
+        const int i = i0 + lane % kKeys;
+        long long off = -1;
+        if (there >> (lane % kKeys) & 1) {
+          uint32_t r;
+          by_page.split(i, pg, r);
+          const int page = table[pg];
+          if (page >= 0 && page < p.at.n_pages) off = page * p.at.ld_page + r * (long long)row_step + head * D;
+        }
+        there = __ballot_sync(~0u, off >= 0) & all;
+        if (there)
+#pragma unroll 1
+          for (int j = 0; j < kKeys * kChunks / 32; ++j) {
+            const int c = j * 32 + lane, row = c / kChunks, chunk = c % kChunks;
+            const long long o = __shfl_sync(~0u, off, row);
+            const long long e = (o < 0 ? 0 : o) + chunk * (16 / (int)sizeof(T));
+            copy16(keys + (row * kChunks + stored<S::kF32, false>(row, chunk)) * 16, static_cast<const T *>(p.k_cache) + e, o >= 0);
+            copy16(values + (row * kChunks + stored<S::kF32, true>(row, chunk)) * 16, static_cast<const T *>(p.v_cache) + e, o >= 0);
+          }
       }
     }
+    if (lane == 0) masks[warp][stage] = there;
     // the queries of a part into L1 while its first keys are on their way
     if (warp == 0 && (to.unit == 0 || to.number == at.number)) {
-      const int h0 = to.part / sp.blocks * share_heads + to.part % sp.blocks * HB;
+      const int h0 = head * share_heads + to.part % sp.blocks * HB;
       const char *q = reinterpret_cast<const char *>(static_cast<const T *>(p.q) + to.s * p.ldq + (long long)h0 * D);
       for (int i = lane * 128; i < min(HB, share_heads - to.part % sp.blocks * HB) * D * (int)sizeof(T); i += 32 * 128)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
     }
     to.next(p, sp.parts, t1);
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) {
     if (to.number < t1) load(i);
     commit();
   }
+  // rows of sequences without a place meanwhile
+  if (!sp.whole)
+#pragma unroll 1
+    for (int s = blockIdx.x; s < p.n; s += gridDim.x) {
+      const Range r = places_of(p, s);
+      if (r.len > r.first) continue;
+      for (int i = tid; i < p.H * (D / 4); i += kThreads)
+        finish<T>(p, s, i / (D / 4), D, i % (D / 4), 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (sp.by_part)
+        for (int i = tid; i < sp.parts; i += kThreads) sp.joins[s * sp.parts + i] = make_int4(-1, 0, 0, 0);
+    }
+  if (!sp.whole && at.number >= t1) return;
 
-  using Warp = std::conditional_t<S::kF32, F32Warp<D, HB>, Bf16Warp<D, HB>>;
   Warp w;
   int stage = 0;
   bool fresh = true;
@@ -558,19 +694,26 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
     }
     fresh = last;
     if (last) {
-      w.end(sums + warp * HB * D, ml[warp], lane);
+      // half of the warps hand their sums to the others
+      if (warp >= kHalf) w.give(sums + (warp - kHalf) * HB * D, given[warp - kHalf], lane);
       __syncthreads();
-      const long long part_end = part_begin + at.units;
+      if (warp < kHalf) {
+        w.take(sums + warp * HB * D, given[warp], lane);
+        __syncwarp();
+        w.end(sums + warp * HB * D, ml[warp], lane);
+      }
+      __syncthreads();
+      const int part_end = part_begin + at.units;
       const bool begun = part_begin >= t0, done = part_end <= t1;
       for (int i = tid; i < HB * (D / 4); i += kThreads) {
         const int h = i / (D / 4), c = i % (D / 4);
         float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) m = fmaxf(m, ml[k][h].x);
+        for (int k = 0; k < kHalf; ++k) m = fmaxf(m, ml[k][h].x);
         const float zero = m == -INFINITY ? 0.f : m;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
+        for (int k = 0; k < kHalf; ++k) {
           const float f = sm100::ex2(ml[k][h].x - zero);
           const float4 a = reinterpret_cast<const float4 *>(sums + (k * HB + h) * D)[Warp::quad(h, c)];
           l = fmaf(f, ml[k][h].y, l);
@@ -584,7 +727,9 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
           if (c == 0) sp.ml[piece * HB + h] = make_float2(m, l);
         }
       }
-      if (begun && !done && tid == 0) sp.joins[blockIdx.x] = make_int4(at.s, at.part, static_cast<int>((part_end - 1) / share), 0);
+      if (begun && tid == 0 && !sp.whole && (sp.by_part || !done))
+        sp.joins[sp.by_part ? at.s * sp.parts + at.part : blockIdx.x] =
+            done ? make_int4(-1, 0, 0, 0) : make_int4(at.s, at.part, blockIdx.x, (part_end - 1) / share);
       part_begin = part_end + kPartCost;
     }
     if (at.units == 0) return;
@@ -594,35 +739,32 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const PagedAttn p, const
   }
 }
 
-// The pieces of a part, of the CTAs first .. last, added up: block (first, some of the heads).
+// The pieces of a part added up: block (entry of joins, some of the heads).
 template <typename T, int D, int HB>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn p, const Split sp) {
   constexpr int kQuads = D / 4;
   __shared__ float4 sums[kJoinThreads];
   __shared__ float2 ml[kJoinThreads];
   wait_for_stream();
-  const int4 join = sp.joins[blockIdx.x];
+  const int4 join = sp.joins[blockIdx.x];  // (written by the kernel in front)
   if (join.x < 0) return;
   const int each = HB / gridDim.y, share_heads = p.H / p.Hk, block = join.y % sp.blocks;
   const int heads = min(HB, share_heads - block * HB), h0 = join.y / sp.blocks * share_heads + block * HB;
   const int items = each * kQuads, groups = max(kJoinThreads / items, 1);
-  const int pieces = join.z - blockIdx.x + 1;
+  const int pieces = join.w - join.z + 1;
   for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
     const int i = i0 + threadIdx.x % min(items, kJoinThreads), group = threadIdx.x / min(items, kJoinThreads);
     const int h = blockIdx.y * each + i / kQuads, c = i % kQuads;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, f, f2;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (h < heads) {
 #pragma unroll 4
       for (int k = group; k < pieces; k += groups) {
-        const size_t piece = 2 * (size_t)(blockIdx.x + k) + (k == 0);
+        const size_t piece = 2 * (size_t)(join.z + k) + (k == 0);
         const float2 b = sp.ml[piece * HB + h];
         const float4 a = reinterpret_cast<const float4 *>(sp.sums + (piece * HB + h) * D)[c];
-        const float now = fmaxf(m, b.x), zero = now == -INFINITY ? 0.f : now;
-        const float f = sm100::ex2(m - zero), e = sm100::ex2(b.x - zero);
-        l = l * f + b.y * e;
-        v = make_float4(v.x * f + a.x * e, v.y * f + a.y * e, v.z * f + a.z * e, v.w * f + a.w * e);
-        m = now;
+        meet(m, l, b.x, b.y, f, f2);
+        v = make_float4(v.x * f + a.x * f2, v.y * f + a.y * f2, v.z * f + a.z * f2, v.w * f + a.w * f2);
       }
     }
     if (groups > 1) {
@@ -633,11 +775,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn p, c
         for (int g = 1; g < groups; ++g) {
           const float2 b = ml[g * items + threadIdx.x];
           const float4 a = sums[g * items + threadIdx.x];
-          const float now = fmaxf(m, b.x), zero = now == -INFINITY ? 0.f : now;
-          const float f = sm100::ex2(m - zero), e = sm100::ex2(b.x - zero);
-          l = l * f + b.y * e;
-          v = make_float4(v.x * f + a.x * e, v.y * f + a.y * e, v.z * f + a.z * e, v.w * f + a.w * e);
-          m = now;
+          meet(m, l, b.x, b.y, f, f2);
+          v = make_float4(v.x * f + a.x * f2, v.y * f + a.y * f2, v.z * f + a.z * f2, v.w * f + a.w * f2);
         }
       }
     }
@@ -673,27 +812,37 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
   const long long most = (long long)p.at.max_pages * p.at.page_size;
   long long longest = p.max_len > 0 ? std::min<long long>(p.max_len, most) : most;
   if (p.window > 0) longest = std::min<long long>(longest, p.window);
-  const long long parts = (long long)p.n * sp.parts, slots = (S::kTwo ? 2 : 1) * std::max(sm_count(), 1);
+  const long long parts = (long long)p.n * sp.parts, slots = (long long)S::kCtas * std::max(sm_count(), 1);
   sp.whole = longest <= (long long)kLeast * S::kUnit;
   const FastDiv by(p.at.page_size);
   if (sp.whole) {
     e = launch_early(kernel, dim3(static_cast<unsigned>(parts)), kThreads, S::kBytes, stream, p, sp, by);
     return e == cudaSuccess ? LA_OK : fail("launch failed", e);
   }
+  if ((most / S::kUnit + 2 + kPartCost) * parts > INT_MAX) {
+    set_error("la_paged_attn: n * Hk times max_pages * page_size too large");
+    return LA_ERR_INVALID_ARG;
+  }
   const long long units = ((longest + S::kUnit - 1) / S::kUnit + kPartCost) * parts;
   const int ctas = static_cast<int>(std::min(slots, (units + kLeast - 1) / kLeast));
+  // (of longer rows a part)
+  sp.lines = static_cast<int>(std::min<long long>(((longest - 1) / p.at.page_size + 32) / 32, 64));
+  if ((long long)sp.lines * p.n > INT_MAX / 2) sp.lines = 0;
+  if (p.window > 0) sp.lines = 0;
   const size_t sums = (size_t)2 * ctas * HB * D * 4, ml = (size_t)2 * ctas * HB * sizeof(float2);
+  sp.by_part = parts <= ctas;
+  const size_t entries = sp.by_part ? parts : ctas;
   cudaMemPool_t pool = library_pool();
   if (!pool) return fail("could not create the workspace pool", cudaGetLastError());
   uint8_t *ws = nullptr;
-  e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), sums + ml + (size_t)ctas * sizeof(int4), pool, stream);
+  e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), sums + ml + entries * sizeof(int4), pool, stream);
   if (e != cudaSuccess) return fail("workspace allocation failed", e);
   sp.sums = reinterpret_cast<float *>(ws);
   sp.ml = reinterpret_cast<float2 *>(ws + sums);
   sp.joins = reinterpret_cast<int4 *>(ws + sums + ml);
   e = launch_early(kernel, dim3(ctas), kThreads, S::kBytes, stream, p, sp, by);
   if (e == cudaSuccess)
-    e = launch_early(join_kernel<T, D, HB>, dim3(ctas, parts <= 64 ? HB : 1), kJoinThreads, 0, stream, p, sp);
+    e = launch_early(join_kernel<T, D, HB>, dim3(static_cast<unsigned>(entries), parts <= 64 ? HB : 1), kJoinThreads, 0, stream, p, sp);
   const cudaError_t f = cudaFreeAsync(ws, stream);
   if (e == cudaSuccess) e = f;
   return e == cudaSuccess ? LA_OK : fail("launch failed", e);
