@@ -75,6 +75,24 @@ def la_beam_cache(k_cache, v_cache, table, lens, parent, B, W, page_size, n_page
 
 
 # ---- torch-tensor wrappers -----------------------------------------------------
+# Calls of a few tokens are bound by their host side: the wrappers look at each tensor's attributes once, and leave
+# the general case (and the reasons of a refusal) to functions of their own.
+
+torch = None  # imported by the first call
+
+
+def _setup():
+    global torch, _FLAGS
+    import torch as t
+    _FLAGS = {t.bfloat16: 0, t.float32: _binding.CONSTANTS["LA_F32"]}
+    torch = t
+    return t
+
+
+def _handle(idx, stream):
+    """The current stream's handle where a call runs there, on the current device; else None."""
+    return torch._C._cuda_getCurrentRawStream(idx) if stream is None and torch._C._cuda_getDevice() == idx else None
+
 
 def _inner(t, name, lead):
     """Strides of t's first ``lead`` dimensions; the others must be dense, and rows must not overlap."""
@@ -93,38 +111,43 @@ def _inner(t, name, lead):
             raise ValueError(f"{name}: dimension {i} overlaps itself or the next")
         out.append(s)
         at = s * max(shape[i], 1)
-    return out[::-1]
+    return tuple(out[::-1])
 
 
 def _caches(k_cache, v_cache, lead, idx, dtype):
-    """Page (and layer) strides of the two pools, which must agree."""
-    if k_cache.dim() != lead + 3 or v_cache.shape != k_cache.shape:
-        raise ValueError(f"k_cache and v_cache must be one shape of {lead + 3} dimensions, got {tuple(k_cache.shape)}, "
+    """Shape and page (and layer) strides of the two pools, which must agree."""
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != lead + 3 or v_cache.shape != shape:
+        raise ValueError(f"k_cache and v_cache must be one shape of {lead + 3} dimensions, got {tuple(shape)}, "
                          f"{tuple(v_cache.shape)}")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.get_device() != idx or not t.is_cuda:
-            raise ValueError(f"{name} must be on CUDA device {idx}, got {t.device}")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if k_cache.is_contiguous() and v_cache.is_contiguous():
-        return k_cache.stride()[:lead]
+    if k_cache.get_device() != idx or v_cache.get_device() != idx:
+        raise ValueError(f"k_cache and v_cache must be on CUDA device {idx}, got {k_cache.device}, {v_cache.device}")
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        raise TypeError(f"k_cache and v_cache must be {dtype}, got {k_cache.dtype}, {v_cache.dtype}")
+    if v_cache.stride() == stride and lead == 1:
+        _, size, Hk, d = shape
+        if stride[1:] == (Hk * d, d, 1) and stride[0] >= size * Hk * d:
+            return shape, stride[:1]
     ld = _inner(k_cache, "k_cache", lead)
     if _inner(v_cache, "v_cache", lead) != ld:
         raise ValueError("k_cache and v_cache must have the same strides")
-    return ld
+    return shape, ld
 
 
 def _table(table, lens, n, idx):
     """(entries of a row, row stride) of a page table, with its lengths checked."""
-    import torch
-    if table.dim() != 2 or table.shape[0] != n or table.dtype is not torch.int32 or table.get_device() != idx:
+    shape, i32 = table.shape, torch.int32
+    if len(shape) != 2 or shape[0] != n or table.dtype is not i32 or table.get_device() != idx:
         raise ValueError(f"table must be int32 [{n}, pages] on CUDA device {idx}")
-    _check(lens, "lens", torch.int32, (n,), idx)
-    width = table.shape[1]
+    if lens.dtype is not i32 or lens.shape != (n,) or lens.get_device() != idx or not lens.is_contiguous():
+        _check(lens, "lens", i32, (n,), idx)
+    width = shape[1]
     step, unit = table.stride()
+    if unit == 1 and step >= width:
+        return width, step if step > width else width
     if (width > 1 and unit != 1) or (n > 1 and step < width):
         raise ValueError("table: the entries of a row must be dense, and rows apart")
-    return width, step if n > 1 and step > width else width
+    return width, width if n <= 1 else step
 
 
 def cache_append(q, k, v, k_cache, v_cache, table, lens, freq=None, pos=None, sections=None, interleaved=False,
@@ -136,11 +159,12 @@ def cache_append(q, k, v, k_cache, v_cache, table, lens, freq=None, pos=None, se
     cu_seqlens int32 [n+1] (None: one token for each sequence). freq float64
     [pairs], pos int32 [total,axes] (None: the place in the cache) and sections
     as rotary; freq None: no rotation. Returns the turned queries (or None)."""
-    import torch
-    idx, dt, i32 = _index(k, "k"), k.dtype, torch.int32
-    ldk, ldv = _rows(k, "k"), _rows(v, "v")
-    N, Hk, d = k.shape
-    if v.shape != k.shape or v.dtype is not dt or v.get_device() != idx:
+    t = torch or _setup()
+    idx, dt, shape, ldk, ldv = k.get_device(), k.dtype, k.shape, _rows(k, "k"), _rows(v, "v")
+    if idx < 0:
+        _index(k, "k")
+    N, Hk, d = shape
+    if v.shape != shape or v.dtype is not dt or v.get_device() != idx:
         raise ValueError("v must have k's shape, dtype and device")
     H = ldq = 0
     if q is not None:
@@ -148,33 +172,46 @@ def cache_append(q, k, v, k_cache, v_cache, table, lens, freq=None, pos=None, se
         Nq, H, dq = q.shape
         if Nq != N or dq != d or q.dtype is not dt or q.get_device() != idx:
             raise ValueError("q and k must agree in tokens, channels, dtype and device")
-    n = N if cu_seqlens is None else cu_seqlens.numel() - 1
-    _check(cu_seqlens, "cu_seqlens", i32, (n + 1,), idx)
-    (ld_page,) = _caches(k_cache, v_cache, 1, idx, dt)
-    if tuple(k_cache.shape[2:]) != (Hk, d):
-        raise ValueError(f"caches must be [pages, page_size, {Hk}, {d}], got {tuple(k_cache.shape)}")
+    n = N
+    if cu_seqlens is not None:
+        n = cu_seqlens.numel() - 1
+        _check(cu_seqlens, "cu_seqlens", t.int32, (n + 1,), idx)
+    pages, (ld_page,) = _caches(k_cache, v_cache, 1, idx, dt)
+    if pages[2] != Hk or pages[3] != d:
+        raise ValueError(f"caches must be [pages, page_size, {Hk}, {d}], got {tuple(pages)}")
     width, ld_table = _table(table, lens, n, idx)
-    axes, s = 0, (0, 0, 0)
+    axes, s0, s1, s2 = 0, 0, 0, 0
     if freq is not None:
-        pairs = freq.numel()
-        s = (pairs,) if sections is None else tuple(sections)
-        axes = len(s)
-        if sum(s) != pairs or not 1 <= axes <= 3:
-            raise ValueError("sections: the pairs of one to three axes, as many as freq has")
-        s = (s + (0, 0))[:3]
-    _check(freq, "freq", torch.float64, (s[0] + s[1] + s[2],), idx)
-    _check(pos, "pos", i32, (N, axes), idx)
-    _check(q_out, "q_out", dt, (N, H, d), idx)
-    flags = _flag(dt) | (LAYER_CONSTANTS["LA_ROT_INTERLEAVED"] if interleaved else 0)
+        s0 = pairs = freq.numel()
+        axes = 1
+        if sections is not None:
+            axes = len(sections)
+            if sum(sections) != pairs or not 1 <= axes <= 3:
+                raise ValueError("sections: the pairs of one to three axes, as many as freq has")
+            s0, s1, s2 = (*sections, 0, 0)[:3]
+        _check(freq, "freq", t.float64, (pairs,), idx)
+    if pos is not None:
+        _check(pos, "pos", t.int32, (N, axes), idx)
+    if q_out is not None:
+        _check(q_out, "q_out", dt, (N, H, d), idx)
+    flags = _FLAGS.get(dt)
+    if flags is None:
+        _flag(dt)
+    if interleaved:
+        flags |= LAYER_CONSTANTS["LA_ROT_INTERLEAVED"]
 
     def body(handle):
-        a = None if q is None else q.new_empty((N, H, d)) if q_out is None else q_out
-        _run("la_cache_append", _at(q), k.data_ptr(), v.data_ptr(), _at(a), k_cache.data_ptr(), v_cache.data_ptr(),
-             table.data_ptr(), lens.data_ptr(), _at(cu_seqlens), _at(pos), _at(freq), axes, *s, n, N, H, Hk, d,
-             k_cache.shape[1], k_cache.shape[0], width, ld_table, ldq, ldk, ldv, ld_page, flags, handle)
+        a = None if q is None else q_out
+        if a is None and q is not None:
+            a = t.empty((N, H, d), dtype=dt, device=q.device)
+        _run("la_cache_append", None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             None if a is None else a.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(),
+             lens.data_ptr(), _at(cu_seqlens), _at(pos), _at(freq), axes, s0, s1, s2, n, N, H, Hk, d, pages[1], pages[0],
+             width, ld_table, ldq, ldk, ldv, ld_page, flags, handle)
         return a
 
-    return _launch(idx, stream, body)
+    handle = _handle(idx, stream)
+    return body(handle) if handle is not None else _launch(idx, stream, body)
 
 
 def paged_attn(q, k_cache, v_cache, table, lens, scale=None, window=0, max_len=0, with_lse=False, o=None, stream=None):
@@ -183,56 +220,71 @@ def paged_attn(q, k_cache, v_cache, table, lens, scale=None, window=0, max_len=0
     v_cache [pages,page_size,Hk,d], page stride free; table int32
     [n,max_pages]; lens int32 [n]; scale None: d^-1/2; window > 0: the last
     places only. Returns (o [n,H,d], lse fp32 [n,H] or None)."""
-    import torch
-    ldq = _rows(q, "q")
-    idx, dt = _index(q, "q"), q.dtype
+    t = torch or _setup()
+    idx, dt, ldq = q.get_device(), q.dtype, _rows(q, "q")
+    if idx < 0:
+        _index(q, "q")
     n, H, d = q.shape
-    (ld_page,) = _caches(k_cache, v_cache, 1, idx, dt)
-    pages, size, Hk, dk = k_cache.shape
-    if dk != d:
-        raise ValueError(f"caches must have q's {d} channels, got {dk}")
+    pages, (ld_page,) = _caches(k_cache, v_cache, 1, idx, dt)
+    if pages[3] != d:
+        raise ValueError(f"caches must have q's {d} channels, got {pages[3]}")
     width, ld_table = _table(table, lens, n, idx)
-    _check(o, "o", dt, (n, H, d), idx)
-    flags = _flag(dt)
+    if o is not None:
+        _check(o, "o", dt, (n, H, d), idx)
+    flags = _FLAGS.get(dt)
+    if flags is None:
+        _flag(dt)
 
     def body(handle):
-        out = q.new_empty((n, H, d)) if o is None else o
-        lse = q.new_empty((n, H), dtype=torch.float32) if with_lse else None
+        out = t.empty((n, H, d), dtype=dt, device=q.device) if o is None else o
+        lse = t.empty((n, H), dtype=t.float32, device=q.device) if with_lse else None
         _run("la_paged_attn", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _at(lse),
-             table.data_ptr(), lens.data_ptr(), n, H, Hk, d, size, pages, width, ld_table, max_len, window,
+             table.data_ptr(), lens.data_ptr(), n, H, pages[2], d, pages[1], pages[0], width, ld_table, max_len, window,
              d ** -0.5 if scale is None else scale, ldq, ld_page, flags, handle)
         return out, lse
 
-    return _launch(idx, stream, body)
+    handle = _handle(idx, stream)
+    return body(handle) if handle is not None else _launch(idx, stream, body)
 
 
 def beam_select(logits, scores, K=None, done=None, eos=0, stream=None):
     """Beam search's step (la_beam_select). logits [B,W,V] (bf16 or fp32, row
     stride free); scores fp32 [B,W]; done bool or uint8 [B,W] or None; K None: W.
     Returns (scores fp32, parent int32, token int32), each [B,K], best first."""
-    import torch
-    if logits.dim() != 3:
-        raise ValueError(f"logits must be [B, W, V], got {tuple(logits.shape)}")
-    idx, f32, i32 = _index(logits, "logits"), torch.float32, torch.int32
-    B, W, V = logits.shape
+    t = torch or _setup()
+    shape, idx, f32, i32 = logits.shape, logits.get_device(), t.float32, t.int32
+    if len(shape) != 3:
+        raise ValueError(f"logits must be [B, W, V], got {tuple(shape)}")
+    if idx < 0:
+        _index(logits, "logits")
+    B, W, V = shape
     sb, sw, sv = logits.stride()
-    ld = V if logits.is_contiguous() else sw if W > 1 else sb if B > 1 else V
-    if (V > 1 and sv != 1) or (W > 1 and B > 1 and sb != W * sw) or ld < V:
-        raise ValueError("logits: a row must be dense, and rows at one stride")
+    if sv == 1 and sb == W * sw and sw >= V:
+        ld = sw
+    else:
+        ld = V if logits.is_contiguous() else sw if W > 1 else sb if B > 1 else V
+        if (V > 1 and sv != 1) or (W > 1 and B > 1 and sb != W * sw) or ld < V:
+            raise ValueError("logits: a row must be dense, and rows at one stride")
     K = W if K is None else K
     _check(scores, "scores", f32, (B, W), idx)
     if done is not None:
-        _check(done, "done", torch.bool if done.dtype is torch.bool else torch.uint8, (B, W), idx)
-    flags = _flag(logits.dtype)
+        _check(done, "done", t.bool if done.dtype is t.bool else t.uint8, (B, W), idx)
+    flags = _FLAGS.get(logits.dtype)
+    if flags is None:
+        _flag(logits.dtype)
 
     def body(handle):
-        best = scores.new_empty((B, K))
-        parent, token = scores.new_empty((B, K), dtype=i32), scores.new_empty((B, K), dtype=i32)
+        if K == W:
+            best = t.empty_like(scores)
+        else:
+            best = t.empty((B, K), dtype=f32, device=scores.device)
+        parent, token = t.empty_like(best, dtype=i32), t.empty_like(best, dtype=i32)
         _run("la_beam_select", logits.data_ptr(), scores.data_ptr(), _at(done), best.data_ptr(), parent.data_ptr(),
              token.data_ptr(), B, W, V, K, ld, eos, flags, handle)
         return best, parent, token
 
-    return _launch(idx, stream, body)
+    handle = _handle(idx, stream)
+    return body(handle) if handle is not None else _launch(idx, stream, body)
 
 
 def beam_states(pool, parent, slots=None, layered=False, stream=None):
@@ -240,7 +292,8 @@ def beam_states(pool, parent, slots=None, layered=False, stream=None):
     row slots[b*W + w] becomes what row slots[b*W + parent[b,w]] was. pool
     [rows, ...], or [layers, rows, ...] with ``layered``, any dtype, a row dense;
     parent int32 [B,W]; slots int32 [B*W] (None: row b*W + w). Returns pool."""
-    import torch
+    if torch is None:
+        _setup()
     idx, lead = _index(pool, "pool"), 2 if layered else 1
     if pool.dim() < lead:
         raise ValueError(f"pool must have {lead} dimensions or more, got {tuple(pool.shape)}")
@@ -260,7 +313,8 @@ def beam_states(pool, parent, slots=None, layered=False, stream=None):
              pool.shape[0] if layered else 1, row * e, ld[-1] * e, ld[0] * e if layered else 0, handle)
         return pool
 
-    return _launch(idx, stream, body)
+    handle = _handle(idx, stream)
+    return body(handle) if handle is not None else _launch(idx, stream, body)
 
 
 def beam_cache(k_cache, v_cache, table, lens, parent, layered=False, stream=None):
@@ -269,15 +323,16 @@ def beam_cache(k_cache, v_cache, table, lens, parent, layered=False, stream=None
     k_cache, v_cache [pages,page_size,Hk,d], or [layers,pages,page_size,Hk,d]
     with ``layered``, page and layer strides free; table int32 [B*W,max_pages];
     lens int32 [B*W]; parent int32 [B,W]. Returns (k_cache, v_cache, table)."""
-    import torch
+    if torch is None:
+        _setup()
     idx, lead = _index(k_cache, "k_cache"), 2 if layered else 1
     if parent.dim() != 2:
         raise ValueError(f"parent must be [B, W], got {tuple(parent.shape)}")
     B, W = parent.shape
     _check(parent, "parent", torch.int32, (B, W), idx)
-    ld = _caches(k_cache, v_cache, lead, idx, k_cache.dtype)
+    shape, ld = _caches(k_cache, v_cache, lead, idx, k_cache.dtype)
     width, ld_table = _table(table, lens, B * W, idx)
-    pages, size, Hk, d = k_cache.shape[lead - 1:]
+    pages, size, Hk, d = shape[lead - 1:]
     e = k_cache.element_size()
 
     def body(handle):
@@ -286,4 +341,5 @@ def beam_cache(k_cache, v_cache, table, lens, parent, layered=False, stream=None
              ld[-1] * e, ld[0] * e if layered else 0, handle)
         return k_cache, v_cache, table
 
-    return _launch(idx, stream, body)
+    handle = _handle(idx, stream)
+    return body(handle) if handle is not None else _launch(idx, stream, body)
