@@ -789,8 +789,13 @@ int fail(const char *what, cudaError_t e) {
   return LA_ERR_CUDA;
 }
 
-// Units below which a part is not split.
-constexpr int kLeast = 2;
+// Least units of a run: parts of a few units are still spread over the SMs (one sequence of 4096 places, 16/4 heads of
+// 128: 1 unit 10.2 us, 2 10.9, 4 12.4).
+constexpr int kLeast = 1;
+// Units up to which a part is one CTA's, which saves the second kernel; and where there are parts for half of the CTAs
+// or more. (16/4 heads of 128, bfloat16, whole and split: 16 x 384 places 9.6 and 12.7 us, 1 x 384 9.1 and 8.9,
+// 1 x 512 10.7 and 9.1; 64 x 384 12.2 and 16.8, 64 x 768 21.9 and 26.3.)
+constexpr int kWhole = 6, kWholeOfMany = 16;
 
 template <typename T, int D, int HB>
 int launch(const PagedAttn &p, cudaStream_t stream) {
@@ -813,7 +818,7 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
   long long longest = p.max_len > 0 ? std::min<long long>(p.max_len, most) : most;
   if (p.window > 0) longest = std::min<long long>(longest, p.window);
   const long long parts = (long long)p.n * sp.parts, slots = (long long)S::kCtas * std::max(sm_count(), 1);
-  sp.whole = longest <= (long long)kLeast * S::kUnit;
+  sp.whole = longest <= (long long)(2 * parts >= slots ? kWholeOfMany : kWhole) * S::kUnit;
   const FastDiv by(p.at.page_size);
   if (sp.whole) {
     e = launch_early(kernel, dim3(static_cast<unsigned>(parts)), kThreads, S::kBytes, stream, p, sp, by);

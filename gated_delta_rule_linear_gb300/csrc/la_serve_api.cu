@@ -107,7 +107,7 @@ int la_beam_select(const void *logits, const float *scores, const unsigned char 
   if (B < 0 || V < 1) return bad(fn, "B must be >= 0, V >= 1");
   if (W < 1 || W > kMaxBeams) return unsupported(fn, "W must be 1..32", W);
   if (K < 1 || K > kMaxBeams) return unsupported(fn, "K must be 1..32", K);
-  if ((long long)W * V > INT_MAX || K > W * V) return bad(fn, "K must be <= W*V, W*V below 2^31");
+  if ((long long)W * V > INT_MAX - 65535 || K > W * V) return bad(fn, "K must be <= W*V, W*V below 2^31 - 2^16");
   if (((long long)V / 128 + 1) * W * B > INT_MAX / 2) return bad(fn, "B*W*V too large");
   if (ld < V) return bad(fn, "ld must be >= V");
   if (done && (eos < 0 || eos >= V)) return bad(fn, "eos must be in 0..V-1");

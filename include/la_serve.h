@@ -82,8 +82,9 @@ int la_cache_append(const void *q, const void *k, const void *v, void *q_out, vo
  *   flags   LA_F32 (float32 q, o, caches) or 0 (bfloat16)
  *   q, o, k_cache, v_cache 16-byte aligned; ldq, ld_page multiples of 16 bytes
  *
- * Workspace from the library's pool where the length may be split: up to
- * 4*SMs*16*(d+2)*4 bytes (about 10 MB). What the cache holds behind a
+ * n*Hk*max_pages*page_size is below 2^36 (with more than 16 heads for each of
+ * Hk, H/16 counts in its place). Workspace from the library's pool where the
+ * length may be split: up to about 6 MB. What the cache holds behind a
  * sequence's length, or in front of its window, is not used, whatever it is;
  * inside it, inputs are finite.
  */
@@ -106,7 +107,7 @@ int la_paged_attn(const void *q, const void *k_cache, const void *v_cache, void 
  *           continuation eos, at scores[w]; its logits are not read
  *   scores_out float32 [B][K], parent int32 [B][K] (the beam, 0..W-1), token
  *           int32 [B][K]: outputs, not the inputs
- *   1 <= W <= 32, 1 <= K <= 32, K <= W*V, W*V < 2^31, 0 <= eos < V (with done)
+ *   1 <= W <= 32, 1 <= K <= 32, K <= W*V, W*V < 2^31 - 2^16, 0 <= eos < V (with done)
  *
  * Equal candidates are taken in the order of w*V + v. Candidates without a
  * value (a token not allowed, a beam with no token allowed, whose score is not

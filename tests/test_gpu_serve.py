@@ -90,6 +90,23 @@ def test_append_of_padded_and_crossing_bounds():
     # the unused end of a batch holds zeros, or repeats the last bound; bounds outside [0, total]; overlapping ones
     for cu in ([0, 4, 9, 0, 0], [0, 4, 9, 9, 9], [-5, 4, 9, 100, 100], [0, 5, 2, 8, 8]):
         check_append(gen, [4, 5, 0, 0], [9, 3, 20, 5], 2, 1, 64, [32], 8, BF, cu=cu)
+    lens = [2 ** 31 - 1, -(2 ** 31), 7]  # of three tokens each: no places, but for the last
+    kc = rand(gen, 9, 8, 1, 64, dtype=BF).cuda()
+    vc, k = kc.clone(), rand(gen, 9, 1, 64, dtype=BF).cuda()
+    table = torch.arange(9, dtype=torch.int32).reshape(3, 3).cuda()
+    before = kc.clone()
+    la.cache_append(None, k, k, kc, vc, table, ints(lens).cuda(), cu_seqlens=ints([0, 3, 6, 9]).cuda())
+    before[6, 4:7] = k[6:]
+    assert torch.equal(kc, before) and torch.equal(vc, before)
+
+
+def test_append_of_many_sequences():
+    """More sequences than a block has threads, many of them empty, padded by zeros."""
+    gen = torch.Generator().manual_seed(11)
+    n = 1500
+    new = [int(x) for x in torch.randint(0, 3, (n,), generator=gen)]
+    cu = [sum(new[:i]) for i in range(n + 1)] + [0] * 500
+    check_append(gen, new + [0] * 500, torch.randint(0, 40, (n + 500,), generator=gen).tolist(), 2, 1, 64, [32], 16, BF, cu=cu)
 
 
 def test_append_without_places():

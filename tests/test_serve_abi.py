@@ -150,6 +150,7 @@ BAD = {
         (dict(K=33), UNSUPPORTED, "K must be 1..32"),
         (dict(W=1, V=3, ld=3, eos=1), INVALID, "K must be <= W*V"),
         (dict(V=2 ** 30, ld=2 ** 30), INVALID, "W*V below 2^31"),
+        (dict(W=1, V=2 ** 31 - 1, ld=2 ** 31), INVALID, "W*V below 2^31"),
         (dict(B=2 ** 28), INVALID, "too large"),
         (dict(ld=99), INVALID, "ld must be >= V"),
         (dict(eos=100), INVALID, "eos must be"),
