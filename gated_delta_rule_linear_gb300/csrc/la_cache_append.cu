@@ -6,6 +6,10 @@
 // A CTA takes up to 8 tokens. Its threads look through the sequences for them
 // once; from there on a token has warps of its own, which form its cosines and
 // sines while the table entry and the rows (asked into L2 first) are on their way.
+//
+// 32768 tokens of 16 + 4 + 4 heads of 128, bfloat16: 68 us, 5.9 TB/s (a CTA's
+// tokens together, with cosines read across banks: 75.7 us); 128 single tokens:
+// 5 us, a chain of four loads from memory and the launch.
 #include <climits>
 #include <type_traits>
 

@@ -3,33 +3,39 @@
 // running maximum and sum (Milakov and Gimelshein, 2018).
 //
 // Bound by reading keys and values once. The heads that share a key/value head
-// are the rows of one block of 8 or 16 (a `part`, of a sequence), so that a place
-// is read once for all of them.
+// are the rows of one block of up to 8 or 16 (a `part` of a sequence), so that a
+// place is read once for all of them.
 //
-// Work. The places of a part are cut into units of four warps' blocks; the units
-// of all parts, one after the other, are dealt to the CTAs in equal runs, however
-// long the sequences are (each CTA adds up the lengths for itself: nothing is
-// known on the host). A CTA's run begins and ends inside a part: what it has of
-// that goes to a workspace, and join_kernel adds the pieces up. Every other part
-// is finished where it was begun.
+// Work. The places of a part are cut into units, a block of keys for each of the
+// CTA's four warps; the units of all parts, one after the other, are dealt to the
+// CTAs in equal runs, however long the sequences are (each CTA adds up the lengths
+// for itself: nothing is known on the host). A CTA's run begins and ends inside a
+// part: what it has of that goes to a workspace, and join_kernel adds the pieces
+// up. Every other part is finished where it was begun.
 //
-// A warp streams its blocks through a ring of stages in shared memory by 16-byte
+// A warp streams its blocks through two stages of shared memory by 16-byte
 // asynchronous copies, across the ends of parts, with no barrier but its own; the
-// CTA's warps meet at the end of a part only.
+// CTA's warps meet at the end of a part only, two handing their sums to the other
+// two.
 //
 // bfloat16: S = Q K^T and O = P V by 16 x 8 x 16 matrix instructions of a warp.
-// With 8 or 16 rows the tensor cores have an eighth of a tile's work, and the
-// operands come straight from the 16-byte rows as they are stored: channels are
-// taken in the order in which a thread holds them, for keys and queries alike. P
-// keeps 16 bits as a high and a low bfloat16 part; with up to 8 heads the low part
-// is in the tile's other 8 rows and costs nothing.
+// With 8 or 16 rows the tensor cores have an eighth of a tile's work (112 of the
+// 128 rows of a tcgen05 product would be empty), and the operands come straight from
+// the 16-byte rows as they are stored: channels are taken in the order in which a
+// thread holds them, for keys and queries alike. P keeps 16 bits as a high and a
+// low bfloat16 part; with up to 8 heads the low part is in the tile's other 8 rows
+// and costs nothing. float32: CUDA cores, see F32Warp.
 //
-// float32: CUDA cores, see F32Warp.
+// 64 sequences of 16384 places, 32/8 heads of 128, bfloat16: 611 us, 7.0 TB/s. Two
+// of 131072, 16/2 heads: 50 us of 40; what is not reading is the launch, the way
+// lengths -> table -> first keys (3.7 us) and the pieces' join (3 us). 16 heads a
+// block are bound by instructions (32/2 heads of 128: 4.7 TB/s; the low part of P
+// is a second product there), 8 heads in float32 too (3.8 to 5.8 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <climits>
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "la_f32x2.cuh"
@@ -61,6 +67,7 @@ template <typename T, int D, int HB> struct Shape {
 };
 
 // What a part costs besides its units, in units: its queries, and the meeting of the warps at its end.
+// (128 ragged sequences: 0 49.8 us, 1 43.4, 2 43.7.)
 constexpr int kPartCost = 1;
 
 // What the CTAs of a call share: rows of a part, pieces of parts in the workspace.
@@ -69,7 +76,6 @@ struct Split {
   int parts;       // parts of a sequence: Hk * blocks
   int lines;       // 128-byte lines of a table row that are asked for ahead
   int whole;       // a CTA takes one whole part: no pieces, no workspace
-  int least;       // least units of a run
   float *sums;     // [2 * CTAs][HB][D]
   float2 *ml;      // [2 * CTAs][HB]: maximum (of log2) and sum
   int4 *joins;     // sequence, part, first and last CTA with a piece of it; sequence -1: none
@@ -554,7 +560,8 @@ attn_kernel(const PagedAttn p, const Split sp, const FastDiv by_page) {
       if (w < warp) upto += scan[w];
       total += scan[w];
     }
-    share = max((total + gridDim.x - 1) / gridDim.x, (unsigned)sp.least);
+    // (runs of one unit too: one sequence of 4096 places, 16/4 heads of 128, 10.2 us; of 2 units at least 10.9, 4 12.4)
+    share = max((total + gridDim.x - 1) / gridDim.x, 1u);
     t0 = min((long long)blockIdx.x * share, (long long)total);
     t1 = min(t0 + share, total);
     if (t0 < t1) {
@@ -789,9 +796,6 @@ int fail(const char *what, cudaError_t e) {
   return LA_ERR_CUDA;
 }
 
-// Least units of a run: parts of a few units are still spread over the SMs (one sequence of 4096 places, 16/4 heads of
-// 128: 1 unit 10.2 us, 2 10.9, 4 12.4).
-constexpr int kLeast = 1;
 // Units up to which a part is one CTA's, which saves the second kernel; and where there are parts for half of the CTAs
 // or more. (16/4 heads of 128, bfloat16, whole and split: 16 x 384 places 9.6 and 12.7 us, 1 x 384 9.1 and 8.9,
 // 1 x 512 10.7 and 9.1; 64 x 384 12.2 and 16.8, 64 x 768 21.9 and 26.3.)
@@ -813,7 +817,6 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
   Split sp = {};
   sp.blocks = (p.H / p.Hk + HB - 1) / HB;
   sp.parts = p.Hk * sp.blocks;
-  sp.least = kLeast;
   const long long most = (long long)p.at.max_pages * p.at.page_size;
   long long longest = p.max_len > 0 ? std::min<long long>(p.max_len, most) : most;
   if (p.window > 0) longest = std::min<long long>(longest, p.window);
@@ -829,7 +832,7 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
     return LA_ERR_INVALID_ARG;
   }
   const long long units = ((longest + S::kUnit - 1) / S::kUnit + kPartCost) * parts;
-  const int ctas = static_cast<int>(std::min(slots, (units + kLeast - 1) / kLeast));
+  const int ctas = static_cast<int>(std::min(slots, units));
   // (of longer rows a part)
   sp.lines = static_cast<int>(std::min<long long>(((longest - 1) / p.at.page_size + 32) / 32, 64));
   if ((long long)sp.lines * p.n > INT_MAX / 2) sp.lines = 0;
