@@ -29,7 +29,7 @@
 // 64 sequences of 16384 places, 32/8 heads of 128, bfloat16: 611 us, 7.0 TB/s. Two
 // of 131072, 16/2 heads: 50 us of 40; what is not reading is the launch, the way
 // lengths -> table -> first keys (3.7 us) and the pieces' join (3 us). 16 heads a
-// block are bound by instructions (32/2 heads of 128: 4.7 TB/s; the low part of P
+// block are bound by instructions (32/2 heads of 128: 5.0 TB/s; the low part of P
 // is a second product there), 8 heads in float32 too (3.8 to 5.8 TB/s).
 #include <cuda_bf16.h>
 
@@ -849,8 +849,10 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
   sp.ml = reinterpret_cast<float2 *>(ws + sums);
   sp.joins = reinterpret_cast<int4 *>(ws + sums + ml);
   e = launch_early(kernel, dim3(ctas), kThreads, S::kBytes, stream, p, sp, by);
+  unsigned apart = 1;  // blocks of a part's heads: up to two for each SM (64 parts of 16 heads, the call: 4 a part 53 us, 16 57)
+  while (2 * apart <= HB && 2 * apart * entries <= 2 * (size_t)std::max(sm_count(), 1)) apart *= 2;
   if (e == cudaSuccess)
-    e = launch_early(join_kernel<T, D, HB>, dim3(static_cast<unsigned>(entries), parts <= 64 ? HB : 1), kJoinThreads, 0, stream, p, sp);
+    e = launch_early(join_kernel<T, D, HB>, dim3(static_cast<unsigned>(entries), apart), kJoinThreads, 0, stream, p, sp);
   const cudaError_t f = cudaFreeAsync(ws, stream);
   if (e == cudaSuccess) e = f;
   return e == cudaSuccess ? LA_OK : fail("launch failed", e);
