@@ -13,9 +13,9 @@
 // index together, so that the order is right for equal logits (bfloat16 has
 // many). Warps do not wait for one another.
 //
-// The sum. exp(x - r) with one reference r for a part, its first largest value:
-// a floating-point sum may grow above one. In pairs inside a lane's 16 bytes, in
-// two float32 across lanes. Which elements meet in which order depends on their
+// The sum. exp(x - r) with the largest value so far as the reference r (an
+// exponent is rounded to 2^-24 of itself: of those that count, none may be
+// large). In pairs inside a lane's 16 bytes, in two float32 across lanes. Which elements meet in which order depends on their
 // index alone, not on where a row lies, so that two beams with the same logits get
 // the same sum; rows that do not start at 16 bytes are shifted into place for this.
 //
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const BeamSelect p, int 
     if (isnan(m)) m = INFINITY;
     top = fmaxf(top, m);
     const float high = unordered(__reduce_max_sync(~0u, ordered(m + 0.f)));  // (+ 0: one zero)
-    if (high > ref + 64.f || ref == -INFINITY) {  // the first value; later only where the sum could overflow
+    if (high > ref) {
       sum = mul2(sum, high < INFINITY && ref > -INFINITY ? expf(ref - high) : 0.f);
       ref = high;
     }

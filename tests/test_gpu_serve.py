@@ -380,6 +380,16 @@ def test_select_masks_of_the_lowest_value(dtype):
     check_select(logits, scores, 6)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_select_values_that_grow_along_the_row(dtype):
+    """Sums whose later terms are far above the first ones, in every part of a row."""
+    for V in (700, 2048, 13144):
+        logits, scores = select_case(2, 4, V, 8, dtype, V)
+        for period in (2, 128, 256, 1024):
+            rising = (30.0 * ((torch.arange(V) // period) % 2)).to(dtype)
+            check_select((logits + rising).to(dtype), scores, 8)
+
+
 def test_select_rows_at_every_alignment():
     """Vocabularies and strides that put rows at any offset from 16 bytes; rows that are alike tie."""
     for dtype in (BF, F32):
