@@ -15,9 +15,10 @@
 //
 // The sum. exp(x - r) with the largest value so far as the reference r (an
 // exponent is rounded to 2^-24 of itself: of those that count, none may be
-// large). In pairs inside a lane's 16 bytes, in two float32 across lanes. Which elements meet in which order depends on their
-// index alone, not on where a row lies, so that two beams with the same logits get
-// the same sum; rows that do not start at 16 bytes are shifted into place for this.
+// large). In pairs inside a lane's 16 bytes, in two float32 across lanes. Which
+// elements meet in which order depends on their index alone, not on where a row
+// lies, so that two beams with the same logits get the same sum; rows that do not
+// start at 16 bytes are shifted into place for this.
 //
 // Code. Both kernels are short, and what they run once or twice is rolled up:
 // fetching straight-line code takes longer than running it (with all sorts
@@ -88,7 +89,8 @@ __device__ __forceinline__ Word sorted(Word k, int lane) {
   return k;
 }
 // The 32 largest of two such lists, as one.
-__device__ __forceinline__ u64 merged(u64 a, u64 b, int lane) {
+template <typename Word>
+__device__ __forceinline__ Word merged(Word a, Word b, int lane) {
   a = max(a, __shfl_xor_sync(~0u, b, 31));
 #pragma unroll 1
   for (int j = 16; j > 0; j /= 2) a = exchange(a, j, (lane & j) == 0);
@@ -343,15 +345,15 @@ __device__ __forceinline__ double log_of(float2 x) {
 }
 
 constexpr int kSelectThreads = 256, kSelectWarps = kSelectThreads / 32;
-constexpr int kList = 256;  // parts and candidates that the bound may leave
+constexpr int kList = 256;   // parts and candidates that the bound may leave
 
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect p, int parts, const FastDiv by_parts,
-                                                                const FastDiv by_K, const FastDiv by_V, const Part *part,
+                                                                const FastDiv by_K, const FastDiv by_V, Part *part,
                                                                 const u64 *keys) {
   __shared__ double logs[kMaxBeams];  // of each beam's sum of exp(x - top)
   __shared__ float tops[kMaxBeams];
   __shared__ float base[kMaxBeams];   // about score - log; NaN: its candidates have no value, infinity: it has ended
-  __shared__ float bounds[kSelectWarps];
+  __shared__ unsigned heads[kSelectThreads];
   __shared__ Candidate list[kList];
   __shared__ int passed[kList];
   __shared__ int passing, count;
@@ -360,7 +362,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect
   const float *scores = p.scores + b * p.W;
   const int lists = p.W * parts, all = lists * p.K;
   const u64 *mine = keys + (size_t)b * all;
-  const u64 first = tid < lists ? mine[tid * p.K] : 0;  // (that of an ended beam is not used)
+  // Threads look at each list's first candidate, at 2^deep of each when the lists are fewer than the threads.
+  int deep = 0;
+  while (lists << (deep + 1) <= kSelectThreads && 2 << deep <= p.K) ++deep;
+  const int looks = lists << deep, mask = (1 << deep) - 1;
+  const u64 first = tid < looks ? mine[(tid >> deep) * p.K + (tid & mask)] : 0;  // (that of an ended beam is not used)
 #pragma unroll 1
   for (int w = warp; w < p.W; w += kSelectWarps) {
     const Part *s = part + (size_t)(b * p.W + w) * parts;
@@ -411,34 +417,45 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect
     const double x = (double)scores[w] + (((double)unordered(static_cast<unsigned>(k >> 32)) - tops[w]) - logs[w]);
     return {ordered(x), ~(first + ~static_cast<unsigned>(k))};
   };
-  // As in a part: the K-th largest of a warp's lanes bounds what can be among the K best. Lanes take the parts' first
-  // candidates; all in float32, with what that may be off taken from the bound.
+  // As in a part: the K-th largest of the threads' bounds what can be among the K best, and so does that of a warp's. For few
+  // the best of the warps' is near enough (1 x 4: 9.5 us, with all threads' 10.2); for many it leaves most candidates (2 x 16
+  // rows of 27787, 32 of each: 65 us, with all threads' 27). All in float32, with what that may be off taken from the bound.
   float head = -INFINITY;
   bool any = false;
 #pragma unroll 1
-  for (int i = tid; i < lists; i += kSelectThreads) {
+  for (int i = tid; i < looks; i += kSelectThreads) {
     unsigned w, j;
-    by_parts.split(i, w, j);
-    const float c = rough(w, j * p.K, i == tid ? first : mine[i * p.K]);
+    by_parts.split(i >> deep, w, j);
+    const float c = rough(w, j * p.K + (i & mask), i == tid ? first : mine[i * p.K]);
     if (!isnan(c)) head = fmaxf(head, c), any = true;
   }
-  const unsigned order = sorted(any ? ordered(head) : 0u, lane);
-  if (lane == p.K - 1) bounds[warp] = order ? unordered(order) : -INFINITY;
+  unsigned order = sorted(any ? ordered(head) : 0u, lane);
+  heads[tid] = order;
   __syncthreads();
-  float low = bounds[0], size = 0.f;
+  unsigned bound = 0;
+  if (p.K <= 8) {
 #pragma unroll
-  for (int i = 1; i < kSelectWarps; ++i) low = fmaxf(low, bounds[i]);
+    for (int i = 0; i < kSelectWarps; ++i) bound = max(bound, heads[i * 32 + p.K - 1]);
+  } else {  // the 32 best of two warps, until one has those of all
+#pragma unroll 1
+    for (int half = kSelectWarps / 2; half > 0; half /= 2) {
+      if (warp < half) heads[tid] = order = merged(order, heads[tid + half * 32], lane);
+      __syncthreads();
+    }
+    bound = heads[p.K - 1];
+  }
+  float low = bound ? unordered(bound) : -INFINITY, size = 0.f;
   if (lane < p.W && isfinite(base[lane])) size = fabsf(base[lane]);
   size = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(size)));
   low -= 1e-6f * (fabsf(low) + size);  // (three roundings of up to 2^-24)
   // the parts whose first candidate passes, then their candidates that pass
 #pragma unroll 1
-  for (int i = tid; i < lists; i += kSelectThreads) {
+  for (int i = tid; i < looks; i += kSelectThreads) {
     unsigned w, j;
-    by_parts.split(i, w, j);
-    if (!(rough(w, j * p.K, i == tid ? first : mine[i * p.K]) >= low)) continue;
+    by_parts.split(i >> deep, w, j);
+    if (i & mask || !(rough(w, j * p.K, i == tid ? first : mine[i * p.K]) >= low)) continue;
     const int n = atomicAdd(&passing, 1);
-    if (n < kList) passed[n] = i;
+    if (n < kList) passed[n] = i >> deep;
   }
   __syncthreads();
   const bool few = passing <= kList;
@@ -475,35 +492,46 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect
     }
     return;
   }
-  // too many that are equal: the next one below the last, K times
-  Candidate last = {~0ull, ~0u};
+  // Too many that are equal, or fewer than K with a value among those looked at: the parts' lists fall, so they are joined,
+  // each thread with the best of its parts' next ones. How many a part has given stands in its record, whose sums are used.
+  Part *mark = part + (size_t)b * lists;
+#pragma unroll 1
+  for (int i = tid; i < lists; i += kSelectThreads) mark[i].bad = 0;
+  Candidate best = {0, 0};
+  int from = -1;
+  bool look = true;
 #pragma unroll 1
   for (int r = 0; r < p.K; ++r) {
-    Candidate best = {0, 0};
+    if (look) {
+      best = {0, 0};
 #pragma unroll 1
-    for (int i = tid; i < all; i += kSelectThreads) {
-      unsigned l, w, j, at;
-      by_K.split(i, l, at);
-      by_parts.split(l, w, j);
-      at += j * p.K;
-      const u64 k = mine[i];
-      if (isnan(rough(w, at, k))) continue;
-      const Candidate o = candidate(w, at, k);
-      if (above(last, o) && above(o, best)) best = o;
+      for (int i = tid; i < lists; i += kSelectThreads) {
+        unsigned w, j;
+        by_parts.split(i, w, j);
+        const int next = mark[i].bad;
+        if (next == p.K) continue;
+        const u64 k = mine[i * p.K + next];
+        if (isnan(rough(w, j * p.K + next, k))) continue;
+        const Candidate o = candidate(w, j * p.K + next, k);
+        if (above(o, best)) best = o, from = i;
+      }
     }
+    Candidate top = best;
 #pragma unroll 1
     for (int d = 16; d > 0; d /= 2) {
-      const Candidate o = {__shfl_xor_sync(~0u, best.score, d), __shfl_xor_sync(~0u, best.rank, d)};
-      if (above(o, best)) best = o;
+      const Candidate o = {__shfl_xor_sync(~0u, top.score, d), __shfl_xor_sync(~0u, top.rank, d)};
+      if (above(o, top)) top = o;
     }
     __syncthreads();
-    if (lane == 0) list[warp] = best;
+    if (lane == 0) list[warp] = top;
     __syncthreads();
-    last = list[0];
+    top = list[0];
 #pragma unroll 1
     for (int i = 1; i < kSelectWarps; ++i)
-      if (above(list[i], last)) last = list[i];
-    if (tid == 0) put(r, last);
+      if (above(list[i], top)) top = list[i];
+    look = top.rank == best.rank && from >= 0;
+    if (look) ++mark[from].bad;
+    if (tid == 0) put(r, top);
   }
 }
 

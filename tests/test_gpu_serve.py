@@ -359,6 +359,18 @@ def test_select_ties():
             assert torch.equal(parent.cpu(), want[1]) and torch.equal(token.cpu(), want[2])
 
 
+def test_select_first_step():
+    """One beam with a score and the others without: all K from its row, of few parts or many; fewer tokens than K."""
+    for W, V, K in ((4, 700, 32), (16, 2129, 32), (16, 20011, 16), (32, 5003, 32)):
+        for dtype in (BF, F32):
+            logits, scores = select_case(2, W, V, K, dtype, V + W)
+            scores[:, 0] = 0.0
+            scores[:, 1:] = -INF
+            check_select(logits, scores, K)
+            logits[1, :, 5:] = -INF
+            check_select(logits, scores, K)
+
+
 def test_select_rising_and_falling_rows():
     """Orders that put all of a row's best in one place."""
     for V in (4096, 20000):
