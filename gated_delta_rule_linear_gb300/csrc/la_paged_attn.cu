@@ -798,8 +798,11 @@ int fail(const char *what, cudaError_t e) {
 
 // Units up to which a part is one CTA's, which saves the second kernel; and where there are parts for half of the CTAs
 // or more. (16/4 heads of 128, bfloat16, whole and split: 16 x 384 places 9.6 and 12.7 us, 1 x 384 9.1 and 8.9,
-// 1 x 512 10.7 and 9.1; 64 x 384 12.2 and 16.8, 64 x 768 21.9 and 26.3.)
-constexpr int kWhole = 6, kWholeOfMany = 16;
+// 1 x 512 10.7 and 9.1; 64 x 384 12.2 and 16.8, 64 x 768 21.9 and 26.3.) Where few CTAs of bfloat16 fit on a SM and there
+// are several parts for each, a run is better again, as one part's keys come while the one before ends (126 x 200 places,
+// 32/32 heads of 128: 94 and 83 us, of 256 220 and 193; 126 x 64 of 256 114 and 82; 126 x 400, 16/8 of 128 46.5 and 44.2;
+// heads of 64: 126 x 400 77 and 80; float32, 126 x 200 of 128 128 and 150).
+constexpr int kWhole = 6, kWholeOfMany = 16, kManyParts = 3;
 
 template <typename T, int D, int HB>
 int launch(const PagedAttn &p, cudaStream_t stream) {
@@ -821,13 +824,15 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
   long long longest = p.max_len > 0 ? std::min<long long>(p.max_len, most) : most;
   if (p.window > 0) longest = std::min<long long>(longest, p.window);
   const long long parts = (long long)p.n * sp.parts, slots = (long long)S::kCtas * std::max(sm_count(), 1);
-  sp.whole = longest <= (long long)(2 * parts >= slots ? kWholeOfMany : kWhole) * S::kUnit;
+  const bool countable = (most / S::kUnit + 2 + kPartCost) * parts <= INT_MAX;  // all units of the table
+  sp.whole = longest <= (long long)(2 * parts >= slots ? kWholeOfMany : kWhole) * S::kUnit &&
+             (S::kF32 || S::kCtas > 2 || parts < kManyParts * slots || !countable || most == 0);
   const FastDiv by(p.at.page_size);
   if (sp.whole) {
     e = launch_early(kernel, dim3(static_cast<unsigned>(parts)), kThreads, S::kBytes, stream, p, sp, by);
     return e == cudaSuccess ? LA_OK : fail("launch failed", e);
   }
-  if ((most / S::kUnit + 2 + kPartCost) * parts > INT_MAX) {
+  if (!countable) {
     set_error("la_paged_attn: n * Hk times max_pages * page_size too large");
     return LA_ERR_INVALID_ARG;
   }

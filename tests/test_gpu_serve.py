@@ -194,6 +194,24 @@ def test_attn_over_split_lengths(n, Hk, top):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,H,Hk,d,page,window,top", [
+    (130, 16, 8, 128, 16, 0, 70), (130, 8, 8, 256, 20, 0, 40), (130, 16, 8, 128, 64, 9, 200), (200, 16, 8, 128, 16, 0, 1),
+    (70, 32, 32, 64, 16, 0, 90),
+])
+def test_attn_of_many_short_sequences(n, H, Hk, d, page, window, top, dtype):
+    """Several parts for each CTA, of a unit or two, some of the sequences empty; without and with a longest length."""
+    gen = torch.Generator().manual_seed(n + d)
+    lens = torch.randint(0, top + 1, (n,), generator=gen).tolist()
+    lens[0] = lens[-1] = lens[n // 2] = 0
+    lens[1] = top
+    table, pages = ref.make_tables(lens, page, gen)
+    q = rand(gen, n, H, d, dtype=dtype)
+    kc, vc = (rand(gen, pages, page, Hk, d, dtype=dtype) for _ in range(2))
+    check_attn(q, kc, vc, table, lens, window)
+    check_attn(q, kc, vc, table, lens, window, max_len=top)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_attn_leaves_out_what_is_not_there(dtype):
     """Pages outside the pool, lengths behind the table; NaN and infinity behind the length, in front of the window,
     in pages that nobody has, and beside the heads of a page."""
