@@ -824,7 +824,7 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
   long long longest = p.max_len > 0 ? std::min<long long>(p.max_len, most) : most;
   if (p.window > 0) longest = std::min<long long>(longest, p.window);
   const long long parts = (long long)p.n * sp.parts, slots = (long long)S::kCtas * std::max(sm_count(), 1);
-  const bool countable = (most / S::kUnit + 2 + kPartCost) * parts <= INT_MAX;  // all units of the table
+  const bool countable = most / S::kUnit + 2 + kPartCost <= INT_MAX / std::max(parts, 1ll);  // all units of the table
   sp.whole = longest <= (long long)(2 * parts >= slots ? kWholeOfMany : kWhole) * S::kUnit &&
              (S::kF32 || S::kCtas > 2 || parts < kManyParts * slots || !countable || most == 0);
   const FastDiv by(p.at.page_size);
