@@ -73,10 +73,22 @@ __device__ __forceinline__ float unordered(unsigned u) {
   return __int_as_float(b ^ (b >> 31 & 0x7fffffff));
 }
 
+// A candidate: its score in the order of unsigned integers, then the order of w * V + v, reversed. 0, 0: none.
+struct Candidate {
+  u64 score;
+  unsigned rank;  // ~(w * V + v)
+};
+__device__ __forceinline__ bool operator>(const Candidate &a, const Candidate &b) {
+  return a.score > b.score || (a.score == b.score && a.rank > b.rank);
+}
+
+template <typename Word> __device__ __forceinline__ Word of_lane(Word k, int x) { return __shfl_xor_sync(~0u, k, x); }
+__device__ __forceinline__ Candidate of_lane(const Candidate &k, int x) { return {of_lane(k.score, x), of_lane(k.rank, x)}; }
+
 // Bitonic exchange with the lane j away; `top` keeps the larger one.
 template <typename Word>
 __device__ __forceinline__ Word exchange(Word k, int j, bool top) {
-  const Word o = __shfl_xor_sync(~0u, k, j);
+  const Word o = of_lane(k, j);
   return (o > k) == top ? o : k;
 }
 // A warp's keys in descending order over its lanes.
@@ -91,7 +103,8 @@ __device__ __forceinline__ Word sorted(Word k, int lane) {
 // The 32 largest of two such lists, as one.
 template <typename Word>
 __device__ __forceinline__ Word merged(Word a, Word b, int lane) {
-  a = max(a, __shfl_xor_sync(~0u, b, 31));
+  const Word o = of_lane(b, 31);
+  if (o > a) a = o;
 #pragma unroll 1
   for (int j = 16; j > 0; j /= 2) a = exchange(a, j, (lane & j) == 0);
   return a;
@@ -269,8 +282,7 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const BeamSelect p, int 
   }
   // the K-th largest of the lanes': the largest again and again for few (8 best as above: 12.5 us, sorted 12.8)
   float cut;
-  bool bad = false;
-  unsigned order = ordered(top + 0.f);
+  unsigned order = ordered(top + 0.f), high = 0;
   if (p.K <= 8) {
     unsigned m;
 #pragma unroll 1
@@ -279,14 +291,15 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const BeamSelect p, int 
       const bool is = order == m;
       gone += __popc(__ballot_sync(~0u, is));
       if (is) order = 0;
-      bad |= unordered(m) == INFINITY;
+      high = max(high, m);
     }
     cut = unordered(m);
   } else {
     order = sorted(order, lane);
-    bad = unordered(__shfl_sync(~0u, order, 0)) == INFINITY;
+    high = __shfl_sync(~0u, order, 0);
     cut = unordered(__shfl_sync(~0u, order, p.K - 1));
   }
+  const bool bad = unordered(high) == INFINITY;
   int n = 0;  // granules that pass, in the order of their elements
 #pragma unroll 1
   for (int i = 0; i < G && !bad; ++i) {
@@ -321,6 +334,7 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const BeamSelect p, int 
     // what comes now has higher indexes than all this: no use for a value equal to the K-th
     const u64 kth = __shfl_sync(~0u, best, p.K - 1);
     if (kth) cut = fmaxf(cut, unordered(min(static_cast<unsigned>(kth >> 32) + 1, ordered(INFINITY))));
+    if (cut > unordered(high)) break;  // (all equal, or none allowed)
   }
   __syncwarp();
   const u64 mine = lane < count ? c.key[lane] : 0;
@@ -340,14 +354,6 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const BeamSelect p, int 
   if (lane == 0) part[id] = {bad || ref == -INFINITY ? make_float2(0.f, 0.f) : sum, ref, bad};
 }
 
-// A candidate: its score in the order of unsigned integers, then the order of w * V + v, reversed. 0, 0: none.
-struct Candidate {
-  u64 score;
-  unsigned rank;  // ~(w * V + v)
-};
-__device__ __forceinline__ bool above(const Candidate &a, const Candidate &b) {
-  return a.score > b.score || (a.score == b.score && a.rank > b.rank);
-}
 __device__ __forceinline__ u64 ordered(double x) {
   const long long b = __double_as_longlong(x);
   return static_cast<u64>(b ^ (b >> 63 & 0x7fffffffffffffffll)) ^ 0x8000000000000000ull;
@@ -375,10 +381,10 @@ __device__ __forceinline__ double log_of(float2 x) {
 }
 
 constexpr int kSelectThreads = 256, kSelectWarps = kSelectThreads / 32;
-constexpr int kList = 256;   // parts and candidates that the bound may leave
+constexpr int kList = kSelectThreads;  // parts and candidates that the bound may leave
 
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect p, int parts, const FastDiv by_parts,
-                                                                const FastDiv by_K, const FastDiv by_V, Part *part,
+                                                                const FastDiv by_K, const FastDiv by_V, const Part *part,
                                                                 const u64 *keys) {
   __shared__ double logs[kMaxBeams];  // of each beam's sum of exp(x - top)
   __shared__ float tops[kMaxBeams];
@@ -518,54 +524,40 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect
       const int i = min(i0 + tid / 8, n - 1);
       const Candidate k = list[i];
       int r = 0;
-      for (int o = tid % 8; o < n; o += 8) r += above(list[o], k);
+      for (int o = tid % 8; o < n; o += 8) r += list[o] > k;
 #pragma unroll
       for (int d = 4; d > 0; d /= 2) r += __shfl_xor_sync(~0u, r, d);
       if (tid % 8 == 0 && i0 + tid / 8 < n && r < p.K) put(r, k);
     }
     return;
   }
-  // Too many that are equal, or fewer than K with a value among those looked at: the parts' lists fall, so they are joined,
-  // each thread with the best of its parts' next ones. How many a part has given stands in its record, whose sums are used.
-  Part *mark = part + (size_t)b * lists;
-#pragma unroll 1
-  for (int i = tid; i < lists; i += kSelectThreads) mark[i].bad = 0;
+  // Too many that are equal, or fewer than K with a value among those looked at: warps keep the best 32 that they meet, in
+  // order, and are joined two by two. (2 x 16 bfloat16 rows of 50257 zeros, 32 best: 48 us for both
+  // kernels; one more candidate of the falling lists at a time 82.)
   Candidate best = {0, 0};
-  int from = -1;
-  bool next_one = true;
+  u64 next = tid < all ? mine[tid] : 0;
 #pragma unroll 1
-  for (int r = 0; r < p.K; ++r) {
-    if (next_one) {
-      best = {0, 0};
-#pragma unroll 1
-      for (int i = tid; i < lists; i += kSelectThreads) {
-        unsigned w, j;
-        by_parts.split(i, w, j);
-        const int next = mark[i].bad;
-        if (next == p.K) continue;
-        const u64 k = mine[i * p.K + next];
-        if (isnan(rough(w, j * p.K + next, k))) continue;
-        const Candidate o = candidate(w, j * p.K + next, k);
-        if (above(o, best)) best = o, from = i;
-      }
+  for (int i = tid; i - lane < all; i += kSelectThreads) {
+    Candidate o = {0, 0};
+    const u64 k = next;
+    if (i + kSelectThreads < all) next = mine[i + kSelectThreads];
+    if (i < all) {
+      unsigned l, r, w, j;
+      by_K.split(i, l, r);
+      by_parts.split(l, w, j);
+      if (rough(w, j * p.K + r, k) >= low) o = candidate(w, j * p.K + r, k);
     }
-    Candidate top = best;
-#pragma unroll 1
-    for (int d = 16; d > 0; d /= 2) {
-      const Candidate o = {__shfl_xor_sync(~0u, top.score, d), __shfl_xor_sync(~0u, top.rank, d)};
-      if (above(o, top)) top = o;
-    }
-    __syncthreads();
-    if (lane == 0) list[warp] = top;
-    __syncthreads();
-    top = list[0];
-#pragma unroll 1
-    for (int i = 1; i < kSelectWarps; ++i)
-      if (above(list[i], top)) top = list[i];
-    next_one = top.rank == best.rank && from >= 0;
-    if (next_one) ++mark[from].bad;
-    if (tid == 0) put(r, top);
+    const Candidate last = {__shfl_sync(~0u, best.score, p.K - 1), __shfl_sync(~0u, best.rank, p.K - 1)};
+    if (__any_sync(~0u, o > last)) best = merged(best, sorted(o, lane), lane);
   }
+#pragma unroll 1
+  for (int half = kSelectWarps / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (warp >= half) list[tid] = best;
+    __syncthreads();
+    if (warp < half) best = merged(best, list[tid + half * 32], lane);
+  }
+  if (tid < p.K) put(tid, best);
 }
 
 // Granules of a lane: few for short rows, so that all SMs have some, but not so few that the second kernel has more than
