@@ -270,9 +270,13 @@ template <int D, int HB> struct Bf16Warp {
     }
   }
 
+  // Rows without a head are left out at a part's end where rows are long (126 x 64 places, 32/32 heads of 256: 82 us with
+  // them, 78 without; heads of 64: 25 and 26).
+  static constexpr bool kSkip = D == 256;
   // The warp's sums to another warp, as they are held.
   static constexpr int kGiven = R;  // maxima and sums of a lane
-  __device__ __forceinline__ void give(float *sums, float2 (*ml)[32], int lane) {
+  __device__ __forceinline__ void give(float *sums, float2 (*ml)[32], int lane, int heads) {
+    if (kSkip && lane >> 2 >= heads) return;
 #pragma unroll
     for (int r = 0; r < R; ++r) ml[r][lane] = make_float2(m[r], l[r]);
 #pragma unroll
@@ -281,7 +285,8 @@ template <int D, int HB> struct Bf16Warp {
       else reinterpret_cast<float4 *>(sums)[i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
     }
   }
-  __device__ __forceinline__ void take(const float *sums, const float2 (*ml)[32], int lane) {
+  __device__ __forceinline__ void take(const float *sums, const float2 (*ml)[32], int lane, int heads) {
+    if (kSkip && lane >> 2 >= heads) return;
     float f[R], f2[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) meet(m[r], l[r], ml[r][lane].x, ml[r][lane].y, f[r], f2[r]);
@@ -302,12 +307,13 @@ template <int D, int HB> struct Bf16Warp {
     }
   }
   // The warp's sums into [HB][D] and [HB] of shared memory.
-  __device__ __forceinline__ void end(float *sums, float2 *ml, int lane) {
+  __device__ __forceinline__ void end(float *sums, float2 *ml, int lane, int heads) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      if (kSkip && g + 8 * r >= heads) continue;
       if (t == 0) ml[g + 8 * r] = make_float2(m[r], l[r]);
       float4 *row = reinterpret_cast<float4 *>(sums + (g + 8 * r) * D);
 #pragma unroll
@@ -449,7 +455,7 @@ template <int D, int HB> struct F32Warp {
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[h][j][e] += __shfl_xor_sync(~0u, o[h][j][e], 16);
   }
-  __device__ __forceinline__ void give(float *sums, float2 (*ml)[32], int lane) {
+  __device__ __forceinline__ void give(float *sums, float2 (*ml)[32], int lane, int) {
     halves();
     ml[0][lane] = make_float2(m, l);
     if (lane < kLanes)
@@ -459,7 +465,7 @@ template <int D, int HB> struct F32Warp {
         for (int j = 0; j < kPer; ++j)
           reinterpret_cast<float4 *>(sums)[(h * kPer + j) * kLanes + lane] = make_float4(o[h][j][0], o[h][j][1], o[h][j][2], o[h][j][3]);
   }
-  __device__ __forceinline__ void take(const float *sums, const float2 (*ml)[32], int lane) {
+  __device__ __forceinline__ void take(const float *sums, const float2 (*ml)[32], int lane, int) {
     halves();
     float mine, theirs;
     meet(m, l, ml[0][lane].x, ml[0][lane].y, mine, theirs);
@@ -477,7 +483,7 @@ template <int D, int HB> struct F32Warp {
     }
   }
   // (behind take: the rows' halves are together)
-  __device__ __forceinline__ void end(float *sums, float2 *ml, int lane) {
+  __device__ __forceinline__ void end(float *sums, float2 *ml, int lane, int) {
 #pragma unroll
     for (int d = HB; d < 32; d *= 2) l += __shfl_xor_sync(~0u, l, d);
     if (lane < HB) ml[lane] = make_float2(m, l);
@@ -702,17 +708,17 @@ attn_kernel(const PagedAttn p, const Split sp, const FastDiv by_page) {
     fresh = last;
     if (last) {
       // half of the warps hand their sums to the others
-      if (warp >= kHalf) w.give(sums + (warp - kHalf) * HB * D, given[warp - kHalf], lane);
+      if (warp >= kHalf) w.give(sums + (warp - kHalf) * HB * D, given[warp - kHalf], lane, heads);
       __syncthreads();
       if (warp < kHalf) {
-        w.take(sums + warp * HB * D, given[warp], lane);
+        w.take(sums + warp * HB * D, given[warp], lane, heads);
         __syncwarp();
-        w.end(sums + warp * HB * D, ml[warp], lane);
+        w.end(sums + warp * HB * D, ml[warp], lane, heads);
       }
       __syncthreads();
       const int part_end = part_begin + at.units;
       const bool begun = part_begin >= t0, done = part_end <= t1;
-      for (int i = tid; i < HB * (D / 4); i += kThreads) {
+      for (int i = tid; i < heads * (D / 4); i += kThreads) {
         const int h = i / (D / 4), c = i % (D / 4);
         float m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -727,7 +733,7 @@ attn_kernel(const PagedAttn p, const Split sp, const FastDiv by_page) {
           v.x = fmaf(f, a.x, v.x); v.y = fmaf(f, a.y, v.y); v.z = fmaf(f, a.z, v.z); v.w = fmaf(f, a.w, v.w);
         }
         if (begun && done) {
-          if (h < heads) finish<T>(p, at.s, h0 + h, D, c, m, l, v);
+          finish<T>(p, at.s, h0 + h, D, c, m, l, v);
         } else {
           const size_t piece = 2 * (size_t)blockIdx.x + begun;
           reinterpret_cast<float4 *>(sp.sums + (piece * HB + h) * D)[c] = v;
