@@ -43,6 +43,7 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kThreads = 64, kWarps = kThreads / 32;  // of the first kernel
+constexpr int kCoarse = 16;          // up to so many of a part by the lanes' largest values alone
 constexpr float kLog2e = 1.44269504f;
 
 // What the first kernel leaves of a part; its K keys are in an array of their own.
@@ -297,7 +298,23 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const BeamSelect p, int 
   } else {
     order = sorted(order, lane);
     high = __shfl_sync(~0u, order, 0);
-    cut = unordered(__shfl_sync(~0u, order, p.K - 1));
+    unsigned low = __shfl_sync(~0u, order, p.K - 1);
+    // near 32 that is the least of the lanes' and leaves some hundred: from there up by halving while K granules pass (18 x
+    // 16 rows of 43624, 32 best: this kernel 28 us without, 19 with; 18 x 12, 24 best 13.6 and 12.9; 32 x 8 of 50257, 16
+    // best 14.3 and 16; small parts 22 x 16 of 3830, 32 best, the call: 24 and 27)
+#pragma unroll 1
+    for (unsigned up = high; G == 8 && p.K > kCoarse && low < up;) {
+      const unsigned mid = up - (up - low) / 2;
+      const float at = unordered(mid);
+      int pass = 0;
+#pragma unroll
+      for (int i = 0; i < G; ++i) pass += c.most[i * 32 + lane] >= at;
+      pass = __reduce_add_sync(~0u, pass);
+      if (pass >= p.K) low = mid;
+      else up = mid - 1;
+      if (pass >= p.K && pass <= p.K + 4) break;
+    }
+    cut = unordered(low);
   }
   const bool bad = unordered(high) == INFINITY;
   int n = 0;  // granules that pass, in the order of their elements
