@@ -40,8 +40,8 @@ __device__ __forceinline__ void set_moves(Moves &m, int W, int from, long long a
   __syncthreads();
 }
 
-// The rows of `pools` pools, pool(l) their bases, each of n columns of type U; this thread is number `thread` of
-// `threads`.
+// The rows of `pools` pools (one at least), pool(l) their bases, each of n columns of type U; this thread is number
+// `thread` of `threads`.
 template <typename U, int WMAX, typename Pool>
 __device__ __forceinline__ void move_columns(const Moves &m, Pool pool, unsigned pools, unsigned n, unsigned thread,
                                              unsigned threads) {
@@ -131,7 +131,9 @@ cudaError_t states(const BeamStates &p, cudaStream_t stream) {
 
 template <typename U>
 cudaError_t cache(const BeamCache &p, cudaStream_t stream) {
-  const int chunks = chunks_of(2 * p.layers * (p.page_size * p.token_bytes / (long long)sizeof(U)), p.B);
+  // (no layers, or tokens of no bytes: the table alone, as a block of the others would take the first pool for its own)
+  const long long columns = 2 * p.layers * (p.page_size * p.token_bytes / (long long)sizeof(U));
+  const int chunks = columns > 0 ? chunks_of(columns, p.B) : 0;
   const unsigned grid = static_cast<unsigned>(p.B) * (chunks + 1);
   const FastDiv by(p.page_size);
   if (p.W <= 4) return launch_early(cache_kernel<U, 4>, dim3(grid), kThreads, 0, stream, p, by, chunks);

@@ -148,7 +148,8 @@ int la_beam_states(void *pool, const int *slots, const int *parent, int B, int W
  * no counts of references are needed.
  *
  *   k_cache, v_cache  layers x n_pages pages of page_size tokens of token_bytes
- *           bytes: page i of layer l at byte l*ld_layer + i*ld_page of both
+ *           bytes: page i of layer l at byte l*ld_layer + i*ld_page of both;
+ *           layers = 0: the table alone changes, the caches are not used
  *   table   int32 [B*W][max_pages], row stride ld_table: the same for all
  *           layers; changed in place
  *   lens    int32 [B*W]: the tokens in the cache; the beams of a request have

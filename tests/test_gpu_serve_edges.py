@@ -1,0 +1,41 @@
+"""Calls of the serving operators at the edges of what their header allows, on the GPU against float64."""
+import pytest
+import torch
+
+import gated_delta_rule_linear_gb300 as la
+import servelib as ref
+from test_gpu_serve import BF, ints, rand, some_parents, up
+
+pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------- reordering
+
+@pytest.mark.parametrize("layers", [0, 1])
+@pytest.mark.parametrize("token", [0, 128])
+def test_cache_of_no_layers_or_no_bytes(layers, token):
+    """The table follows the parents; caches of no layers, or of tokens without bytes, stay as they are. (One layer of
+    tokens with bytes: the copies of the open pages that the others leave out.)"""
+    gen = torch.Generator().manual_seed(layers + token)
+    B, W, page = 2, 4, 8
+    lens = [5] * W + [21] * W
+    table, pages = ref.make_tables([x + 1 for x in lens], page, gen)
+    parent = some_parents(gen, B, W)
+    kc, vc = (rand(gen, 1, pages, page, 1, 64, dtype=BF) for _ in range(2))
+    want_t, want_k, want_v = table.clone(), kc.clone(), vc.clone()
+    for i, j in enumerate(ref.moved(list(range(B * W)), parent, W)):
+        full, fill = divmod(lens[i], page)
+        want_t[i, :full] = table[j, :full]
+        if layers and token:
+            mine, theirs = int(table[i, full]), int(table[j, full])
+            want_k[:, mine, :fill], want_v[:, mine, :fill] = kc[:, theirs, :fill], vc[:, theirs, :fill]
+    gk, gv, gt, gl, gp = up(kc, vc, table, ints(lens), parent)
+    rc = la.la_beam_cache(gk, gv, gt, gl, gp, B, W, page, pages, table.shape[1], table.shape[1], layers, token, page * 128,
+                          pages * page * 128, torch.cuda.current_stream().cuda_stream)
+    assert rc == la.CONSTANTS["LA_OK"], la.la_last_error()
+    assert torch.equal(gt.cpu(), want_t) and torch.equal(gk.cpu(), want_k) and torch.equal(gv.cpu(), want_v)
+    if layers == 0:
+        none = torch.zeros(0, pages, page, 1, token // 2, dtype=BF, device="cuda")
+        got = table.cuda()
+        la.beam_cache(none, none.clone(), got, gl, gp, layered=True)
+        assert torch.equal(got.cpu(), want_t)
