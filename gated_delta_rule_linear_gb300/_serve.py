@@ -102,7 +102,7 @@ def _inner(t, name, lead):
         if i >= lead:
             if shape[i] > 1 and stride[i] != n:
                 raise ValueError(f"{name}: dimensions {lead} and up must be dense")
-            n *= shape[i]
+            n *= max(shape[i], 1)  # (as torch's strides of empty tensors)
     at = n
     out = []
     for i in range(lead - 1, -1, -1):
