@@ -218,8 +218,10 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const BeamSelect p, int 
     for (int i = lane; i <= 32 * G; i += 32) {
       const char *at = src + i * 16;
       const int there = static_cast<int>(min(max((long long)(end - at), 0ll), 16ll));
-      if (at >= lo) {
-        copy16(c.data + i, there ? at : lo, there);
+      if (there == 0) {  // (no copy of zero bytes: its source would have to be aligned all the same)
+        c.data[i] = make_uint4(0, 0, 0, 0);
+      } else if (at >= lo) {
+        copy16(c.data + i, at, there);
       } else {
 #pragma unroll 1
         for (int e = off / (int)sizeof(T); e * (int)sizeof(T) < there; ++e)

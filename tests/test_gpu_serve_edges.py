@@ -4,9 +4,29 @@ import torch
 
 import gated_delta_rule_linear_gb300 as la
 import servelib as ref
-from test_gpu_serve import BF, ints, rand, some_parents, up
+from layerlib import hold
+from test_gpu_serve import BF, F32, ints, rand, some_parents, up
 
 pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------- selection
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_select_short_rows_at_every_alignment(dtype):
+    """Rows that end in the first 16 bytes of a part or right behind a part, the first one at any element of 16 bytes: all
+    granules behind them are nobody's, and nothing of memory is asked for there."""
+    for first in range(16 // dtype.itemsize):
+        for V in (1, 2, 7, 9, 255, 256, 257, 513):
+            gen = torch.Generator().manual_seed(first + V)
+            flat = (3 * torch.randn(first + 2 * V, generator=gen)).to(dtype)
+            logits, scores, K = flat[first:].view(1, 2, V), torch.tensor([[-1.0, -1.25]]), min(3, 2 * V)
+            c = ref.candidates(logits, scores)
+            assert ref.nearest(c, K) > 1e-5
+            want = ref.selection(c, K)
+            best, parent, token = la.beam_select(flat.cuda()[first:].view(1, 2, V), scores.cuda(), K)
+            assert torch.equal(parent.cpu(), want[1]) and torch.equal(token.cpu(), want[2])
+            hold(best, want[0], ref.select_bound(want[0]), "scores")
 
 
 # -------------------------------------------------------------- reordering
