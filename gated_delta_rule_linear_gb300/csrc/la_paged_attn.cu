@@ -567,9 +567,10 @@ attn_kernel(const PagedAttn p, const Split sp, const FastDiv by_page) {
       total += scan[w];
     }
     // (runs of one unit too: one sequence of 4096 places, 16/4 heads of 128, 10.2 us; of 2 units at least 10.9, 4 12.4)
-    share = max((total + gridDim.x - 1) / gridDim.x, 1u);
-    t0 = min((long long)blockIdx.x * share, (long long)total);
-    t1 = min(t0 + share, total);
+    share = share_of(total, gridDim.x);
+    const UnitRun run = run_of(blockIdx.x, share, total);
+    t0 = run.first;
+    t1 = run.end;
     if (t0 < t1) {
       int before = upto - mine;
       if (before <= t0 && t0 < upto) {

@@ -52,6 +52,19 @@ struct AppendParams {
 };
 int launch_cache_append(const AppendParams &p, cudaStream_t stream);
 
+// The units [first, end) of `total` numbered ones that are a CTA's, `share` to each.
+struct UnitRun {
+  int first, end;
+};
+__host__ __device__ inline int share_of(int total, unsigned ctas) {
+  const unsigned share = (static_cast<unsigned>(total) + ctas - 1) / ctas;
+  return share > 0 ? static_cast<int>(share) : 1;
+}
+__host__ __device__ inline UnitRun run_of(unsigned cta, int share, int total) {
+  const long long first = (long long)cta * share, end = first + share;  // (an int may hold total only)
+  return {static_cast<int>(first < total ? first : total), static_cast<int>(end < total ? end : total)};
+}
+
 struct PagedAttn {
   const void *q, *k_cache, *v_cache;
   void *o;
