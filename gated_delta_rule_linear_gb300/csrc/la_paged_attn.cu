@@ -814,6 +814,19 @@ constexpr int kWhole = 6, kWholeOfMany = 16, kManyParts = 3;
 template <typename T, int D, int HB>
 int launch(const PagedAttn &p, cudaStream_t stream) {
   using S = Shape<T, D, HB>;
+  Split sp = {};
+  sp.blocks = (p.H / p.Hk + HB - 1) / HB;
+  sp.parts = p.Hk * sp.blocks;
+  const long long most = std::min((long long)p.at.max_pages * p.at.page_size, (long long)kMostPlaces);
+  long long longest = p.max_len > 0 ? std::min<long long>(p.max_len, most) : most;
+  if (p.window > 0) longest = std::min<long long>(longest, p.window);
+  const long long parts = (long long)p.n * sp.parts;
+  // all units of the table, whatever max_len says; where an int does not hold them, short lengths take whole parts
+  const bool countable = most / S::kUnit + 2 + kPartCost <= INT_MAX / std::max(parts, 1ll);
+  if (!countable && longest > (long long)kWholeOfMany * S::kUnit) {
+    set_error("la_paged_attn: n * Hk times max_pages * page_size too large");
+    return LA_ERR_INVALID_ARG;
+  }
   auto kernel = attn_kernel<T, D, HB>;
   static std::atomic<bool> ready[64];  // once for each device
   int dev = 0;
@@ -824,24 +837,14 @@ int launch(const PagedAttn &p, cudaStream_t stream) {
     if (e != cudaSuccess) return fail("shared memory", e);
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
-  Split sp = {};
-  sp.blocks = (p.H / p.Hk + HB - 1) / HB;
-  sp.parts = p.Hk * sp.blocks;
-  const long long most = (long long)p.at.max_pages * p.at.page_size;
-  long long longest = p.max_len > 0 ? std::min<long long>(p.max_len, most) : most;
-  if (p.window > 0) longest = std::min<long long>(longest, p.window);
-  const long long parts = (long long)p.n * sp.parts, slots = (long long)S::kCtas * std::max(sm_count(), 1);
-  const bool countable = most / S::kUnit + 2 + kPartCost <= INT_MAX / std::max(parts, 1ll);  // all units of the table
-  sp.whole = longest <= (long long)(2 * parts >= slots ? kWholeOfMany : kWhole) * S::kUnit &&
-             (S::kF32 || S::kCtas > 2 || parts < kManyParts * slots || !countable || most == 0);
+  const long long slots = (long long)S::kCtas * std::max(sm_count(), 1);
+  sp.whole = !countable || most == 0 ||
+             (longest <= (long long)(2 * parts >= slots ? kWholeOfMany : kWhole) * S::kUnit &&
+              (S::kF32 || S::kCtas > 2 || parts < kManyParts * slots));
   const FastDiv by(p.at.page_size);
   if (sp.whole) {
     e = launch_early(kernel, dim3(static_cast<unsigned>(parts)), kThreads, S::kBytes, stream, p, sp, by);
     return e == cudaSuccess ? LA_OK : fail("launch failed", e);
-  }
-  if (!countable) {
-    set_error("la_paged_attn: n * Hk times max_pages * page_size too large");
-    return LA_ERR_INVALID_ARG;
   }
   const long long units = ((longest + S::kUnit - 1) / S::kUnit + kPartCost) * parts;
   const int ctas = static_cast<int>(std::min(slots, units));

@@ -82,11 +82,12 @@ int la_cache_append(const void *q, const void *k, const void *v, void *q_out, vo
  *   flags   LA_F32 (float32 q, o, caches) or 0 (bfloat16)
  *   q, o, k_cache, v_cache 16-byte aligned; ldq, ld_page multiples of 16 bytes
  *
- * n*Hk*max_pages*page_size is below 2^36 (with more than 16 heads for each of
- * Hk, H/16 counts in its place). Workspace from the library's pool where the
- * length may be split: up to about 6 MB. What the cache holds behind a
- * sequence's length, or in front of its window, is not used, whatever it is;
- * inside it, inputs are finite.
+ * n*Hk*ceil(H/Hk / R)*max_pages*page_size is below 2^36 with R = 16 in
+ * bfloat16, below 2^35 with R = 8 in float32 (2^34 with d = 256); of
+ * max_pages*page_size, 2^31 - 2^16 at most count. Larger tables may be refused.
+ * Workspace from the library's pool where the length may be split: up to about
+ * 6 MB. What the cache holds behind a sequence's length, or in front of its
+ * window, is not used, whatever it is; inside it, inputs are finite.
  */
 int la_paged_attn(const void *q, const void *k_cache, const void *v_cache, void *o, float *lse, const int *table,
                   const int *lens, int n, int H, int Hk, int d, int page_size, int n_pages, int max_pages,

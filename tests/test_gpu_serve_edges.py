@@ -10,6 +10,29 @@ from test_gpu_serve import BF, F32, ints, rand, some_parents, up
 pytestmark = pytest.mark.gpu
 
 
+# --------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("n,H,Hk,d,dtype,pages,length", [
+    # just below 2^36 (bfloat16), 2^35 and 2^34 (float32) places of all parts
+    (31, 1, 1, 64, BF, 2047, 70), (4, 32, 2, 128, BF, 2047, 900), (2, 96, 2, 256, BF, 2047, 5),
+    (15, 4, 1, 128, F32, 2047, 3000), (7, 4, 1, 256, F32, 2047, 40), (7, 8, 1, 256, F32, 2047, 400),
+    (3, 16, 1, 256, F32, 2047, 40),
+    # of larger tables no more than 2^31 - 2^16 places of a sequence count
+    (1, 4, 2, 128, BF, 1 << 20, 2 ** 31 - 1), (2, 8, 1, 256, F32, 1 << 20, 700),
+])
+def test_attn_of_the_largest_tables(n, H, Hk, d, dtype, pages, length):
+    """Tables of pages that are not there (of 2^20 places each), as large as the header allows them: no place, no result."""
+    page = 1 << 20
+    q = torch.ones(n, H, d, dtype=dtype, device="cuda")
+    o, lse = torch.full_like(q, 7.0), torch.full((n, H), 7.0, device="cuda")
+    table = torch.full((n, pages), -1, dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), length, dtype=torch.int32, device="cuda")
+    rc = la.la_paged_attn(q, None, None, o, lse, table, lens, n, H, Hk, d, page, 0, pages, pages, 0, 0, 0.125, H * d,
+                          page * Hk * d, la.LA_F32 if dtype is F32 else 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == la.CONSTANTS["LA_OK"], la.la_last_error()
+    assert torch.equal(o, torch.zeros_like(o)) and bool((lse == -ref.INF).all())
+
+
 # --------------------------------------------------------------- selection
 
 @pytest.mark.parametrize("dtype", [BF, F32])
