@@ -503,9 +503,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect
     bound = heads[p.K - 1];
   }
   float low = bound ? unordered(bound) : -INFINITY, size = 0.f;
-  if (lane < p.W && isfinite(base[lane])) size = fabsf(base[lane]);
+  if (lane < p.W && isfinite(base[lane])) size = fabsf(base[lane]) + fabsf(static_cast<float>(logs[lane]));
   size = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(size)));
-  low -= 1e-6f * (fabsf(low) + size);  // (three roundings of up to 2^-24)
+  // 2^-24 each of the log, of base, of x - top (|base| + |low| at most) and of their sum, for the bound and for what it is held
+  // against: below 2^-22 (|low| + |base| + log). (base alone is not enough: it is small where a score is near the log.)
+  low -= 1e-6f * (fabsf(low) + size);
   // the parts whose first candidate passes, then their candidates that pass
 #pragma unroll 1
   for (int i = tid; i < looks; i += kSelectThreads) {

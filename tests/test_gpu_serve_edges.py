@@ -1,4 +1,6 @@
 """Calls of the serving operators at the edges of what their header allows, on the GPU against float64."""
+import math
+
 import pytest
 import torch
 
@@ -50,6 +52,24 @@ def test_select_short_rows_at_every_alignment(dtype):
             best, parent, token = la.beam_select(flat.cuda()[first:].view(1, 2, V), scores.cuda(), K)
             assert torch.equal(parent.cpu(), want[1]) and torch.equal(token.cpu(), want[2])
             hold(best, want[0], ref.select_bound(want[0]), "scores")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [702, 5029, 33012])
+def test_select_scores_about_the_log_of_the_sum(V, dtype):
+    """A beam of V equal logits whose score is log V rounded up in float32, against one that has ended: its best is what the
+    rounding added, 2.2e-7 to 4.4e-7, the other's 0.45 or 1.55 times that. The sum is V, its log good to 1e-8."""
+    gain = float(torch.tensor(math.log(V))) - math.log(V)
+    assert 2e-7 < gain < 4.5e-7
+    logits = torch.zeros(1, 2, V, dtype=dtype).cuda()
+    for live in (0, 1):
+        for other in (0.45 * gain, 1.55 * gain):
+            scores, done = torch.full((1, 2), other), torch.ones(1, 2, dtype=torch.bool)
+            scores[0, live], done[0, live] = math.log(V), False
+            best, parent, token = la.beam_select(logits, scores.cuda(), 1, done=done.cuda(), eos=V // 2)
+            want = (live, 0, gain) if other < gain else (1 - live, V // 2, other)
+            assert (int(parent), int(token)) == want[:2]
+            assert abs(float(best) - want[2]) < 1e-8
 
 
 # -------------------------------------------------------------- reordering
