@@ -72,6 +72,26 @@ def test_select_scores_about_the_log_of_the_sum(V, dtype):
             assert abs(float(best) - want[2]) < 1e-8
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [700, 5003, 50257, 160001])
+def test_select_sums_of_one_large_and_many_equal_logits(V, dtype):
+    """Roundings that are the same in every term, and do not average out. A term is off by 2^-22 (its exponential) and, at a
+    distance a below the largest, by a (2^-23 + 2^-26): the difference, its product with log2 e and that constant. It is
+    scaled to the row's largest once at most (expf, 2^-22), and summed in pairs over six levels of 2^-24; the score is
+    rounded once."""
+    gen = torch.Generator().manual_seed(V)
+    rows = torch.linspace(4.9, 10.6, 24).to(dtype)
+    logits = (-rows)[None, :, None].expand(1, -1, V).clone()
+    at = torch.randint(0, V, (24,), generator=gen)
+    logits[0, torch.arange(24), at] = 0.0
+    a = rows.double()
+    want = -torch.log1p((V - 1) * torch.exp(-a))
+    bound = 2.0 ** -22 * 3.5 + a * (2.0 ** -23 + 2.0 ** -26) + 2.0 ** -24 * want.abs() + 1e-8
+    best, parent, token = la.beam_select(logits[0][:, None].contiguous().cuda(), torch.zeros(24, 1).cuda(), 1)
+    assert torch.equal(token.cpu()[:, 0], at.int()) and not bool(parent.any())
+    hold(best[:, 0], want, bound, "scores")
+
+
 # -------------------------------------------------------------- reordering
 
 @pytest.mark.parametrize("layers", [0, 1])
