@@ -95,23 +95,22 @@ def _handle(idx, stream):
 
 
 def _inner(t, name, lead):
-    """Strides of t's first ``lead`` dimensions; the others must be dense, and rows must not overlap."""
+    """Strides of t's first ``lead`` dimensions, one inside the other in any order; the others must be dense, and rows
+    must not overlap."""
     shape, stride = t.shape, t.stride()
     n = 1
-    for i in range(t.dim() - 1, -1, -1):
-        if i >= lead:
-            if shape[i] > 1 and stride[i] != n:
-                raise ValueError(f"{name}: dimensions {lead} and up must be dense")
-            n *= max(shape[i], 1)  # (as torch's strides of empty tensors)
-    at = n
-    out = []
-    for i in range(lead - 1, -1, -1):
-        s = stride[i] if shape[i] > 1 else max(stride[i], at)
-        if s < at:
-            raise ValueError(f"{name}: dimension {i} overlaps itself or the next")
-        out.append(s)
-        at = s * max(shape[i], 1)
-    return tuple(out[::-1])
+    for i in range(t.dim() - 1, lead - 1, -1):
+        if shape[i] > 1 and stride[i] != n:
+            raise ValueError(f"{name}: dimensions {lead} and up must be dense")
+        n *= max(shape[i], 1)  # (as torch's strides of empty tensors)
+    out = [n] * lead
+    end = n  # elements that the dimensions inside reach over
+    for s, i in sorted((stride[i], i) for i in range(lead) if shape[i] > 1):
+        if s < end:
+            raise ValueError(f"{name}: rows of dimension {i} overlap")
+        out[i] = s
+        end += s * (shape[i] - 1)
+    return tuple(out)
 
 
 def _caches(k_cache, v_cache, lead, idx, dtype):

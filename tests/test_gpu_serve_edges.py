@@ -122,3 +122,65 @@ def test_cache_of_no_layers_or_no_bytes(layers, token):
         got = table.cuda()
         la.beam_cache(none, none.clone(), got, gl, gp, layered=True)
         assert torch.equal(got.cpu(), want_t)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (F32, 3)])
+@pytest.mark.parametrize("order", ["layers inside pages", "pages inside layers", "one page", "one layer"])
+def test_cache_in_strided_pools(order, dtype, d):
+    """Keys and values of all layers in one pool, layers in front of or behind the pages, with room between them; what is not
+    the open pages' stays as it is. d = 3: 4 bytes at a time."""
+    gen = torch.Generator().manual_seed(len(order) + d)
+    B, W, page, Hk = 2, 3, 4, 2
+    layers = 1 if order == "one layer" else 3
+    lens = [6] * W + [11] * W
+    table, pages = ref.make_tables([x + 1 for x in lens], page, gen)
+    if order == "one page":
+        table, pages, lens = torch.zeros(B * W, 1, dtype=torch.int32), 1, [3] * (B * W)
+        table[1:] = -1
+    inside = order == "layers inside pages"
+    pool = rand(gen, *((pages, layers + 1) if inside else (layers, pages + 2)), 2, page, Hk, d, dtype=dtype)
+    view = lambda p: (p[:, :layers].transpose(0, 1) if inside else p[:, :pages]).unbind(2)  # noqa: E731
+    parent = some_parents(gen, B, W)
+    want, want_t = pool.clone(), table.clone()
+    wk, wv = view(want)
+    kc, vc = view(pool)
+    for i, j in enumerate(ref.moved(list(range(B * W)), parent, W)):
+        full, fill = divmod(lens[i], page)
+        want_t[i, :full] = table[j, :full]
+        mine, theirs = int(table[i, full]), int(table[j, full])
+        if mine >= 0 and theirs >= 0:
+            wk[:, mine, :fill], wv[:, mine, :fill] = kc[:, theirs, :fill], vc[:, theirs, :fill]
+    got = pool.cuda()
+    gk, gv = view(got)
+    gt = table.cuda()
+    la.beam_cache(gk, gv, gt, *up(ints(lens), parent), layered=True)
+    assert torch.equal(gt.cpu(), want_t) and torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("inside", [False, True])
+def test_states_in_strided_pools(inside):
+    gen = torch.Generator().manual_seed(3)
+    B, W, layers = 3, 5, 4
+    pool = rand(gen, *((B * W + 2, layers + 1) if inside else (layers, B * W + 2)), 6, 10)
+    view = lambda p: p[:, :layers].transpose(0, 1) if inside else p[:, :B * W]  # noqa: E731
+    parent = some_parents(gen, B, W)
+    want = pool.clone()
+    view(want)[:, :B * W] = view(pool)[:, ref.moved(list(range(B * W)), parent, W)]
+    got = pool.cuda()
+    la.beam_states(view(got), parent.cuda(), layered=True)
+    assert torch.equal(got.cpu(), want)
+
+
+def test_pools_that_overlap_are_refused():
+    one = torch.zeros(1, 8, 4, 2, 64, dtype=BF, device="cuda")
+    parent, lens = ints([[0, 0]]).cuda(), ints([1, 1]).cuda()
+    table = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        la.beam_states(one.expand(3, -1, -1, -1, -1), parent, layered=True)
+    with pytest.raises(ValueError, match="overlap"):
+        la.beam_cache(one.expand(3, -1, -1, -1, -1), one.expand(3, -1, -1, -1, -1), table, lens, parent, layered=True)
+    flat = torch.zeros(4096, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):  # layers closer than a page
+        la.beam_states(flat.as_strided((2, 4, 64), (32, 256, 1)), parent, layered=True)
+    with pytest.raises(ValueError, match="dense"):
+        la.beam_states(flat.as_strided((2, 4, 64), (1024, 256, 2)), parent, layered=True)
