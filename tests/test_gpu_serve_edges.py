@@ -7,7 +7,7 @@ import torch
 import gated_delta_rule_linear_gb300 as la
 import servelib as ref
 from layerlib import hold
-from test_gpu_serve import BF, F32, ints, rand, some_parents, up
+from test_gpu_serve import BF, F32, NAN, check_attn, ints, rand, some_parents, up
 
 pytestmark = pytest.mark.gpu
 
@@ -33,6 +33,57 @@ def test_attn_of_the_largest_tables(n, H, Hk, d, dtype, pages, length):
                           page * Hk * d, la.LA_F32 if dtype is F32 else 0, torch.cuda.current_stream().cuda_stream)
     assert rc == la.CONSTANTS["LA_OK"], la.la_last_error()
     assert torch.equal(o, torch.zeros_like(o)) and bool((lse == -ref.INF).all())
+
+
+@pytest.mark.parametrize("dtype,lens,H,Hk,d,page,window", [
+    # bfloat16, 9 to 16 heads a key head, and more, in blocks of 16
+    (BF, [0, 1, 64, 65, 700], 18, 2, 256, 16, 0), (BF, [513, 40, 3], 16, 1, 256, 20, 0), (BF, [2000], 24, 2, 256, 64, 1500),
+    (BF, [9000, 17], 17, 1, 256, 128, 0), (BF, [300, 70, 1], 10, 1, 64, 7, 33), (BF, [5000], 33, 1, 64, 64, 0),
+    (BF, [4000, 0, 12], 13, 1, 128, 16, 0),
+    # float32, 5 to 8 heads, and more, in blocks of 8
+    (F32, [0, 1, 16, 17, 700], 10, 2, 256, 16, 0), (F32, [513, 40, 3], 8, 1, 256, 20, 0), (F32, [2000], 12, 2, 256, 3, 1500),
+    (F32, [5000, 17], 9, 1, 256, 128, 0), (F32, [300, 70, 1], 7, 1, 64, 7, 33), (F32, [4000, 0, 12], 17, 1, 128, 16, 0),
+])
+def test_attn_of_blocks_of_heads(dtype, lens, H, Hk, d, page, window):
+    """Key heads with more queries than fill a small block: full and ragged blocks, whole parts and split ones."""
+    gen = torch.Generator().manual_seed(H + d)
+    table, pages = ref.make_tables(lens, page, gen)
+    q = rand(gen, len(lens), H, d, dtype=dtype)
+    kc, vc = (rand(gen, pages, page, Hk, d, dtype=dtype) for _ in range(2))
+    check_attn(q, kc, vc, table, lens, window)
+    check_attn(q, kc, vc, table, lens, window, max_len=max(lens))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,share", [(64, 12), (128, 12), (256, 12), (256, 6)])
+def test_attn_of_blocks_of_heads_leaves_out_what_is_not_there(dtype, d, share):
+    """NaN and infinity behind the length, in front of the window and in pages that nobody has."""
+    gen = torch.Generator().manual_seed(d + share)
+    lens, page, Hk, window = [50, 49, 0, 400, 64], 16, 2, 37
+    table, pages = ref.make_tables(lens, page, gen)
+    q = rand(gen, len(lens), Hk * share, d, dtype=dtype)
+    kc, vc = (rand(gen, pages, page, Hk, d, dtype=dtype) for _ in range(2))
+    used = torch.zeros(pages, page, dtype=torch.bool)
+    for s, L in enumerate(lens):
+        for p in range(max(L - window, 0), L):
+            used[int(table[s, p // page]), p % page] = True
+    kc[~used], vc[~used] = NAN, ref.INF
+    check_attn(q, kc, vc, table, lens, window)
+    check_attn(q, kc, vc, table, lens, window, max_len=400)
+
+
+@pytest.mark.parametrize("dtype,share,d,n,top", [(BF, 16, 256, 150, 90), (BF, 11, 64, 330, 90), (F32, 8, 256, 160, 60),
+                                                 (F32, 6, 128, 160, 100)])
+def test_attn_of_blocks_of_heads_of_many_short_sequences(dtype, share, d, n, top):
+    """Several parts for each CTA, of a unit or two, some of the sequences empty."""
+    gen = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, top + 1, (n,), generator=gen).tolist()
+    lens[0], lens[1], lens[-1] = 0, top, 0
+    table, pages = ref.make_tables(lens, 16, gen)
+    q = rand(gen, n, 4 * share, d, dtype=dtype)
+    kc, vc = (rand(gen, pages, 16, 4, d, dtype=dtype) for _ in range(2))
+    check_attn(q, kc, vc, table, lens)
+    check_attn(q, kc, vc, table, lens, max_len=top)
 
 
 # --------------------------------------------------------------- selection
