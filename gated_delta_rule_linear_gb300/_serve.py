@@ -79,6 +79,7 @@ def la_beam_cache(k_cache, v_cache, table, lens, parent, B, W, page_size, n_page
 # the general case (and the reasons of a refusal) to functions of their own.
 
 torch = None  # imported by the first call
+_INT = range(-(1 << 31), 1 << 31)  # what an int argument holds: ctypes would pass the low 32 bits of others
 
 
 def _setup():
@@ -228,6 +229,8 @@ def paged_attn(q, k_cache, v_cache, table, lens, scale=None, window=0, max_len=0
     if pages[3] != d:
         raise ValueError(f"caches must have q's {d} channels, got {pages[3]}")
     width, ld_table = _table(table, lens, n, idx)
+    if max_len not in _INT or window not in _INT:
+        raise ValueError(f"max_len and window must be below 2^31, got {max_len}, {window}")
     if o is not None:
         _check(o, "o", dt, (n, H, d), idx)
     flags = _FLAGS.get(dt)
@@ -265,6 +268,8 @@ def beam_select(logits, scores, K=None, done=None, eos=0, stream=None):
         if (V > 1 and sv != 1) or (W > 1 and B > 1 and sb != W * sw) or ld < V:
             raise ValueError("logits: a row must be dense, and rows at one stride")
     K = W if K is None else K
+    if K not in _INT or eos not in _INT:
+        raise ValueError(f"K and eos must be below 2^31, got {K}, {eos}")
     _check(scores, "scores", f32, (B, W), idx)
     if done is not None:
         _check(done, "done", t.bool if done.dtype is t.bool else t.uint8, (B, W), idx)

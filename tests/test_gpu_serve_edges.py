@@ -143,6 +143,26 @@ def test_select_sums_of_one_large_and_many_equal_logits(V, dtype):
     hold(best[:, 0], want, bound, "scores")
 
 
+def test_numbers_that_an_int_does_not_hold_are_refused():
+    """2^32 + 5 is not 5."""
+    far = 2 ** 32 + 5
+    logits, scores = torch.zeros(1, 2, 50, device="cuda"), torch.zeros(1, 2, device="cuda")
+    done = torch.ones(1, 2, dtype=torch.bool, device="cuda")
+    for kw in (dict(eos=far, done=done), dict(eos=5 - 2 ** 32, done=done), dict(K=far)):
+        with pytest.raises(ValueError, match="below 2"):
+            la.beam_select(logits, scores, **kw)
+    q, cache = torch.zeros(1, 2, 64, dtype=BF, device="cuda"), torch.zeros(2, 16, 1, 64, dtype=BF, device="cuda")
+    table, lens = ints([[0, 1]]).cuda(), ints([30]).cuda()
+    for kw in (dict(window=far), dict(max_len=far), dict(window=-(2 ** 40))):
+        with pytest.raises(ValueError, match="below 2"):
+            la.paged_attn(q, cache, cache, table, lens, **kw)
+    for kw in (dict(window=-1), dict(max_len=-1)):
+        with pytest.raises(la.LAError):
+            la.paged_attn(q, cache, cache, table, lens, **kw)
+    with pytest.raises(la.LAError):
+        la.beam_select(logits, scores, eos=50, done=done)
+
+
 # -------------------------------------------------------------- reordering
 
 @pytest.mark.parametrize("layers", [0, 1])
