@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const BeamSelect p, int 
 }
 
 __device__ __forceinline__ u64 ordered(double x) {
-  const long long b = __double_as_longlong(x);
+  const long long b = __double_as_longlong(x + 0.0);  // (one zero: scores of ended beams may be either)
   return static_cast<u64>(b ^ (b >> 63 & 0x7fffffffffffffffll)) ^ 0x8000000000000000ull;
 }
 __device__ __forceinline__ double unordered(u64 u) {

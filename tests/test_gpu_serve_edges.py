@@ -143,6 +143,22 @@ def test_select_sums_of_one_large_and_many_equal_logits(V, dtype):
     hold(best[:, 0], want, bound, "scores")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_select_of_both_zeros(dtype):
+    """Scores of +0 and -0 are equal, of ended beams and of beams with one token."""
+    zeros = torch.tensor([[-0.0, 0.0, -0.0, 0.0, 0.0, -0.0]])
+    one = torch.zeros(1, 6, 1, dtype=dtype)
+    one[0, ::2] = -0.0
+    done = torch.tensor([[True, False, True, False, True, True]])
+    for d in (torch.ones(1, 6, dtype=torch.bool), None, done):
+        for K in (1, 3, 6):
+            best, parent, token = la.beam_select(one.cuda(), zeros.cuda(), K, done=None if d is None else d.cuda())
+            assert parent.tolist() == [list(range(K))] and not bool(token.any()) and bool((best == 0).all())
+    logits = torch.full((1, 6, 300), -1.0, dtype=dtype)
+    best, parent, token = la.beam_select(logits.cuda(), zeros.cuda(), 6, done=torch.ones(1, 6, dtype=torch.bool).cuda(), eos=7)
+    assert parent.tolist() == [list(range(6))] and token.tolist() == [[7] * 6] and bool((best == 0).all())
+
+
 def test_numbers_that_an_int_does_not_hold_are_refused():
     """2^32 + 5 is not 5."""
     far = 2 ** 32 + 5
