@@ -471,8 +471,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect
     if (base[w] == INFINITY && at == 0) return {isfinite(scores[w]) ? ordered((double)scores[w]) : none, ~(first + p.eos)};
     if (base[w] == INFINITY) return {none, ~(first + at - (at <= p.eos))};
     if (isnan(base[w])) return {none, ~(first + at)};
-    // (not x - (top + log): a top near the type's limits would swallow the log)
-    const double x = (double)scores[w] + (((double)unordered(static_cast<unsigned>(k >> 32)) - tops[w]) - logs[w]);
+    // The log last: what is in front of it is exact, so that equal candidates of beams with the same sum stay equal.
+    // (And not x - (top + log): a top near the type's limits would swallow the log.)
+    const double x = ((double)scores[w] + ((double)unordered(static_cast<unsigned>(k >> 32)) - tops[w])) - logs[w];
     return {ordered(x), ~(first + ~static_cast<unsigned>(k))};
   };
   // As in a part: the K-th largest of the threads' bounds what can be among the K best, and so does that of a warp's. For few

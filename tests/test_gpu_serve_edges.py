@@ -159,6 +159,25 @@ def test_select_of_both_zeros(dtype):
     assert parent.tolist() == [list(range(6))] and token.tolist() == [[7] * 6] and bool((best == 0).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V,W,K", [(40, 6, 32), (60, 32, 32), (300, 12, 32), (3001, 8, 24)])
+def test_select_of_equal_candidates_of_other_scores(V, W, K, dtype):
+    """Beams with the same logits, multiples of 1/4, and whole scores: many candidates are equal, as a score more makes up for
+    four quarters of a logit. They come in the order of w*V + v, also where one logit has nearly all of the sum, whose log
+    has bits of any weight then."""
+    for seed in range(24):
+        gen = torch.Generator().manual_seed(seed)
+        row = -0.25 * torch.randint(0, 60, (V,), generator=gen).double()
+        if seed % 2:
+            row -= 5.0 + seed / 4
+            row[seed] = 0.0
+        scores = torch.randint(0, 30, (W,), generator=gen).double()
+        c = (scores[:, None] + row).flatten()  # without the log, which is one for all
+        at = torch.sort(-c, stable=True)[1][:K]
+        best, parent, token = la.beam_select(row.to(dtype).expand(1, W, V).contiguous().cuda(), scores[None].float().cuda(), K)
+        assert parent.cpu()[0].tolist() == (at // V).tolist() and token.cpu()[0].tolist() == (at % V).tolist()
+
+
 def test_numbers_that_an_int_does_not_hold_are_refused():
     """2^32 + 5 is not 5."""
     far = 2 ** 32 + 5
