@@ -394,7 +394,7 @@ __device__ __forceinline__ double log_of(float2 x) {
   const float s = num / den, s_lo = (fmaf(-s, den, num) + lo - s * den_lo) / den;
   const float z = s * s;
   const float tail = s * z * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 11, 1.f / 9), 1.f / 7), 1.f / 5), 1.f / 3);
-  // k ln 2 in two float32, the first with a product that is exact
+  // k ln 2 in two float32, the first with a product that is exact (the pair of Moshier's Cephes library)
   const float ln = k * 0.693359375f, ln_lo = fmaf(k, -2.12194440e-4f, 2.f * (s_lo + tail));
   return (double)ln + ((double)(2.f * s) + ln_lo);
 }

@@ -4,7 +4,9 @@
 //
 // Bound by reading keys and values once. The heads that share a key/value head
 // are the rows of one block of up to 8 or 16 (a `part` of a sequence), so that a
-// place is read once for all of them.
+// place is read once for all of a block. More heads than that (16, float32: 8) are
+// several blocks, and each reads the places again (32 x 8192, bfloat16, 32/1 heads
+// of 128: 48 us, 16/1 31).
 //
 // Work. The places of a part are cut into units, a block of keys for each of the
 // CTA's four warps; the units of all parts, one after the other, are dealt to the
@@ -26,11 +28,13 @@
 // low bfloat16 part; with up to 8 heads the low part is in the tile's other 8 rows
 // and costs nothing. float32: CUDA cores, see F32Warp.
 //
-// 64 sequences of 16384 places, 32/8 heads of 128, bfloat16: 611 us, 7.0 TB/s. Two
-// of 131072, 16/2 heads: 50 us of 40; what is not reading is the launch, the way
-// lengths -> table -> first keys (3.7 us) and the pieces' join (3 us). 16 heads a
-// block are bound by instructions (32/2 heads of 128: 5.0 TB/s; the low part of P
-// is a second product there), 8 heads in float32 too (3.8 to 5.8 TB/s).
+// 64 sequences of 16384 places, 32/8 heads of 128, bfloat16: 608 to 629 us, 6.8 to
+// 7.0 TB/s. Two of 131072, 16/2 heads: 50 us of 40; what is not reading is the
+// launch, the way lengths -> table -> first keys (3.7 us) and the pieces' join (3
+// us). 16 heads a block: 5.2 TB/s (32/2 heads of 128). Nothing is at its limit there
+// (issue 36 %, tensor pipe 21 %): two warps a scheduler do not cover a block's chain
+// of S, maximum and P V, whose low part is a second product. 8 heads in float32:
+// instructions, 4.6 to 5.8 TB/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>
