@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect
                                                                 const u64 *keys) {
   __shared__ double logs[kMaxBeams];  // of each beam's sum of exp(x - top)
   __shared__ float tops[kMaxBeams];
-  __shared__ float base[kMaxBeams];   // about score - log; NaN: its candidates have no value, infinity: it has ended
+  __shared__ float base[kMaxBeams];   // about score - log; NaN: its candidates have no value, infinity: it has ended, with a score
   __shared__ unsigned heads[kSelectThreads];
   __shared__ Candidate list[kList];
   __shared__ int passed[kList];
@@ -452,23 +452,23 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const BeamSelect
       const double log = value ? log_of(sum) : 0;
       logs[w] = log;
       tops[w] = top;
-      base[w] = done ? INFINITY : value ? score - static_cast<float>(log) : CUDART_NAN_F;
+      base[w] = done && isfinite(score) ? INFINITY : value ? score - static_cast<float>(log) : CUDART_NAN_F;
     }
   }
   if (tid == 0) passing = count = 0;
   __syncthreads();
   // Candidate at = j * K + r of beam w is the r-th of part j, with key k; an ended beam's first one is eos, its others and
-  // those of a beam without values the first tokens, without a value. Inside a part they fall.
+  // those of a beam without values (an ended one without a score too) the first tokens, without a value. Inside a part they fall.
   auto rough = [&](int w, int at, u64 k) -> float {  // its score, to float32; NaN: none
     const float c = base[w];
-    if (c == INFINITY) return at == 0 && isfinite(scores[w]) ? scores[w] : at < p.K && at < p.V ? -INFINITY : CUDART_NAN_F;
+    if (c == INFINITY) return at == 0 ? scores[w] : at < p.K && at < p.V ? -INFINITY : CUDART_NAN_F;
     if (isnan(c)) return at < p.K && at < p.V ? -INFINITY : CUDART_NAN_F;
     return k ? c + (unordered(static_cast<unsigned>(k >> 32)) - tops[w]) : CUDART_NAN_F;
   };
   auto candidate = [&](int w, int at, u64 k) -> Candidate {
     const u64 none = ordered(-(double)INFINITY);
     const unsigned first = static_cast<unsigned>(w * p.V);
-    if (base[w] == INFINITY && at == 0) return {isfinite(scores[w]) ? ordered((double)scores[w]) : none, ~(first + p.eos)};
+    if (base[w] == INFINITY && at == 0) return {ordered((double)scores[w]), ~(first + p.eos)};
     if (base[w] == INFINITY) return {none, ~(first + at - (at <= p.eos))};
     if (isnan(base[w])) return {none, ~(first + at)};
     // The log last: what is in front of it is exact, so that equal candidates of beams with the same sum stay equal.

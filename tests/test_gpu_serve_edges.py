@@ -178,6 +178,21 @@ def test_select_of_equal_candidates_of_other_scores(V, W, K, dtype):
         assert parent.cpu()[0].tolist() == (at // V).tolist() and token.cpu()[0].tolist() == (at % V).tolist()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_select_of_ended_beams_without_a_score(dtype):
+    """All their candidates are -infinity, eos like the others, and come in the order of the index; with the eos in front of,
+    among and behind the first K tokens."""
+    for V, K in ((349, 21), (5, 10), (9000, 32), (40, 1)):
+        logits = torch.zeros(4, 3, V, dtype=dtype)
+        scores = torch.tensor([[-ref.INF] * 3, [NAN, ref.INF, -ref.INF], [-ref.INF, -2.0, -ref.INF], [-1.0, NAN, -3.0]])
+        done = torch.tensor([[True] * 3, [True] * 3, [True] * 3, [True, True, False]])
+        for eos in (0, V // 2, V - 1):
+            want = ref.selection(ref.candidates(logits, scores, done, eos), K)
+            best, parent, token = la.beam_select(*up(logits, scores), K, done=done.cuda(), eos=eos)
+            assert torch.equal(parent.cpu(), want[1]) and torch.equal(token.cpu(), want[2])
+            assert torch.equal(best.cpu() == -ref.INF, want[0] == -ref.INF)
+
+
 def test_numbers_that_an_int_does_not_hold_are_refused():
     """2^32 + 5 is not 5."""
     far = 2 ** 32 + 5
